@@ -263,7 +263,7 @@ def _prepare_sparse(case, g):
                  sm_scale=1 / math.sqrt(192.0))
     if own:                       # the plan that a serving loop keeps for the layers of a step
         from paged_mla_decode_02_gb300 import mla
-        dec = mla.MLASparseDecoder(R, H, k, kf, kl)
+        dec = mla.MLASparseDecoder(R, H, N, k, kf, kl)
         dec.plan(kv_indptr.cpu(), state["kv_indices"], kv_len.cpu(), P, state["sm_scale"])
         state["decoder"] = dec
     return state
