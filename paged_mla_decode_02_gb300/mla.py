@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in ``include/mla_decode.h`` (ctypes).
+"""Python binding of the C ABI in ``include/mla_decode.h`` and
+``include/mla_paging.h`` (ctypes).
 
 Argument marshalling only: every step of the decode runs in the library's
 CUDA kernels.  PyTorch tensors supply device memory and the current stream;
@@ -34,7 +35,8 @@ EXPORTED = ("mla_plan_create", "mla_decode_plan", "mla_decode_run", "mla_decode_
             "mla_plan_check_status", "mla_plan_info", "mla_plan_destroy", "mla_status_string",
             "mla_plan_last_error", "mla_plan_partition_host", "mla_plan_set_profile_events",
             "mla_decode_noalloc", "mla_decode_plan_multi", "mla_merge_states",
-            "mla_absorb_q", "mla_project_out")
+            "mla_absorb_q", "mla_project_out", "mla_build_tables", "mla_rope_append",
+            "mla_summarize_pages", "mla_page_scores", "mla_select_pages")
 
 
 class MLAError(RuntimeError):
@@ -53,6 +55,12 @@ class PlanInfo(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class RopeSpec(ctypes.Structure):
+    """mla_rope_t (see mla_paging.h); made by ``rope_spec``."""
+    _fields_ = [("n_axes", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("axis_of_pair", ctypes.c_int32 * 32), ("inv_freq", ctypes.c_double * 32)]
 
 
 _lib = None
@@ -116,6 +124,21 @@ def bind_library(path: str) -> ctypes.CDLL:
     lib.mla_decode_noalloc.restype = c_int
     lib.mla_decode_noalloc.argtypes = [_I32P, _VP, _I32P, c_int, c_int, c_int, c_float, _VP, _VP,
                                        _VP, _VP, c_float, c_int, _VP, c_int, _VP, c_int, _VP]
+    c_i64 = ctypes.c_int64
+    lib.mla_build_tables.restype = c_int
+    lib.mla_build_tables.argtypes = [_VP, _VP, _VP, _VP, c_i64, c_int, _VP, _VP, _VP, c_int, c_int, c_int, _VP,
+                                     _VP, c_i64, _VP, _VP, _VP, c_i64, _VP, _VP]
+    lib.mla_rope_append.restype = c_int
+    lib.mla_rope_append.argtypes = [ctypes.POINTER(RopeSpec), _VP, c_i64, _VP, _VP, c_i64, c_i64, _VP, _VP, c_i64,
+                                    _VP, c_i64, _VP, c_float, _VP, _VP, c_int, c_float, c_int, c_int, c_i64, c_int,
+                                    c_int, _VP]
+    lib.mla_summarize_pages.restype = c_int
+    lib.mla_summarize_pages.argtypes = [_VP, c_i64, _VP, _VP, c_int, c_float, c_int, c_int, _VP, c_int, _VP]
+    lib.mla_page_scores.restype = c_int
+    lib.mla_page_scores.argtypes = [_VP, _VP, _VP, c_int, _VP, _VP, c_i64, c_int, c_int, _VP, c_i64, c_int, _VP]
+    lib.mla_select_pages.restype = c_int
+    lib.mla_select_pages.argtypes = [_VP, c_i64, _VP, _VP, c_i64, c_int, c_int, c_int, c_int, _VP, _VP, c_i64,
+                                     c_int, _VP]
     return lib
 
 
@@ -414,7 +437,224 @@ def mla_plan_partition_host(kv_indptr, kv_len, num_workers: int, tile_tokens: in
 
 
 # ---------------------------------------------------------------------------
-# Convenience wrapper
+# Around the decode (include/mla_paging.h)
+# ---------------------------------------------------------------------------
+
+def _on_device(dtype, contiguous: bool = True, **tensors) -> None:
+    """Each named tensor is on the current CUDA device, of ``dtype`` and (by
+    default) contiguous."""
+    import torch
+    device = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if not t.is_cuda or t.get_device() != device:
+            raise ValueError(f"{name} must be on the current CUDA device")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _row_stride(name: str, t, rows: int, cols=None) -> int:
+    """The row stride of a [rows, cols] tensor whose rows are runs of adjacent
+    entries (strides of dimensions of one entry or none say nothing)."""
+    if t.dim() != 2 or t.shape[0] != rows or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [{rows}, {'columns' if cols is None else cols}], got {tuple(t.shape)}")
+    width = t.shape[1]
+    if width > 1 and rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have adjacent entries in a row")
+    if rows < 2:
+        return width
+    if t.stride(0) < 0:
+        raise ValueError(f"{name} must not have a negative stride")
+    return t.stride(0)
+
+
+def _check_cache(ckv_cache, kpe_cache) -> int:
+    """The layout of a paged cache; returns its dtype code."""
+    code = _dtype_code(ckv_cache, "ckv_cache")
+    if code == DTYPE_FP32:
+        raise ValueError("ckv_cache must be bfloat16 or float8_e4m3fn")
+    _on_device(ckv_cache.dtype, ckv_cache=ckv_cache, kpe_cache=kpe_cache)
+    if ckv_cache.dim() != 3 or ckv_cache.shape[2] != 512:
+        raise ValueError(f"ckv_cache must be [num_pages, page_size, 512], got {tuple(ckv_cache.shape)}")
+    if kpe_cache.shape != (ckv_cache.shape[0], ckv_cache.shape[1], 64):
+        raise ValueError(f"kpe_cache must be [num_pages, page_size, 64] like ckv_cache, "
+                         f"got {tuple(kpe_cache.shape)}")
+    return code
+
+
+def mla_build_tables(kv_len, new_len, block_table, free_pages, free_count, page_size: int, kv_indptr, kv_indices,
+                     q_indptr, slots, positions, status, kv_len_out=None, free_count_out=None, stream=None) -> None:
+    """One step of the page tables on the device (see mla_paging.h): kv_len,
+    new_len [B]; block_table [B, max_pages] (rows may be strided); free_pages
+    [num_pages]; outputs kv_indptr, q_indptr [B + 1], kv_indices, slots
+    (int64), positions, status [1].  Without kv_len_out / free_count_out the
+    lengths and the count are updated in place."""
+    import torch
+    if kv_len_out is None:
+        kv_len_out = kv_len
+    if free_count_out is None:
+        free_count_out = free_count
+    _on_device(torch.int32, kv_len=kv_len, new_len=new_len, kv_len_out=kv_len_out, free_pages=free_pages,
+               free_count=free_count, free_count_out=free_count_out, kv_indptr=kv_indptr, kv_indices=kv_indices,
+               q_indptr=q_indptr, positions=positions, status=status)
+    _on_device(torch.int32, contiguous=False, block_table=block_table)
+    _on_device(torch.int64, slots=slots)
+    batch = kv_len.numel()
+    stride = _row_stride("block_table", block_table, batch)
+    if new_len.numel() != batch or kv_len_out.numel() != batch:
+        raise ValueError("kv_len, new_len and kv_len_out must have one entry per request")
+    if kv_indptr.numel() != batch + 1 or q_indptr.numel() != batch + 1:
+        raise ValueError("kv_indptr and q_indptr must have batch + 1 entries")
+    if positions.numel() != slots.numel():
+        raise ValueError("slots and positions must have the same length")
+    if free_count.numel() != 1 or free_count_out.numel() != 1 or status.numel() != 1:
+        raise ValueError("free_count, free_count_out and status must have one entry")
+    st = load_library().mla_build_tables(
+        kv_len.data_ptr(), new_len.data_ptr(), kv_len_out.data_ptr(), block_table.data_ptr(), stride,
+        block_table.shape[1], free_pages.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(),
+        free_pages.numel(), batch, int(page_size), kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(),
+        q_indptr.data_ptr(), slots.data_ptr(), positions.data_ptr(), slots.numel(), status.data_ptr(),
+        _stream_handle(stream))
+    _check(st, None, "mla_build_tables")
+
+
+def rope_spec(inv_freq, axis_of_pair=None, interleaved: bool = False, scale: float = 1.0) -> RopeSpec:
+    """The rotary embedding of the 64 rope dims: 32 inverse frequencies
+    (radians per position), for each pair the position axis it follows (all
+    the first by default), and the layout of a pair: dims (2i, 2i+1) if
+    interleaved, else (i, i+32).  ``scale`` multiplies cos and sin."""
+    freq = [float(f) for f in inv_freq]
+    axes = [0] * 32 if axis_of_pair is None else [int(a) for a in axis_of_pair]
+    if len(freq) != 32 or len(axes) != 32:
+        raise ValueError("inv_freq and axis_of_pair must have 32 entries")
+    spec = RopeSpec(max(axes) + 1, int(bool(interleaved)), float(scale))
+    spec.axis_of_pair[:] = axes
+    spec.inv_freq[:] = freq
+    return spec
+
+
+def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weight, eps: float, ckv_cache, kpe_cache,
+                    q_pe_out=None, kv_scale: float = 1.0, check_status: bool = False, stream=None):
+    """Rotate the queries and rope keys of a step's tokens, norm their latent
+    rows and write both into the cache at ``slots`` (see mla_paging.h).
+    positions int32 [n_axes, T] (or [T] for one axis; an expanded first
+    dimension is taken as it is), slots int64 [T], q_pe [T, H, 64] or None,
+    ckv [T, 512], kpe [T, 64] bf16 (rows may be strided), norm_weight bf16
+    [512] or None.  Returns (or fills) q_pe_out, contiguous."""
+    import torch
+    code = _check_cache(ckv_cache, kpe_cache)
+    if positions.dim() == 1:
+        positions = positions[None]
+    _on_device(torch.int32, contiguous=False, positions=positions)
+    _on_device(torch.int64, slots=slots)
+    _on_device(torch.bfloat16, contiguous=False, ckv=ckv, kpe=kpe)
+    T = slots.numel()
+    n_axes = rope.n_axes
+    if positions.dim() != 2 or positions.shape[0] < n_axes:
+        raise ValueError("positions must be [n_axes, tokens]")
+    axis_stride = _row_stride("positions", positions, positions.shape[0], T)
+    ckv_stride, kpe_stride = _row_stride("ckv", ckv, T, 512), _row_stride("kpe", kpe, T, 64)
+    if norm_weight is not None:
+        _on_device(torch.bfloat16, norm_weight=norm_weight)
+        if norm_weight.numel() != 512:
+            raise ValueError("norm_weight must have 512 entries")
+    H, q_ptr, q_t, q_h, out_ptr = 0, None, 0, 0, None
+    if q_pe is not None:
+        _on_device(torch.bfloat16, contiguous=False, q_pe=q_pe)
+        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != 64 or (q_pe.numel() and q_pe.stride(2) != 1):
+            raise ValueError("q_pe must be [tokens, heads, 64] with adjacent dims")
+        H = q_pe.shape[1]
+        q_t, q_h = q_pe.stride(0) if T > 1 else 0, q_pe.stride(1) if H > 1 else 0
+        if q_pe_out is None:
+            q_pe_out = torch.empty((T, H, 64), dtype=torch.bfloat16, device=q_pe.device)
+        else:
+            _on_device(torch.bfloat16, q_pe_out=q_pe_out)
+            if q_pe_out.shape != q_pe.shape:
+                raise ValueError("q_pe_out must have the shape of q_pe")
+        q_ptr, out_ptr = q_pe.data_ptr(), q_pe_out.data_ptr()
+    elif q_pe_out is not None:
+        raise ValueError("q_pe_out needs q_pe")
+    st = load_library().mla_rope_append(
+        ctypes.byref(rope), positions.data_ptr(), axis_stride, slots.data_ptr(), q_ptr,
+        q_t, q_h, out_ptr, ckv.data_ptr(), ckv_stride, kpe.data_ptr(), kpe_stride,
+        None if norm_weight is None else norm_weight.data_ptr(), eps, ckv_cache.data_ptr(), kpe_cache.data_ptr(),
+        code, kv_scale, ckv_cache.shape[0], ckv_cache.shape[1], T, H, int(bool(check_status)),
+        _stream_handle(stream))
+    _check(st, None, "mla_rope_append")
+    return q_pe_out
+
+
+def mla_summarize_pages(slots, ckv_cache, kpe_cache, summaries, kv_scale: float = 1.0, check_status: bool = False,
+                        stream=None) -> None:
+    """Mean rows of the pages that the tokens at ``slots`` completed, into
+    summaries bf16 [num_pages, 576] (see mla_paging.h)."""
+    import torch
+    code = _check_cache(ckv_cache, kpe_cache)
+    _on_device(torch.int64, slots=slots)
+    _on_device(torch.bfloat16, summaries=summaries)
+    if summaries.shape != (ckv_cache.shape[0], 576):
+        raise ValueError("summaries must be [num_pages, 576]")
+    st = load_library().mla_summarize_pages(slots.data_ptr(), slots.numel(), ckv_cache.data_ptr(),
+                                            kpe_cache.data_ptr(), code, kv_scale, ckv_cache.shape[0],
+                                            ckv_cache.shape[1], summaries.data_ptr(), int(bool(check_status)),
+                                            _stream_handle(stream))
+    _check(st, None, "mla_summarize_pages")
+
+
+def mla_page_scores(q_nope, q_pe, summaries, kv_indptr, kv_indices, scores, check_status: bool = False,
+                    stream=None) -> None:
+    """scores[r, p] = best score over the heads of row r of the p-th page of
+    its list (see mla_paging.h): q_nope bf16 [R, H, 512], q_pe bf16 [R, H, 64]
+    (or [R, tokens, heads, .]: one choice for all of a request's query tokens),
+    kv_indptr / kv_indices int32 device tensors, scores fp32 [R, >= longest
+    list] (rows may be strided)."""
+    import torch
+    _on_device(torch.bfloat16, q_nope=q_nope, q_pe=q_pe, summaries=summaries)
+    _on_device(torch.int32, kv_indptr=kv_indptr, kv_indices=kv_indices)
+    _on_device(torch.float32, contiguous=False, scores=scores)
+    rows = kv_indptr.numel() - 1
+    lead = q_nope.shape[:-1]
+    if len(lead) < 2 or lead[0] != rows or q_nope.shape[-1] != 512 or q_pe.shape != lead + (64,):
+        raise ValueError("q_nope must be [rows, ..., 512] and q_pe [rows, ..., 64], kv_indptr [rows + 1]")
+    if summaries.dim() != 2 or summaries.shape[1] != 576:
+        raise ValueError("summaries must be [num_pages, 576]")
+    stride = _row_stride("scores", scores, rows)
+    if stride < scores.shape[1]:
+        raise ValueError("scores must not overlap")
+    heads = lead[1] if len(lead) == 2 else lead[1] * lead[2]
+    st = load_library().mla_page_scores(q_nope.data_ptr(), q_pe.data_ptr(), summaries.data_ptr(),
+                                        summaries.shape[0], kv_indptr.data_ptr(), kv_indices.data_ptr(),
+                                        kv_indices.numel(), rows, heads, scores.data_ptr(), stride,
+                                        int(bool(check_status)), _stream_handle(stream))
+    _check(st, None, "mla_page_scores")
+
+
+def mla_select_pages(scores, kv_indptr, kv_indices, top_k: int, keep_first: int, keep_last: int, sel_indptr,
+                     sel_indices, check_status: bool = False, stream=None) -> None:
+    """The page lists of a sparse decode: of each row's pages the first
+    keep_first, the last keep_last and the best scoring others, min(top_k, n)
+    in all, in their order (see mla_paging.h)."""
+    import torch
+    _on_device(torch.int32, kv_indptr=kv_indptr, kv_indices=kv_indices, sel_indptr=sel_indptr,
+               sel_indices=sel_indices)
+    _on_device(torch.float32, contiguous=False, scores=scores)
+    rows = kv_indptr.numel() - 1
+    stride = _row_stride("scores", scores, rows)
+    if stride < scores.shape[1]:
+        raise ValueError("scores must not overlap")
+    if sel_indptr.numel() != rows + 1:
+        raise ValueError("sel_indptr must have rows + 1 entries")
+    st = load_library().mla_select_pages(scores.data_ptr(), stride, kv_indptr.data_ptr(),
+                                         kv_indices.data_ptr(), kv_indices.numel(), rows, int(top_k),
+                                         int(keep_first), int(keep_last), sel_indptr.data_ptr(),
+                                         sel_indices.data_ptr(), sel_indices.numel(), int(bool(check_status)),
+                                         _stream_handle(stream))
+    _check(st, None, "mla_select_pages")
+
+
+# ---------------------------------------------------------------------------
+# Convenience wrappers
 # ---------------------------------------------------------------------------
 
 class MLADecoder:
@@ -469,3 +709,107 @@ class MLADecoder:
             self.close()
         except Exception:
             pass
+
+
+class MLASparseDecoder:
+    """A decode that reads at most ``top_k`` pages of each request: the first
+    ``keep_first``, the last ``keep_last`` and those whose mean rows score best
+    against the query.  ``plan(...)`` once per batch layout, ``run(...)`` per
+    step or layer: mla_page_scores, mla_select_pages, then the decode over the
+    selected pages, all queued on the stream without synchronisation.
+
+    Holds lists of up to ``max_pages`` pages for each of ``max_batch`` requests.
+    A captured run replays after re-plans of at most the captured batch; like a
+    decode plan's graph it keeps the addresses it was captured with, that of
+    the page list included.
+
+    With q_len query tokens per request (q_len x heads <= 128, batch x q_len <=
+    max_batch) the choice is theirs together, and keep_last must cover the
+    pages that hold them."""
+
+    def __init__(self, max_batch: int, num_heads: int, max_pages: int, top_k: int, keep_first: int = 1,
+                 keep_last: int = 1, kernel="default"):
+        import torch
+        if top_k < 1 or keep_first < 0 or keep_last < 1 or keep_first + keep_last > top_k:
+            raise ValueError("top_k must cover keep_first >= 0 and keep_last >= 1 pages")
+        if max_pages < 1:
+            raise ValueError("max_pages must be >= 1")
+        self.decoder = MLADecoder(max_batch, num_heads, kernel)
+        self.max_batch, self.max_pages = int(max_batch), int(max_pages)
+        self.top_k, self.keep_first, self.keep_last = int(top_k), int(keep_first), int(keep_last)
+        dev = torch.device("cuda", torch.cuda.current_device())
+        self.sel_indices = torch.zeros(self.max_batch * self.top_k, dtype=torch.int32, device=dev)
+        self._sel_indptr = torch.zeros(self.max_batch + 1, dtype=torch.int32, device=dev)
+        self._kv_indptr = torch.zeros(self.max_batch + 1, dtype=torch.int32, device=dev)
+        self._scores = torch.empty((self.max_batch, self.max_pages), dtype=torch.float32, device=dev)
+        self._kv_indices = None
+        self.batch = 0
+
+    def plan(self, kv_indptr, kv_indices, kv_len, page_size: int, sm_scale: float, stream=None,
+             q_len: int = 0) -> None:
+        """Arguments as for ``MLADecoder.plan``: the whole page lists, of which
+        run() reads the selected pages."""
+        import torch
+        indptr, lens = _i32_host(kv_indptr), _i32_host(kv_len)
+        if lens.ndim != 1 or indptr.shape != (lens.shape[0] + 1,):
+            raise ValueError("kv_indptr must have batch + 1 entries")
+        if page_size not in (16, 32, 64):
+            raise MLAError(ERR_UNSUPPORTED, "page_size must be 16, 32 or 64")
+        batch = lens.shape[0]
+        pages = np.diff(indptr.astype(np.int64))
+        if indptr[0] != 0 or np.any(lens < 0) or np.any(pages != -(-lens.astype(np.int64) // page_size)):
+            raise ValueError("kv_indptr must count ceil(kv_len / page_size) pages for each request")
+        if batch > self.max_batch or np.any(pages > self.max_pages):
+            raise MLAError(ERR_CAPACITY, "the batch exceeds the decoder's max_batch or max_pages")
+        _on_device(torch.int32, kv_indices=kv_indices)
+        if kv_indices.numel() < indptr[-1]:
+            raise ValueError("kv_indices is shorter than kv_indptr says")
+        if q_len * self.decoder.num_heads > 128:
+            raise MLAError(ERR_UNSUPPORTED, "q_len x heads exceeds 128")
+        if q_len > 1 and (self.keep_last - 1) * page_size + 1 < q_len:
+            raise ValueError("keep_last must cover the pages of the q_len query tokens")
+        kept = np.minimum(pages, self.top_k)
+        sel_indptr = np.zeros(batch + 1, np.int32)
+        sel_indptr[1:] = np.cumsum(kept)
+        sel_len = (lens - (pages - kept) * page_size).astype(np.int32)
+        self.decoder.plan(sel_indptr, self.sel_indices, sel_len, page_size, sm_scale, stream=stream, q_len=q_len)
+        # rows past the batch get empty lists: a graph of a larger batch replays this plan
+        whole = np.full(self.max_batch + 1, indptr[-1], np.int32)
+        whole[:batch + 1] = indptr
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            self._kv_indptr.copy_(torch.from_numpy(whole))
+        self._kv_indices, self.batch = kv_indices, batch   # keep the borrowed page list alive
+
+    @property
+    def sel_indptr(self):
+        """Device offsets of each request's selected pages in ``sel_indices``, after a run."""
+        return self._sel_indptr[:self.batch + 1]
+
+    def run(self, q_nope, q_pe, ckv_cache, kpe_cache, summaries, out=None, lse=None, kv_scale: float = 1.0,
+            out_dtype=None, stream=None):
+        """One step: q_nope [B, H, 512] and q_pe [B, H, 64] (or [B, Q, H, .]),
+        the cache and its page summaries [num_pages, 576]; returns out, lse."""
+        if self._kv_indices is None:
+            raise MLAError(ERR_NOT_PLANNED, "MLASparseDecoder.run before plan")
+        n = self.batch
+        indptr, scores = self._kv_indptr[:n + 1], self._scores[:n]
+        mla_page_scores(q_nope, q_pe, summaries, indptr, self._kv_indices, scores, stream=stream)
+        mla_select_pages(scores, indptr, self._kv_indices, self.top_k, self.keep_first, self.keep_last,
+                         self.sel_indptr, self.sel_indices, stream=stream)
+        return self.decoder.run(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale, out_dtype, stream)
+
+    def check_status(self) -> int:
+        """Synchronise and raise on a device error of the choice or the decode."""
+        import torch
+        torch.cuda.synchronize()
+        # a call of no rows queues nothing and reports what the kernels recorded
+        _check(load_library().mla_page_scores(None, None, None, 1, None, None, 0, 0, 1, None, 0, 1,
+                                              _stream_handle(None)), None, "MLASparseDecoder")
+        return self.decoder.check_status()
+
+    def close(self) -> None:
+        self.decoder.close()
