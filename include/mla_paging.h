@@ -185,7 +185,8 @@ mla_status_t mla_summarize_pages(const int64_t* slots, int64_t tokens, const voi
  *              as they were
  * num_heads 1 .. 128; q_nope, q_pe and summaries 16-byte aligned.  A page id
  * outside [0, num_pages) scores -inf and is reported; a row whose list leaves
- * kv_indices or is longer than score_stride is reported and skipped.
+ * kv_indices or is longer than score_stride (or 2^30 pages) is reported and
+ * skipped.
  * rows <= 4096 (else MLA_ERR_CAPACITY).
  */
 mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, const void* summaries,

@@ -1,0 +1,64 @@
+// tcgen05 and TMA instructions issued by one elected lane of a converged warp.
+//
+// These instructions take their operands from uniform registers.  Where the
+// issuing lane is picked by a predicate or a branch on the thread index, the
+// operands are not known to be uniform and each MMA costs about 110 cycles to
+// issue, whatever its size (measured: M 128, K 16, N 16 to 128).  With the
+// lane elected inside the instruction's own block, in a warp whose index came
+// through a shuffle, it is 39 cycles for N = 16 and 64 for N = 128, the
+// tensor core's own time.
+#pragma once
+#include "tc_utils.cuh"
+
+namespace mla {
+namespace tc {
+
+// The index of this thread's warp, known to be the same in all of its lanes.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16.
+__device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One arrive on the mbarrier when every MMA issued so far has completed.
+__device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      "}\n" ::"r"(bar)
+      : "memory");
+}
+// Announce `bytes` on the mbarrier and load the box at {x, y}.
+__device__ __forceinline__ void tma_load_2d_elect(uint32_t dst, const void* tmap, int32_t x, int32_t y, uint32_t bar,
+                                                  uint32_t bytes) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%4], %5;\n"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];\n"
+      "}\n" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar), "r"(bytes)
+      : "memory");
+}
+
+}  // namespace tc
+}  // namespace mla

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "device_utils.cuh"
+#include "issue.cuh"
 #include "launch.h"
 #include "mla_internal.h"
 #include "mla_paging.h"
@@ -17,6 +18,7 @@ namespace mla {
 namespace {
 
 constexpr int kMaxRows = 4096;
+constexpr int64_t kMaxList = 1 << 30;   // pages of a list
 __device__ int32_t g_select_err;   // first device error of this file's kernels
 
 // Row r's page list: its first entry and length, or nothing (reported) when
@@ -41,14 +43,15 @@ __device__ __forceinline__ int list_of(const Lists& l, int r, int* first) {
 //
 // A row's scores are the row maxima of S = summaries[pages] . q^T, a product
 // of M = pages, N = heads, K = 576 that reads 1152 bytes per page: bound by
-// HBM.  The pages of all rows in a line (the page lists laid end to end) are
-// cut into one even run for each SM; a CTA takes its run in tiles of up to
-// 128 pages of one row.
-// - One warp copies, in nine chunks of 64 dims through a ring in shared
-//   memory, the pages' rows (tile::gather4, each lane the four pages it
-//   holds the ids of) and the row's queries (from L2: reading them again for
-//   every tile costs less than keeping 144 KB of them resident would leave
-//   for pages in flight).
+// HBM, and next by what passes from L2 to the SMs.  The pages of all rows in
+// a line (the page lists laid end to end) are cut into one even run for each
+// SM; a CTA takes its run in tiles of up to 128 pages of one row.
+// - One warp copies a row's queries into shared memory by TMA, in nine panels
+//   of 64 dims that stay for all tiles of the row (and make way one by one for
+//   the next row's).
+// - Four warps copy the pages' rows, a 64-dim chunk at a time, through a ring
+//   of panels with cp.async.  (As tile::gather4 copies the TMA took 90 cycles
+//   for four 128-byte rows, half the speed.)
 // - One thread issues the tcgen05 MMAs into one of two TMEM accumulators.
 // - Four warps read the other: a TMEM lane holds one page's products with
 //   all heads, so a thread takes its page's maximum without any exchange.
@@ -61,57 +64,80 @@ struct ScoreArgs {
   int64_t stride;
 };
 
-constexpr int kScoreThreads = 320;      // warp 0 queries, warp 1 MMAs, warps 2..5 maxima, 6..9 pages
-constexpr int kCopyWarps = 4;
-constexpr int kCopiesAhead = 4;         // chunks of pages a copying thread has in flight
+constexpr int kScoreThreads = 448;      // warp 0 queries, warp 1 MMAs, warps 2..5 maxima, 6..13 pages
+constexpr int kCopyWarps = 4;           // of each of two sets that take turns
 constexpr int kTilePages = 128;         // the MMA's M
-constexpr int kChunks = kD / 64;        // copies of 64 dims
-constexpr int kScoreStages = 6;
+constexpr int kChunks = kD / 64;        // panels of 64 dims
 constexpr int kPanelBytes = kTilePages * 128;
-constexpr int kStageBytes = 2 * kPanelBytes;   // pages, then queries (up to 128 heads)
 constexpr int kMinRun = 32;             // pages of a CTA's run, at least
-enum { kFull = 0, kEmpty = kScoreStages, kTFull = 2 * kScoreStages, kTEmpty = kTFull + 2, kFinal = kTEmpty + 2,
-       kNumBar };
+// Panels of the ring: with few heads a whole tile's, so that a short run
+// waits for memory once; with more, what the queries leave room for.
+constexpr int kFewHeads = 48, kStagesFew = kChunks, kStagesMany = 4;
+template <int kStages>
+struct ScoreBars {
+  enum { kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + kChunks, kTFull = kQEmpty + kChunks,
+         kTEmpty = kTFull + 2, kFinal = kTEmpty + 2, kCount };
+};
 
-__host__ __device__ constexpr int scores_smem(int rows) {
-  return kScoreStages * kStageBytes + 8 * kNumBar + 16 + 4 * (rows + 1) + 1024;
+template <int kStages>
+constexpr int scores_smem(int heads, int rows) {
+  return kStages * kPanelBytes + kChunks * ((heads + 15) / 16 * 16) * 128 + 8 * ScoreBars<kStages>::kCount + 16 +
+         4 * (rows + 1) + 1024;
 }
 
 struct Tile {
   int row, page0, pages;   // pages page0 .. page0 + pages - 1 of the row's list
+  bool enters, leaves;     // the first, the last tile of the row in this run
 };
 
+// 16 bytes into shared memory, the 256 around them into L2: the next chunk of
+// the row follows.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <int kStages>
 __global__ void __launch_bounds__(kScoreThreads, 1)
     scores_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qp,
                   const ScoreArgs a) {
   using namespace tc;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  using Bars = ScoreBars<kStages>;
+  constexpr int kCopiesAhead = kStages / 2 - 1;   // chunks of pages a copying thread leaves in flight
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const uint32_t base = smem_u32(sm);
-  const uint32_t bars = base + kScoreStages * kStageBytes;
+  const int heads16 = (a.heads + 15) & ~15;
+  const int q_panel = heads16 * 128;                     // bytes of a panel of queries
+  const int used = kStages * kPanelBytes + kChunks * q_panel;
+  const uint32_t base = smem_u32(sm), q_base = base + kStages * kPanelBytes;
+  const uint32_t bars = base + used;
   auto bar = [&](int i) { return bars + 8 * i; };
-  unsigned char* after = sm + kScoreStages * kStageBytes + 8 * kNumBar;
+  unsigned char* after = sm + used + 8 * Bars::kCount;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(after);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(after + 4);
   int* at = reinterpret_cast<int*>(after + 16);          // [rows + 1]: pages before each row
   __shared__ long long warp_sum[kScoreThreads / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < kNumBar; ++i)
-      mbar_init(bar(i), i < kEmpty ? 1 + kCopyWarps : i == kTEmpty || i == kTEmpty + 1 ? 4 : 1);
+  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
+  auto run_of = [](int64_t pages) {   // pages of a CTA's run
+    const int64_t even = (pages + gridDim.x - 1) / gridDim.x;
+    return even > kMinRun ? even : static_cast<int64_t>(kMinRun);
+  };
+  if (tid == 0) *abort_flag = 0;
+  if (tid < Bars::kCount) {
+    mbar_init(bar(tid), tid < Bars::kEmpty ? kCopyWarps : tid == Bars::kTEmpty || tid == Bars::kTEmpty + 1 ? 4 : 1);
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 2 * kMaxHeads);
+  // (what came before touches no memory of the previous kernel's)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // pages before each row, over the rows' lists as far as they are sound
   long long all;
   {
     const int per = (a.rows + kScoreThreads - 1) / kScoreThreads;
     long long sum = 0;
     int first;
+#pragma unroll 1
     for (int i = 0; i < per; ++i) {
       const int r = tid * per + i;
       if (r < a.rows) sum += list_of(a.lists, r, &first);
@@ -127,6 +153,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     __syncthreads();
     long long before = incl - sum;
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
+#pragma unroll 1
     for (int i = 0; i < per; ++i)
       if (tid * per + i < a.rows) at[tid * per + i + 1] += static_cast<int>(before);
     if (tid == 0) at[0] = 0;
@@ -141,10 +168,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   // this CTA's run of the line of pages
   const int total = all > INT32_MAX ? 0 : static_cast<int>(all);
-  const int even = (total + gridDim.x - 1) / gridDim.x;
-  const int run = even > kMinRun ? even : kMinRun;
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * run;
-  int pos = static_cast<int>(lo < total ? lo : total);
+  const int64_t run = run_of(total), lo = blockIdx.x * run;
+  const int begin = static_cast<int>(lo < total ? lo : total);
+  int pos = begin;
   const int end = static_cast<int>(lo + run < total ? lo + run : total);
   int row = 0;
   if (pos < end) {   // the row that holds page pos
@@ -158,100 +184,120 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   auto next = [&](Tile& t) {
     if (pos >= end) return false;
     while (at[row + 1] <= pos) ++row;
-    int n = at[row + 1] < end ? at[row + 1] - pos : end - pos;
-    n = n < kTilePages ? n : kTilePages;
-    t = {row, pos - at[row], n};
+    const int stop = at[row + 1] < end ? at[row + 1] : end;
+    const int n = stop - pos < kTilePages ? stop - pos : kTilePages;
+    t = {row, pos - at[row], n, pos == at[row] || pos == begin, pos + n == stop};
     pos += n;
     return true;
   };
-  const int heads16 = (a.heads + 15) & ~15;
   bool ok = true;
   Tile t;
 
   if (warp == 0) {
     // ---------------- queries ----------------
-    int st = 0;
-    while (ok && next(t)) {
-      for (int c = 0; c < kChunks; ++c, ++st) {
-        const int slot = st % kScoreStages;
-        if (!(ok = mbar_wait_warp(bar(kEmpty + slot), ((st / kScoreStages) & 1) ^ 1, abort_flag))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(kFull + slot), a.heads * 128);
-          tma_load_2d(base + slot * kStageBytes + kPanelBytes, c < kChunks - 1 ? &map_qn : &map_qp,
-                      c < kChunks - 1 ? 64 * c : 0, t.row * a.heads, bar(kFull + slot));
-        }
-        __syncwarp();
+    // (here and below, votes make the loops' conditions uniform to the compiler)
+    int n = 0, visit = 0;   // panels copied, rows entered
+    while (ok && __any_sync(~0u, next(t))) {
+      if (!__any_sync(~0u, t.enters)) continue;
+      const int y = t.row * a.heads, bytes = a.heads * 128;
+#pragma unroll 1
+      for (int c = 0; c < kChunks - 1; ++c, ++n) {
+        if (!(ok = mbar_wait_warp(bar(Bars::kQEmpty + c), (visit & 1) ^ 1, abort_flag))) break;
+        tma_load_2d_elect(q_base + c * q_panel, &map_qn, 64 * c, y, bar(Bars::kQFull + c), bytes);
       }
+      if (!ok || !(ok = mbar_wait_warp(bar(Bars::kQEmpty + kChunks - 1), (visit & 1) ^ 1, abort_flag))) break;
+      tma_load_2d_elect(q_base + (kChunks - 1) * q_panel, &map_qp, 0, y, bar(Bars::kQFull + kChunks - 1), bytes);
+      ++n;
+      ++visit;
     }
     if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
-    if (lane == 0)   // every copy issued has landed before the CTA leaves
-      for (int k = 1; k <= kScoreStages && k <= st; ++k)
-        mbar_wait_drain(bar(kFull + (st - k) % kScoreStages), ((st - k) / kScoreStages) & 1);
+    if (lane == 0) {   // every copy issued has landed before the CTA leaves
+#pragma unroll 1
+      for (int k = 1; k <= kChunks && k <= n; ++k)
+        mbar_wait_drain(bar(Bars::kQFull + (n - k) % kChunks), ((n - k) / kChunks) & 1);
+    }
     __syncwarp();
   } else if (warp >= 6) {
     // ---------------- pages ----------------
-    // thread i copies 16-byte column i % 8 of rows i / 8 + 16 j
-    const int i = tid - 6 * 32, col = i & 7, row0 = i >> 3;
+    // Two sets of four warps take turns, a chunk each.  Thread i of a set
+    // copies 16-byte column i % 8 of rows i / 8 + 16 j.
+    const int set = (warp - 6) / kCopyWarps, i = (tid - 6 * 32) % (32 * kCopyWarps), col = i & 7, row0 = i >> 3;
     const uint32_t dst = base + row0 * 128 + ((col ^ (row0 & 7)) << 4);
-    int st = 0, done = 0;
-    auto land = [&]() {   // the oldest chunk's copies of this warp are in place
+    auto row_of = [&](const Tile& x, int p) {   // page p of the tile (a wrong id reads page 0; scored -inf below)
+      const int id = a.lists.indices[a.lists.indptr[x.row] + x.page0 + (p < x.pages ? p : x.pages - 1)];
+      return a.summaries + static_cast<int64_t>(id < 0 || id >= a.num_pages ? 0 : id) * (2 * kD);
+    };
+    int turn = set, slot = set % kStages, phase = 1;        // the set's next chunk: its number, slot and phase
+    int landing = set % kStages, pending = 0, first = 0;    // first: number of the tile's first chunk
+    auto land = [&]() {   // the set's oldest chunk in flight is in place
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kFull + done % kScoreStages));
-      ++done;
+      if (lane == 0) mbar_arrive(bar(Bars::kFull + landing));
+      landing += 2;
+      if (landing >= kStages) landing -= kStages;
+      --pending;
     };
     while (ok && next(t)) {
-      const int32_t* ids = a.lists.indices + a.lists.indptr[t.row] + t.page0;
       const char* src[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int p = row0 + 16 * j;
-        int id = p < t.pages ? ids[p] : -1;
-        if (id < 0 || id >= a.num_pages) id = -1;   // not read; scored -inf below
-        src[j] = id < 0 ? nullptr : a.summaries + static_cast<int64_t>(id) * (2 * kD) + 16 * col;
-      }
-      for (int c = 0; c < kChunks; ++c, ++st) {
-        const int slot = st % kScoreStages;
-        if (!(ok = mbar_wait_warp(bar(kEmpty + slot), ((st / kScoreStages) & 1) ^ 1, abort_flag))) break;
+      for (int j = 0; j < 8; ++j) src[j] = row_of(t, row0 + 16 * j) + 16 * col + 128 * (turn - first);
+      const int rows16 = (t.pages + 15) >> 4;
+#pragma unroll 1
+      for (; turn < first + kChunks; turn += 2) {
+        if (!(ok = mbar_wait_warp(bar(Bars::kEmpty + slot), phase, abort_flag))) break;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (src[j]) cp_async_16(dst + slot * kStageBytes + j * 2048, src[j] + 128 * c, 16);
+        for (int j = 0; j < 8; ++j) {
+          if (j < rows16) copy16(dst + slot * kPanelBytes + j * 2048, src[j]);
+          src[j] += 256;
+        }
         cp_async_commit();
-        if (st - done >= kCopiesAhead) {
+        slot += 2;
+        if (slot >= kStages) {
+          slot -= kStages;
+          phase ^= 1;
+        }
+        if (++pending > kCopiesAhead) {
           cp_async_wait<kCopiesAhead>();
           land();
         }
       }
+      first += kChunks;
     }
     cp_async_wait<0>();
-    while (ok && done < st) land();
+    while (ok && pending > 0) land();
     if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
     const uint32_t idesc = idesc_bf16_f32(kTilePages, heads16, false, false);
-    int st = 0, n = 0;
-    for (; ok && next(t); ++n) {
+    int slot = 0, phase = 0, n = 0, visit = -1;   // visit: rows entered before this one
+    for (; ok && __any_sync(~0u, next(t)); ++n) {
       const int acc = n & 1;
-      if (!(ok = mbar_wait_warp(bar(kTEmpty + acc), ((n >> 1) & 1) ^ 1, abort_flag))) break;
-      tc_fence_after();
-      for (int c = 0; c < kChunks; ++c, ++st) {
-        const int slot = st % kScoreStages;
-        if (!(ok = mbar_wait_warp(bar(kFull + slot), (st / kScoreStages) & 1, abort_flag))) break;
+      const bool enters = __any_sync(~0u, t.enters), leaves = __any_sync(~0u, t.leaves);
+      visit += enters;
+      if (!(ok = mbar_wait_warp(bar(Bars::kTEmpty + acc), ((n >> 1) & 1) ^ 1, abort_flag))) break;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c) {
+        if (enters && !(ok = mbar_wait_warp(bar(Bars::kQFull + c), visit & 1, abort_flag))) break;
+        if (!(ok = mbar_wait_warp(bar(Bars::kFull + slot), phase, abort_flag))) break;
         tc_fence_after();
-        const uint32_t sa = base + slot * kStageBytes;
-        const uint64_t da = smem_desc(sa, 16, 1024, kSw128);
-        const uint64_t dq = smem_desc(sa + kPanelBytes, 16, 1024, kSw128);
+        const uint64_t da = smem_desc(base + slot * kPanelBytes, 16, 1024, kSw128);
+        const uint64_t dq = smem_desc(q_base + c * q_panel, 16, 1024, kSw128);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ss(tmem + acc * kMaxHeads, da + 2 * kk, dq + 2 * kk, idesc, (c | kk) != 0, lane == 0);
-        mma_commit(bar(kEmpty + slot), lane == 0);
+          mma_ss_elect(tmem + acc * kMaxHeads, da + 2 * kk, dq + 2 * kk, idesc, (c | kk) != 0);
+        mma_commit_elect(bar(Bars::kEmpty + slot));
+        if (leaves) mma_commit_elect(bar(Bars::kQEmpty + c));
+        if (++slot == kStages) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
       if (!ok) break;
-      mma_commit(bar(kTFull + acc), lane == 0);
+      mma_commit_elect(bar(Bars::kTFull + acc));
     }
     if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
-    mma_commit(bar(kFinal), lane == 0);   // every MMA issued completes before TMEM is freed
-    if (lane == 0) mbar_wait_drain(bar(kFinal), 0);
+    mma_commit_elect(bar(Bars::kFinal));   // every MMA issued completes before TMEM is freed
+    if (lane == 0) mbar_wait_drain(bar(Bars::kFinal), 0);
     __syncwarp();
   } else {
     // ---------------- maxima: page 32 quad + lane of the tile ----------------
@@ -260,7 +306,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int acc = n & 1, p = 32 * quad + lane;
       int id = -1;
       if (p < t.pages) id = a.lists.indices[a.lists.indptr[t.row] + t.page0 + p];
-      if (!(ok = mbar_wait_warp(bar(kTFull + acc), (n >> 1) & 1, abort_flag))) break;
+      if (!(ok = mbar_wait_warp(bar(Bars::kTFull + acc), (n >> 1) & 1, abort_flag))) break;
       tc_fence_after();
       float best = -INFINITY;
       if (32 * quad < t.pages) {
@@ -276,7 +322,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kTEmpty + acc));
+      if (lane == 0) mbar_arrive(bar(Bars::kTEmpty + acc));
       if (p < t.pages) {
         if (id < 0 || id >= a.num_pages) {
           report_error(&g_select_err, kErrBounds);
@@ -320,98 +366,187 @@ struct SelectArgs {
   int32_t* sel_indices;
 };
 
-constexpr int kSelThreads = 1024;
-
-// Scores as unsigned keys in the same order: NaN as -inf, -0 as 0.
+// Scores as unsigned keys in the same order: NaN as -inf, -0 as 0.  Never 0.
 __device__ __forceinline__ uint32_t key_of(float s) {
   if (s != s) s = -INFINITY;
   const uint32_t u = __float_as_uint(s + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ int block_sum(int v, int* sm) {
-  v = __reduce_add_sync(~0u, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return __reduce_add_sync(~0u, sm[threadIdx.x & 31]);
-}
-
-// Exclusive prefix sum over the block's threads; *total receives the sum.
-__device__ __forceinline__ int block_scan(int v, int* sm, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(~0u, incl, d);
-    if (lane >= d) incl += o;
-  }
-  __syncthreads();
-  if (lane == 31) sm[warp] = incl;
-  __syncthreads();
-  int w = sm[lane];
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(~0u, w, d);
-    if (lane >= d) w += o;
-  }
-  *total = __shfl_sync(~0u, w, 31);
-  const int before = __shfl_sync(~0u, w, warp ? warp - 1 : 0);
-  return (warp ? before : 0) + incl - v;
-}
-
-// One CTA per row.  The k-th highest key of the middle pages is found bit by
-// bit: the largest threshold with at least k keys at or above it.  Pages
-// above it are kept, and the first of those equal to it as far as k reaches.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+// One CTA per row.  Each warp holds a run of the row's pages, their keys in
+// registers (kKeys to a thread; 0: a longer row's keys are read again, from
+// L2, in each pass).  The want-th highest key of the middle pages is found by
+// digits of eight bits, from the first bit in which the keys differ down: a
+// histogram of the digit over the keys that agree with the digits found so
+// far, and the digit in which the want-th falls.  That ends when the keys of
+// that digit are all wanted, or with the last bit: then the first of the keys
+// equal to the threshold fill up.  The histograms' adds are to shared memory,
+// in integers, so their order does not show.  What bounds the kernel is
+// latency: three dependent reads of memory, and two barriers a pass.
+template <int kThreads, int kKeys>
+__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ int sm[32];
-  const int tid = threadIdx.x, r = blockIdx.x;
-  // the pages that the rows before this one keep
-  int before = 0, first;
-  for (int i = tid; i < r; i += kSelThreads) before += min(a.top_k, list_of(a.lists, i, &first));
-  before = block_sum(before, sm);
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int sums[kWarps], same_keys[kWarps], places[kWarps];
+  __shared__ uint32_t ors[kWarps], ands[kWarps];
+  __shared__ int hist[4][256], found[4][2];   // of each pass: the digit, and how many of its keys are wanted
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x;
+  const uint32_t below = (1u << lane) - 1;
+  int first;
   const int n = list_of(a.lists, r, &first);
-  const int keep = min(a.top_k, n);
-  if (tid == 0) {
-    if (r == 0) a.sel_indptr[0] = 0;
-    a.sel_indptr[r + 1] = before + keep;
-  }
   const float* s = a.scores + r * a.stride;
   const int32_t* pages = a.lists.indices + first;
+  const int lo = a.keep_first, hi = n - a.keep_last;   // the middle: [lo, hi)
+  const bool all = n <= a.top_k;
+
+  // this warp's run: `steps` times 32 pages from `base`
+  const int steps = (n + kThreads - 1) / kThreads;
+  const int base = warp * steps * 32 + lane;
+  auto key_at = [&](int e) {
+    const int p = base + 32 * e;
+    return !all && p >= lo && p < hi ? key_of(s[p]) : 0u;
+  };
+  uint32_t keys[kKeys > 0 ? kKeys : 1];
+  auto each = [&](auto&& f) {   // f(step, key) over the run, in order
+    if constexpr (kKeys > 0) {
+#pragma unroll
+      for (int e = 0; e < kKeys; ++e)
+        if (e < steps) f(e, keys[e]);
+    } else {
+      for (int e = 0; e < steps; e += 8) {   // eight reads in flight
+        uint32_t k[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) k[j] = e + j < steps ? key_at(e + j) : 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (e + j < steps) f(e + j, k[j]);
+      }
+    }
+  };
+  if constexpr (kKeys > 0) {
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) keys[e] = e < steps ? key_at(e) : 0u;
+  }
+  for (int i = tid; i < 4 * 256; i += kThreads) hist[0][i] = 0;
+  // what the rows before this one keep, and the bits in which keys differ
+  int before = 0, unused;
+  for (int i = tid; i < r; i += kThreads) before += min(a.top_k, list_of(a.lists, i, &unused));
+  uint32_t any = 0, every = ~0u;
+  each([&](int, uint32_t k) {
+    any |= k;
+    every &= k ? k : ~0u;
+  });
+  before = __reduce_add_sync(~0u, before);
+  any = __reduce_or_sync(~0u, any);
+  every = __reduce_and_sync(~0u, every);
+  if (lane == 0) {
+    sums[warp] = before;
+    ors[warp] = any;
+    ands[warp] = every;
+  }
+  __syncthreads();
+  before = __reduce_add_sync(~0u, lane < kWarps ? sums[lane] : 0);
+  if (tid == 0) {
+    if (r == 0) a.sel_indptr[0] = 0;
+    a.sel_indptr[r + 1] = before + min(a.top_k, n);
+  }
   int32_t* out = a.sel_indices + before;
-  if (n <= a.top_k) {
-    for (int p = tid; p < n; p += kSelThreads) out[p] = pages[p];
+  if (all) {
+    for (int p = tid; p < n; p += kThreads) out[p] = pages[p];
     return;
   }
-  const int lo = a.keep_first, hi = n - a.keep_last;
-  const int want = keep - a.keep_first - a.keep_last;
-  uint32_t cut = 0;
+  any = __reduce_or_sync(~0u, lane < kWarps ? ors[lane] : 0u);
+  every = __reduce_and_sync(~0u, lane < kWarps ? ands[lane] : ~0u);
+  const int want = a.top_k - a.keep_first - a.keep_last;
+
+  uint32_t cut = ~0u;   // above every key: none of the middle
+  int ties = 0;         // how many of the keys equal to the cut are kept; -1: all from the cut up
   if (want > 0) {
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t t = cut | 1u << bit;
-      int c = 0;
-      for (int p = lo + tid; p < hi; p += kSelThreads) c += key_of(s[p]) >= t;
-      if (block_sum(c, sm) >= want) cut = t;
+    int need = want, top = 31 - __clz(any ^ every);        // -1: all keys are equal
+    cut = top < 31 ? every >> (top + 1) << (top + 1) : 0u;
+    ties = 0;
+    for (int pass = 0; top >= 0; ++pass) {
+      const int shift = top > 7 ? top - 7 : 0;
+      const uint32_t agree = top < 31 ? ~0u << (top + 1) : 0u, digits = (2u << (top - shift)) - 1;
+      each([&](int, uint32_t k) {
+        if (k && ((k ^ cut) & agree) == 0) atomicAdd(&hist[pass][(k >> shift) & digits], 1);
+      });
+      __syncthreads();
+      if (warp == 0) {
+        // lane l holds the digits 8 (31 - l) .. + 7: the highest come first
+        const int* h = hist[pass] + 8 * (31 - lane);
+        int mine[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += mine[j] = h[j];
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(~0u, incl, d);
+          if (lane >= d) incl += o;
+        }
+        if (incl >= need && incl - sum < need) {           // one lane: the digit is among its own
+          int left = need - (incl - sum), digit = 0, last = 0;
+#pragma unroll
+          for (int j = 7; j >= 0; --j)
+            if (last == 0) {
+              if (mine[j] >= left) {
+                digit = 8 * (31 - lane) + j;
+                last = left == mine[j] ? -left : left;     // negative: all keys of the digit are wanted
+              } else {
+                left -= mine[j];
+              }
+            }
+          found[pass][0] = digit;
+          found[pass][1] = last;
+        }
+      }
+      __syncthreads();
+      cut |= static_cast<uint32_t>(found[pass][0]) << shift;
+      need = found[pass][1];
+      if (need < 0) {
+        ties = -1;
+        break;
+      }
+      top = shift - 1;
     }
-  } else {
-    cut = 0xffffffffu;
+    if (ties == 0) ties = need;
   }
-  int above = 0;
-  for (int p = lo + tid; p < hi; p += kSelThreads) above += key_of(s[p]) > cut;
-  int ties = want - block_sum(above, sm);   // how many of those equal to the cut are kept
-  int at = 0;
-  for (int p0 = 0; p0 < n; p0 += kSelThreads) {
-    const int p = p0 + tid;
-    const bool middle = p >= lo && p < hi;
-    const uint32_t k = middle ? key_of(s[p]) : 0;
-    int total;
-    const int tie = block_scan(middle && k == cut, sm, &total);
-    const bool kept = p < n && (!middle || k > cut || (k == cut && tie < ties));
-    ties -= total;
-    const int place = block_scan(kept, sm, &total);
-    if (kept) out[at + place] = pages[p];
-    at += total;
+
+  // equal keys before this warp's run
+  int tied = 0;
+  if (ties > 0) {
+    int c = 0;
+    each([&](int, uint32_t k) { c += k == cut; });
+    c = __reduce_add_sync(~0u, c);
+    if (lane == 0) same_keys[warp] = c;
+    __syncthreads();
+    tied = __reduce_add_sync(~0u, lane < warp ? same_keys[lane] : 0);
   }
+  // kept pages, a bit per step in `mine`, and how many before this warp's run
+  auto keeps = [&](int e, uint32_t k, int& tied_) {
+    const int p = base + 32 * e;
+    bool kept = p < lo || (p >= hi && p < n) || k > cut || (ties < 0 && k == cut);
+    if (ties > 0) {
+      const uint32_t same = __ballot_sync(~0u, k == cut);
+      kept |= k == cut && tied_ + __popc(same & below) < ties;
+      tied_ += __popc(same);
+    }
+    return kept;
+  };
+  int c = 0, tied1 = tied;
+  each([&](int e, uint32_t k) { c += keeps(e, k, tied1); });
+  c = __reduce_add_sync(~0u, c);
+  if (lane == 0) places[warp] = c;
+  __syncthreads();
+  int place = __reduce_add_sync(~0u, lane < warp ? places[lane] : 0);
+  if (c == 0) return;
+  each([&](int e, uint32_t k) {
+    const bool kept = keeps(e, k, tied);
+    const uint32_t who = __ballot_sync(~0u, kept);
+    if (kept) out[place + __popc(who & below)] = pages[base + 32 * e];
+    place += __popc(who);
+  });
 }
 
 }  // namespace
@@ -433,7 +568,7 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
   ScoreArgs a{};
   a.summaries = static_cast<const char*>(summaries);
   a.num_pages = num_pages;
-  a.lists = {kv_indptr, kv_indices, n_indices, score_stride};
+  a.lists = {kv_indptr, kv_indices, n_indices, score_stride < kMaxList ? score_stride : kMaxList};
   a.rows = rows;
   a.heads = num_heads;
   a.scores = scores;
@@ -448,13 +583,17 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
       return MLA_ERR_CUDA;
     int sms = 0;
     e = current_sms(&sms);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, scores_smem(kMaxRows));
+    const bool few = num_heads <= kFewHeads;
+    auto kernel = few ? scores_kernel<kStagesFew> : scores_kernel<kStagesMany>;
+    const int smem = few ? scores_smem<kStagesFew>(num_heads, rows) : scores_smem<kStagesMany>(num_heads, rows);
+    static_assert(scores_smem<kStagesFew>(kFewHeads, kMaxRows) <= 227 * 1024 - 128 &&
+                  scores_smem<kStagesMany>(kMaxHeads, kMaxRows) <= 227 * 1024 - 128, "shared memory of a CTA");
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     // no more CTAs than the lists have runs of the least length
     const int64_t runs = (n_indices + kMinRun - 1) / kMinRun;
     const int grid = static_cast<int>(runs < 1 ? 1 : runs < sms ? runs : sms);
     if (e == cudaSuccess)
-      e = launch_dependent(scores_kernel, grid, kScoreThreads, scores_smem(rows), 1, s, mn, mp, a);
+      e = launch_dependent(kernel, grid, kScoreThreads, smem, 1, s, mn, mp, a);
   }
   return finish_call(e, &g_select_err, check_status, s);
 }
@@ -475,7 +614,7 @@ extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stri
   SelectArgs a{};
   a.scores = scores;
   a.stride = score_stride;
-  a.lists = {kv_indptr, kv_indices, n_indices, score_stride};
+  a.lists = {kv_indptr, kv_indices, n_indices, score_stride < kMaxList ? score_stride : kMaxList};
   a.rows = rows;
   a.top_k = top_k;
   a.keep_first = keep_first;
@@ -483,7 +622,14 @@ extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stri
   a.sel_indptr = sel_indptr;
   a.sel_indices = sel_indices;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = rows > 0 ? launch_dependent(select_kernel, rows, kSelThreads, 0, 1, s, a)
-                           : cudaMemsetAsync(sel_indptr, 0, sizeof(int32_t), s);
+  cudaError_t e;
+  if (rows == 0)
+    e = cudaMemsetAsync(sel_indptr, 0, sizeof(int32_t), s);
+  else if (score_stride <= 4096)   // lists can be no longer than a row of scores
+    e = launch_dependent(select_kernel<256, 16>, rows, 256, 0, 1, s, a);
+  else if (score_stride <= 16384)
+    e = launch_dependent(select_kernel<1024, 16>, rows, 1024, 0, 1, s, a);
+  else
+    e = launch_dependent(select_kernel<1024, 0>, rows, 1024, 0, 1, s, a);
   return finish_call(e, &g_select_err, check_status, s);
 }

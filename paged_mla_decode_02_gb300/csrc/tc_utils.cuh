@@ -136,17 +136,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
       : "memory");
 }
 
-// Rows y[0..3] of a 2-D tensor map whose box is one row high, columns x ..
-// x + box_x of each, to four consecutive rows in shared memory (the swizzle
-// follows the destination address, as for a tiled load).
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int32_t x, const int (&y)[4], uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
-      : "memory");
-}
-
 // Prefetch the box at {x, y} of a tiled tensor map into L2 (no shared memory).
 __device__ __forceinline__ void tma_prefetch_l2_2d(const void* tmap, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap),

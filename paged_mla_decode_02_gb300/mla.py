@@ -171,8 +171,8 @@ def _ptr(t) -> int:
 
 def _stream_handle(stream) -> int:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the handle alone: a Stream object costs the host several times as much
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -440,13 +440,18 @@ def mla_plan_partition_host(kv_indptr, kv_len, num_workers: int, tile_tokens: in
 # Around the decode (include/mla_paging.h)
 # ---------------------------------------------------------------------------
 
-def _on_device(dtype, contiguous: bool = True, **tensors) -> None:
-    """Each named tensor is on the current CUDA device, of ``dtype`` and (by
-    default) contiguous."""
+def _on_device(dtype, names: str, *tensors, contiguous: bool = True) -> None:
+    """Each tensor (named in order in ``names``) is on the current CUDA device,
+    of ``dtype`` and (by default) contiguous."""
     import torch
     device = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if not t.is_cuda or t.get_device() != device:
+    for t in tensors:
+        if t.get_device() != device or t.dtype is not dtype or (contiguous and not t.is_contiguous()):
+            break
+    else:
+        return
+    for name, t in zip(names.split(), tensors):
+        if t.get_device() != device:
             raise ValueError(f"{name} must be on the current CUDA device")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -474,10 +479,11 @@ def _check_cache(ckv_cache, kpe_cache) -> int:
     code = _dtype_code(ckv_cache, "ckv_cache")
     if code == DTYPE_FP32:
         raise ValueError("ckv_cache must be bfloat16 or float8_e4m3fn")
-    _on_device(ckv_cache.dtype, ckv_cache=ckv_cache, kpe_cache=kpe_cache)
-    if ckv_cache.dim() != 3 or ckv_cache.shape[2] != 512:
-        raise ValueError(f"ckv_cache must be [num_pages, page_size, 512], got {tuple(ckv_cache.shape)}")
-    if kpe_cache.shape != (ckv_cache.shape[0], ckv_cache.shape[1], 64):
+    _on_device(ckv_cache.dtype, "ckv_cache kpe_cache", ckv_cache, kpe_cache)
+    shape = ckv_cache.shape
+    if len(shape) != 3 or shape[2] != 512:
+        raise ValueError(f"ckv_cache must be [num_pages, page_size, 512], got {tuple(shape)}")
+    if kpe_cache.shape != (shape[0], shape[1], 64):
         raise ValueError(f"kpe_cache must be [num_pages, page_size, 64] like ckv_cache, "
                          f"got {tuple(kpe_cache.shape)}")
     return code
@@ -495,11 +501,11 @@ def mla_build_tables(kv_len, new_len, block_table, free_pages, free_count, page_
         kv_len_out = kv_len
     if free_count_out is None:
         free_count_out = free_count
-    _on_device(torch.int32, kv_len=kv_len, new_len=new_len, kv_len_out=kv_len_out, free_pages=free_pages,
-               free_count=free_count, free_count_out=free_count_out, kv_indptr=kv_indptr, kv_indices=kv_indices,
-               q_indptr=q_indptr, positions=positions, status=status)
-    _on_device(torch.int32, contiguous=False, block_table=block_table)
-    _on_device(torch.int64, slots=slots)
+    _on_device(torch.int32, "kv_len new_len kv_len_out free_pages free_count free_count_out kv_indptr kv_indices "
+               "q_indptr positions status", kv_len, new_len, kv_len_out, free_pages, free_count, free_count_out,
+               kv_indptr, kv_indices, q_indptr, positions, status)
+    _on_device(torch.int32, "block_table", block_table, contiguous=False)
+    _on_device(torch.int64, "slots", slots)
     batch = kv_len.numel()
     stride = _row_stride("block_table", block_table, batch)
     if new_len.numel() != batch or kv_len_out.numel() != batch:
@@ -546,9 +552,9 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
     code = _check_cache(ckv_cache, kpe_cache)
     if positions.dim() == 1:
         positions = positions[None]
-    _on_device(torch.int32, contiguous=False, positions=positions)
-    _on_device(torch.int64, slots=slots)
-    _on_device(torch.bfloat16, contiguous=False, ckv=ckv, kpe=kpe)
+    _on_device(torch.int32, "positions", positions, contiguous=False)
+    _on_device(torch.int64, "slots", slots)
+    _on_device(torch.bfloat16, "ckv kpe", ckv, kpe, contiguous=False)
     T = slots.numel()
     n_axes = rope.n_axes
     if positions.dim() != 2 or positions.shape[0] < n_axes:
@@ -556,12 +562,12 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
     axis_stride = _row_stride("positions", positions, positions.shape[0], T)
     ckv_stride, kpe_stride = _row_stride("ckv", ckv, T, 512), _row_stride("kpe", kpe, T, 64)
     if norm_weight is not None:
-        _on_device(torch.bfloat16, norm_weight=norm_weight)
+        _on_device(torch.bfloat16, "norm_weight", norm_weight)
         if norm_weight.numel() != 512:
             raise ValueError("norm_weight must have 512 entries")
     H, q_ptr, q_t, q_h, out_ptr = 0, None, 0, 0, None
     if q_pe is not None:
-        _on_device(torch.bfloat16, contiguous=False, q_pe=q_pe)
+        _on_device(torch.bfloat16, "q_pe", q_pe, contiguous=False)
         if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != 64 or (q_pe.numel() and q_pe.stride(2) != 1):
             raise ValueError("q_pe must be [tokens, heads, 64] with adjacent dims")
         H = q_pe.shape[1]
@@ -569,7 +575,7 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
         if q_pe_out is None:
             q_pe_out = torch.empty((T, H, 64), dtype=torch.bfloat16, device=q_pe.device)
         else:
-            _on_device(torch.bfloat16, q_pe_out=q_pe_out)
+            _on_device(torch.bfloat16, "q_pe_out", q_pe_out)
             if q_pe_out.shape != q_pe.shape:
                 raise ValueError("q_pe_out must have the shape of q_pe")
         q_ptr, out_ptr = q_pe.data_ptr(), q_pe_out.data_ptr()
@@ -591,8 +597,8 @@ def mla_summarize_pages(slots, ckv_cache, kpe_cache, summaries, kv_scale: float 
     summaries bf16 [num_pages, 576] (see mla_paging.h)."""
     import torch
     code = _check_cache(ckv_cache, kpe_cache)
-    _on_device(torch.int64, slots=slots)
-    _on_device(torch.bfloat16, summaries=summaries)
+    _on_device(torch.int64, "slots", slots)
+    _on_device(torch.bfloat16, "summaries", summaries)
     if summaries.shape != (ckv_cache.shape[0], 576):
         raise ValueError("summaries must be [num_pages, 576]")
     st = load_library().mla_summarize_pages(slots.data_ptr(), slots.numel(), ckv_cache.data_ptr(),
@@ -610,9 +616,9 @@ def mla_page_scores(q_nope, q_pe, summaries, kv_indptr, kv_indices, scores, chec
     kv_indptr / kv_indices int32 device tensors, scores fp32 [R, >= longest
     list] (rows may be strided)."""
     import torch
-    _on_device(torch.bfloat16, q_nope=q_nope, q_pe=q_pe, summaries=summaries)
-    _on_device(torch.int32, kv_indptr=kv_indptr, kv_indices=kv_indices)
-    _on_device(torch.float32, contiguous=False, scores=scores)
+    _on_device(torch.bfloat16, "q_nope q_pe summaries", q_nope, q_pe, summaries)
+    _on_device(torch.int32, "kv_indptr kv_indices", kv_indptr, kv_indices)
+    _on_device(torch.float32, "scores", scores, contiguous=False)
     rows = kv_indptr.numel() - 1
     lead = q_nope.shape[:-1]
     if len(lead) < 2 or lead[0] != rows or q_nope.shape[-1] != 512 or q_pe.shape != lead + (64,):
@@ -636,9 +642,9 @@ def mla_select_pages(scores, kv_indptr, kv_indices, top_k: int, keep_first: int,
     keep_first, the last keep_last and the best scoring others, min(top_k, n)
     in all, in their order (see mla_paging.h)."""
     import torch
-    _on_device(torch.int32, kv_indptr=kv_indptr, kv_indices=kv_indices, sel_indptr=sel_indptr,
-               sel_indices=sel_indices)
-    _on_device(torch.float32, contiguous=False, scores=scores)
+    _on_device(torch.int32, "kv_indptr kv_indices sel_indptr sel_indices", kv_indptr, kv_indices, sel_indptr,
+               sel_indices)
+    _on_device(torch.float32, "scores", scores, contiguous=False)
     rows = kv_indptr.numel() - 1
     stride = _row_stride("scores", scores, rows)
     if stride < scores.shape[1]:
@@ -761,7 +767,7 @@ class MLASparseDecoder:
             raise ValueError("kv_indptr must count ceil(kv_len / page_size) pages for each request")
         if batch > self.max_batch or np.any(pages > self.max_pages):
             raise MLAError(ERR_CAPACITY, "the batch exceeds the decoder's max_batch or max_pages")
-        _on_device(torch.int32, kv_indices=kv_indices)
+        _on_device(torch.int32, "kv_indices", kv_indices)
         if kv_indices.numel() < indptr[-1]:
             raise ValueError("kv_indices is shorter than kv_indptr says")
         if q_len * self.decoder.num_heads > 128:
