@@ -28,7 +28,8 @@ __device__ int32_t g_append_err;   // first device error of this file's kernels
 constexpr int kPairs = kDKpe / 2;
 constexpr int kMaxAxes = 8;
 constexpr int kQThreads = 256;
-constexpr int kKvWarps = 8;
+constexpr int kKvWarps = kQThreads / 32;
+constexpr int kMostTokens = 32;     // tokens of a CTA's queries
 
 struct RopeDev {
   uint64_t turn[kPairs];     // f_i / 2 pi as a fraction of 2^64
@@ -56,7 +57,8 @@ struct AppendArgs {
   int64_t cache_slots;       // num_pages * page_size
   int64_t tokens;
   int heads;
-  int64_t q_blocks;
+  int tokens_per_block;      // of a CTA's queries
+  int64_t kv_blocks;
 };
 
 __device__ __forceinline__ float2 cos_sin(const AppendArgs& a, int pair, int64_t t) {
@@ -115,50 +117,118 @@ __device__ __forceinline__ void rotate(float (&lo)[8], float (&hi)[8], const flo
   }
 }
 
+// Two values of a cached row at element offset `at` (even).
+template <bool kFp8>
+__device__ __forceinline__ void store2(void* cache, int64_t at, float x, float y) {
+  if (kFp8)
+    *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(cache) + at) =
+        __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(cache) + at) = pack_bf16x2(x, y);
+}
+template <bool kFp8>
+__device__ __forceinline__ void store1(void* cache, int64_t at, float x) {
+  if (kFp8)
+    static_cast<uint8_t*>(cache)[at] = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+  else
+    static_cast<__nv_bfloat16*>(cache)[at] = __float2bfloat16_rn(x);
+}
+
+// The first CTAs take the keys, a warp per token; the others the queries of a
+// few tokens each.  A token's 32 angles are shared by all of its heads: a CTA
+// makes them once, into shared memory, while its first reads are under way,
+// and then is bound by reading and writing the rows (a thread turns a quarter
+// of a row, 32 bytes each way).
 template <bool kInterleaved, bool kFp8>
 __global__ void __launch_bounds__(kQThreads) append_kernel(const __grid_constant__ AppendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x < a.q_blocks) {
-    // queries: four threads per (token, head) row
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x;
-    const int part = static_cast<int>(i & 3);
-    const int64_t row = i >> 2, t = row / a.heads;
-    if (t >= a.tokens) return;
-    const int64_t slot = a.slots[t];
-    if (slot < 0 || slot >= a.cache_slots) return;
-    const __nv_bfloat16* src = a.q + t * a.q_token_stride + (row - t * a.heads) * a.q_head_stride + 8 * part;
-    float lo[8], hi[8];
-    unpack8(*reinterpret_cast<const uint4*>(src), lo);
-    unpack8(*reinterpret_cast<const uint4*>(src + 32), hi);
-    float2 cs[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x >= a.kv_blocks) {
+    // ---------------- queries ----------------
+    __shared__ float2 turns[kMostTokens][kPairs];
+    __shared__ bool real[kMostTokens];
+    const int64_t t0 = (blockIdx.x - a.kv_blocks) * a.tokens_per_block;
+    const int n = static_cast<int>(a.tokens - t0 < a.tokens_per_block ? a.tokens - t0 : a.tokens_per_block);
+    const int units = n * a.heads * 4, part = tid & 3;
+    auto place = [&](int u, int& t, int& h) {   // quarter u: of token t0 + t, head h
+      t = (u >> 2) / a.heads;
+      h = (u >> 2) - t * a.heads;
+    };
+    auto src = [&](int t, int h) {
+      return reinterpret_cast<const uint4*>(a.q + (t0 + t) * a.q_token_stride + h * a.q_head_stride + 8 * part);
+    };
+    constexpr int kAhead = 2;        // units read before they are turned
+    uint4 lo[kAhead], hi[kAhead];
+    auto read = [&](int u0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) cs[k] = cos_sin(a, pair_of<kInterleaved>(part, k), t);
-    rotate<kInterleaved>(lo, hi, cs);
-    __nv_bfloat16* dst = a.q_out + row * kDKpe + 8 * part;
-    *reinterpret_cast<uint4*>(dst) = pack8(lo);
-    *reinterpret_cast<uint4*>(dst + 32) = pack8(hi);
+      for (int k = 0; k < kAhead; ++k) {
+        const int u = u0 + k * kQThreads;
+        int t, h;
+        if (u < units) {
+          place(u, t, h);
+          lo[k] = src(t, h)[0];
+          hi[k] = src(t, h)[4];
+        }
+      }
+    };
+    read(tid);
+    for (int i = tid; i < n * kPairs; i += kQThreads) turns[i / kPairs][i % kPairs] = cos_sin(a, i % kPairs, t0 + i / kPairs);
+    if (tid < n) {
+      const int64_t slot = a.slots[t0 + tid];
+      real[tid] = slot >= 0 && slot < a.cache_slots;   // (one past the cache is reported with its key)
+    }
+    __syncthreads();
+    for (int u0 = tid; u0 < units; u0 += kAhead * kQThreads) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int u = u0 + k * kQThreads;
+        if (u >= units) break;
+        int t, h;
+        place(u, t, h);
+        float x[8], y[8];
+        unpack8(lo[k], x);
+        unpack8(hi[k], y);
+        float2 cs[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float4 two = *reinterpret_cast<const float4*>(&turns[t][pair_of<kInterleaved>(part, j)]);
+          cs[j] = make_float2(two.x, two.y);
+          cs[j + 1] = make_float2(two.z, two.w);
+        }
+        rotate<kInterleaved>(x, y, cs);
+        if (real[t]) {
+          uint4* dst = reinterpret_cast<uint4*>(a.q_out + ((t0 + t) * a.heads + h) * kDKpe + 8 * part);
+          dst[0] = pack8(x);
+          dst[4] = pack8(y);
+        }
+      }
+      read(u0 + kAhead * kQThreads);
+    }
     return;
   }
-  // keys: one warp per token
-  const int64_t t = (blockIdx.x - a.q_blocks) * kKvWarps + warp;
+  // ---------------- keys ----------------
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kKvWarps + warp;
   if (t >= a.tokens) return;
   const int64_t slot = a.slots[t];
+  const __nv_bfloat16* src = a.ckv + t * a.ckv_stride;
+  float x[2][8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) unpack8(*reinterpret_cast<const uint4*>(src + 256 * j + 8 * lane), x[j]);
+  const __nv_bfloat16* ks = a.kpe + t * a.kpe_stride;
+  const int e0 = kInterleaved ? 2 * lane : lane, e1 = kInterleaved ? e0 + 1 : lane + 32;   // this lane's pair
+  const float k0 = __bfloat162float(ks[e0]), k1 = __bfloat162float(ks[e1]);
+  const float2 cs = cos_sin(a, lane, t);
   if (slot < 0) return;
   if (slot >= a.cache_slots) {
     if (lane == 0) report_error(&g_append_err, kErrBounds);
     return;
   }
-  const __nv_bfloat16* src = a.ckv + t * a.ckv_stride;
-  float x[2][8];
   float sq = 0.f;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    unpack8(*reinterpret_cast<const uint4*>(src + 256 * j + 8 * lane), x[j]);
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) sq += x[j][k] * x[j][k];
-  }
 #pragma unroll
   for (int d = 16; d; d >>= 1) sq += __shfl_xor_sync(~0u, sq, d);
   const float r = a.weight ? rsqrtf(sq * (1.f / kDCkv) + a.eps) : 1.f;
@@ -176,30 +246,21 @@ __global__ void __launch_bounds__(kQThreads) append_kernel(const __grid_constant
     }
     store8<kFp8>(a.ckv_cache, slot * kDCkv + 256 * j + 8 * lane, x[j]);
   }
-  if (lane < 4) {
-    float lo[8], hi[8];
-    const __nv_bfloat16* ks = a.kpe + t * a.kpe_stride + 8 * lane;
-    unpack8(*reinterpret_cast<const uint4*>(ks), lo);
-    unpack8(*reinterpret_cast<const uint4*>(ks + 32), hi);
-    float2 cs[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      cs[k] = cos_sin(a, pair_of<kInterleaved>(lane, k), t);
-      if (kFp8) {
-        cs[k].x *= a.inv_scale;
-        cs[k].y *= a.inv_scale;
-      }
-    }
-    rotate<kInterleaved>(lo, hi, cs);
-    store8<kFp8>(a.kpe_cache, slot * kDKpe + 8 * lane, lo);
-    store8<kFp8>(a.kpe_cache, slot * kDKpe + 8 * lane + 32, hi);
+  const float c = cs.x * a.inv_scale, s = cs.y * a.inv_scale;
+  const float u = k0 * c - k1 * s, v = k0 * s + k1 * c;
+  if (kInterleaved) {
+    store2<kFp8>(a.kpe_cache, slot * kDKpe + e0, u, v);
+  } else {
+    store1<kFp8>(a.kpe_cache, slot * kDKpe + e0, u);
+    store1<kFp8>(a.kpe_cache, slot * kDKpe + e1, v);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Page summaries
 // ---------------------------------------------------------------------------
-constexpr int kSumThreads = 288;   // 72 eight-dim columns x 4 row groups
+constexpr int kSumThreads = 32 * (kD / 64);   // a warp for each 64 dims of a row
+constexpr int kSumBlocksPerSm = 7;            // CTAs of that size that fit an SM
 
 struct SummarizeArgs {
   const int64_t* slots;
@@ -210,6 +271,7 @@ struct SummarizeArgs {
   int64_t cache_slots;
   int page_shift;
   __nv_bfloat16* summaries;
+  int per_block;             // tokens a CTA looks at
 };
 
 template <bool kFp8>
@@ -228,38 +290,48 @@ __device__ __forceinline__ void load8(const void* cache, int64_t at, float (&x)[
   }
 }
 
+// A CTA looks at a run of tokens; for each that completes a page, warp w sums
+// dims 64 w .. 64 w + 63 of the page's rows, four rows to a load (8 lanes of
+// eight dims), and the four partial sums meet in the warp.  No barrier: the
+// warps of a CTA read the same rows at about the same time, and a page's reads
+// are all in flight at once.  Bound by HBM for long prompts.
 template <bool kFp8>
 __global__ void __launch_bounds__(kSumThreads) summarize_kernel(const SummarizeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int P = 1 << a.page_shift;
-  const int64_t slot = a.slots[blockIdx.x];
-  if (slot < 0) return;
-  if (slot >= a.cache_slots) {
-    if (threadIdx.x == 0) report_error(&g_append_err, kErrBounds);
-    return;
-  }
-  if ((slot & (P - 1)) != P - 1) return;
-  __shared__ float part[3][kD];
-  const int64_t first = slot - (P - 1);
-  const int group = threadIdx.x / 72, col = (threadIdx.x % 72) * 8;
-  float sum[8] = {};
-  for (int r = group; r < P; r += 4) {
-    float x[8];
-    if (col < kDCkv) load8<kFp8>(a.ckv, (first + r) * kDCkv + col, x);
-    else load8<kFp8>(a.kpe, (first + r) * kDKpe + col - kDCkv, x);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = 1 << a.page_shift, row0 = lane >> 3, col = 64 * warp + 8 * (lane & 7);
+  const bool pe = warp == kSumThreads / 32 - 1;
+  const int64_t t1 = min(a.tokens, (blockIdx.x + int64_t{1}) * a.per_block);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * a.per_block; t < t1; t += 32) {
+    const int64_t slot = t + lane < t1 ? a.slots[t + lane] : -1;
+    if (slot >= a.cache_slots) report_error(&g_append_err, kErrBounds);
+    uint32_t full = __ballot_sync(~0u, slot >= 0 && slot < a.cache_slots && (slot & (P - 1)) == P - 1);
+    for (; full; full &= full - 1) {
+      const int64_t page = __shfl_sync(~0u, slot, __ffs(full) - 1) >> a.page_shift;
+      float sum[8] = {};
+      for (int r0 = row0; r0 < P; r0 += 16) {   // P is a multiple of 16
+        float x[4][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[k] += x[k];
-  }
-  if (group) {
+        for (int k = 0; k < 4; ++k) {
+          const int64_t row = (page << a.page_shift) + r0 + 4 * k;
+          if (pe) load8<kFp8>(a.kpe, row * kDKpe + col - kDCkv, x[k]);
+          else load8<kFp8>(a.ckv, row * kDCkv + col, x[k]);
+        }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) part[group - 1][col + k] = sum[k];
-  }
-  __syncthreads();
-  if (group) return;
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sum[k] = (sum[k] + part[0][col + k] + part[1][col + k] + part[2][col + k]) * a.scale;
-  *reinterpret_cast<uint4*>(a.summaries + (slot >> a.page_shift) * kD + col) = pack8(sum);
+          for (int j = 0; j < 8; ++j) sum[j] += x[k][j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sum[j] += __shfl_xor_sync(~0u, sum[j], 8);
+        sum[j] += __shfl_xor_sync(~0u, sum[j], 16);
+        sum[j] *= a.scale;
+      }
+      if (row0 == 0) *reinterpret_cast<uint4*>(a.summaries + page * kD + col) = pack8(sum);
+    }
+  }
 }
 
 bool cache_args(const void* ckv_cache, const void* kpe_cache, int kv_dtype, float kv_scale, int num_pages,
@@ -328,10 +400,13 @@ extern "C" mla_status_t mla_rope_append(const mla_rope_t* rope, const int32_t* p
   a.cache_slots = static_cast<int64_t>(num_pages) * page_size;
   a.tokens = tokens;
   a.heads = num_heads > 0 ? num_heads : 1;
-  a.q_blocks = (tokens * num_heads * 4 + kQThreads - 1) / kQThreads;
+  // queries of 128 rows or more to a CTA (two quarters to a thread)
+  a.tokens_per_block = num_heads >= 128 || num_heads == 0 ? 1 : 128 / num_heads < kMostTokens ? 128 / num_heads : kMostTokens;
+  a.kv_blocks = (tokens + kKvWarps - 1) / kKvWarps;
   cudaError_t e = cudaSuccess;
   if (tokens > 0) {
-    const int grid = static_cast<int>(a.q_blocks + (tokens + kKvWarps - 1) / kKvWarps);
+    const int64_t q_blocks = num_heads > 0 ? (tokens + a.tokens_per_block - 1) / a.tokens_per_block : 0;
+    const int grid = static_cast<int>(a.kv_blocks + q_blocks);
     auto kernel = rope->interleaved ? (fp8 ? append_kernel<true, true> : append_kernel<true, false>)
                                     : (fp8 ? append_kernel<false, true> : append_kernel<false, false>);
     e = launch_dependent(kernel, grid, kQThreads, 0, 1, s, a);
@@ -356,9 +431,14 @@ extern "C" mla_status_t mla_summarize_pages(const int64_t* slots, int64_t tokens
   a.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
   a.summaries = static_cast<__nv_bfloat16*>(summaries);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int sms = 0;
   cudaError_t e = cudaSuccess;
-  if (tokens > 0)
+  if (tokens > 0 && (e = current_sms(&sms)) == cudaSuccess) {
+    // as many CTAs as are resident at once, as long as there are tokens for them
+    const int64_t blocks = static_cast<int64_t>(sms) * kSumBlocksPerSm;
+    a.per_block = static_cast<int>((tokens + blocks - 1) / blocks);
     e = launch_dependent(kv_dtype == MLA_DTYPE_FP8_E4M3 ? summarize_kernel<true> : summarize_kernel<false>,
-                         static_cast<int>(tokens), kSumThreads, 0, 1, s, a);
+                         static_cast<int>((tokens + a.per_block - 1) / a.per_block), kSumThreads, 0, 1, s, a);
+  }
   return finish_call(e, &g_append_err, check_status, s);
 }
