@@ -373,26 +373,38 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One CTA per row.  Each warp holds a run of the row's pages, their keys in
-// registers (kKeys to a thread; 0: a longer row's keys are read again, from
-// L2, in each pass).  The want-th highest key of the middle pages is found by
-// digits of eight bits, from the first bit in which the keys differ down: a
-// histogram of the digit over the keys that agree with the digits found so
-// far, and the digit in which the want-th falls.  That ends when the keys of
-// that digit are all wanted, or with the last bit: then the first of the keys
-// equal to the threshold fill up.  The histograms' adds are to shared memory,
-// in integers, so their order does not show.  What bounds the kernel is
-// latency: three dependent reads of memory, and two barriers a pass.
-template <int kThreads, int kKeys>
+// One CTA per row.  The middle pages are ordered by key, then by position:
+// the composite of a page is its key above its distance from the row's end, so
+// no two are equal and the want-th highest composite, the cut, parts kept from
+// left.  It is found by digits of eight bits, from the first bit in which the
+// keys differ down: a histogram of the digit over the pages that agree with
+// the digits found so far (in shared memory, in integers: their order does not
+// show), and the digit in which the want-th falls.  That ends when all pages
+// of the digit are wanted, or when few are left, which are then ranked against
+// each other.  Each warp holds a run of the row's pages in order, so counts
+// of the warps before it place what it keeps.
+// The keys stay in shared memory (kStaged) or, for longer rows, are read again
+// from L2 in each pass.  What bounds the kernel is latency -- three dependent
+// reads of memory, two barriers a pass -- and its code: loops stay rolled, as
+// most of their lines run once or twice.
+// Rows of scores up to this long take a CTA of 256 threads, longer ones of 1024
+// (256 rows of 1024 pages: 5.5 us against 6.6; 64 rows of 2048: 6.8 against 5.5).
+constexpr int64_t kNarrow = 1024;
+constexpr int kFewLeft = 128;            // pages ranked against each other
+constexpr int kStagedPages = 49152;      // keys that fit a CTA's shared memory
+
+template <int kThreads, bool kStaged>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int kWarps = kThreads / 32;
-  __shared__ int sums[kWarps], same_keys[kWarps], places[kWarps];
+  constexpr int kWarps = kThreads / 32, kUnroll = kStaged ? 2 : 8;
+  extern __shared__ uint32_t staged[];
+  __shared__ int sums[kWarps], places[kWarps], hist[2][256], digit_of, need_of, left_of, few;
   __shared__ uint32_t ors[kWarps], ands[kWarps];
-  __shared__ int hist[4][256], found[4][2];   // of each pass: the digit, and how many of its keys are wanted
+  __shared__ unsigned long long rest[kFewLeft], cut_of;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x;
-  const uint32_t below = (1u << lane) - 1;
+  for (int i = tid; i < 512; i += kThreads) hist[0][i] = 0;
+  if (tid == 0) few = 0;
   int first;
   const int n = list_of(a.lists, r, &first);
   const float* s = a.scores + r * a.stride;
@@ -400,43 +412,25 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   const int lo = a.keep_first, hi = n - a.keep_last;   // the middle: [lo, hi)
   const bool all = n <= a.top_k;
 
-  // this warp's run: `steps` times 32 pages from `base`
+  // this warp's run: `steps` times 32 pages from `base`; keys of the middle
+  // pages, 0 for the others
   const int steps = (n + kThreads - 1) / kThreads;
   const int base = warp * steps * 32 + lane;
-  auto key_at = [&](int e) {
-    const int p = base + 32 * e;
-    return !all && p >= lo && p < hi ? key_of(s[p]) : 0u;
-  };
-  uint32_t keys[kKeys > 0 ? kKeys : 1];
-  auto each = [&](auto&& f) {   // f(step, key) over the run, in order
-    if constexpr (kKeys > 0) {
-#pragma unroll
-      for (int e = 0; e < kKeys; ++e)
-        if (e < steps) f(e, keys[e]);
-    } else {
-      for (int e = 0; e < steps; e += 8) {   // eight reads in flight
-        uint32_t k[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) k[j] = e + j < steps ? key_at(e + j) : 0u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (e + j < steps) f(e + j, k[j]);
-      }
+  auto read_key = [&](int p) { return p >= lo && p < hi ? key_of(s[p]) : 0u; };
+  auto key_at = [&](int p) { return kStaged ? staged[p] : read_key(p); };
+  uint32_t any = 0, every = ~0u;
+  if (!all) {
+#pragma unroll 8
+    for (int e = 0; e < steps; ++e) {
+      const uint32_t k = read_key(base + 32 * e);
+      if (kStaged) staged[base + 32 * e] = k;
+      any |= k;
+      every &= k ? k : ~0u;
     }
-  };
-  if constexpr (kKeys > 0) {
-#pragma unroll
-    for (int e = 0; e < kKeys; ++e) keys[e] = e < steps ? key_at(e) : 0u;
   }
-  for (int i = tid; i < 4 * 256; i += kThreads) hist[0][i] = 0;
   // what the rows before this one keep, and the bits in which keys differ
   int before = 0, unused;
   for (int i = tid; i < r; i += kThreads) before += min(a.top_k, list_of(a.lists, i, &unused));
-  uint32_t any = 0, every = ~0u;
-  each([&](int, uint32_t k) {
-    any |= k;
-    every &= k ? k : ~0u;
-  });
   before = __reduce_add_sync(~0u, before);
   any = __reduce_or_sync(~0u, any);
   every = __reduce_and_sync(~0u, every);
@@ -458,95 +452,104 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   }
   any = __reduce_or_sync(~0u, lane < kWarps ? ors[lane] : 0u);
   every = __reduce_and_sync(~0u, lane < kWarps ? ands[lane] : ~0u);
-  const int want = a.top_k - a.keep_first - a.keep_last;
 
-  uint32_t cut = ~0u;   // above every key: none of the middle
-  int ties = 0;         // how many of the keys equal to the cut are kept; -1: all from the cut up
-  if (want > 0) {
-    int need = want, top = 31 - __clz(any ^ every);        // -1: all keys are equal
-    cut = top < 31 ? every >> (top + 1) << (top + 1) : 0u;
-    ties = 0;
-    for (int pass = 0; top >= 0; ++pass) {
-      const int shift = top > 7 ? top - 7 : 0;
-      const uint32_t agree = top < 31 ? ~0u << (top + 1) : 0u, digits = (2u << (top - shift)) - 1;
-      each([&](int, uint32_t k) {
-        if (k && ((k ^ cut) & agree) == 0) atomicAdd(&hist[pass][(k >> shift) & digits], 1);
-      });
+  auto composite = [&](uint32_t k, int p) {
+    return static_cast<unsigned long long>(k) << 32 | static_cast<uint32_t>(n - 1 - p);
+  };
+  unsigned long long cut = ~0ull;   // above every composite: none of the middle
+  int need = a.top_k - a.keep_first - a.keep_last;
+  if (need > 0) {
+    const int tail = 31 - __clz(n);                         // the highest bit of a distance, or above it
+    int top = any != every ? 63 - __clz(any ^ every) : tail;
+    cut = composite(every, n - 1);                          // with what the keys have in common alone
+    if (any != every) cut = top == 63 ? 0 : cut >> (top + 1) << (top + 1);
+    for (int side = 0;; side ^= 1) {
+      const int shift = max(top - 7, top >= 32 ? 32 : 0);   // a digit lies within the key or the distance
+      const uint32_t digits = (2u << (top - shift)) - 1;
+#pragma unroll kUnroll
+      for (int e = 0; e < steps; ++e) {
+        const int p = base + 32 * e;
+        const uint32_t k = key_at(p);
+        const unsigned long long c = composite(k, p);
+        if (k && ((c ^ cut) >> top) < 2) atomicAdd(&hist[side][static_cast<uint32_t>(c >> shift) & digits], 1);
+      }
       __syncthreads();
       if (warp == 0) {
         // lane l holds the digits 8 (31 - l) .. + 7: the highest come first
-        const int* h = hist[pass] + 8 * (31 - lane);
-        int mine[8], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += mine[j] = h[j];
+        const int4* h = reinterpret_cast<const int4*>(hist[side] + 8 * (31 - lane));
+        const int4 u = h[0], v = h[1];
+        const int sum = u.x + u.y + u.z + u.w + v.x + v.y + v.z + v.w;
         int incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int o = __shfl_up_sync(~0u, incl, d);
           if (lane >= d) incl += o;
         }
-        if (incl >= need && incl - sum < need) {           // one lane: the digit is among its own
-          int left = need - (incl - sum), digit = 0, last = 0;
+        // the lane that the need-th falls to, and its digits one to a lane
+        const uint32_t reach = __ballot_sync(~0u, incl >= need);
+        const int owner = __ffs(reach) - 1, above = __shfl_sync(~0u, incl - sum, owner);
+        const int digit = 8 * (31 - owner) + 7 - (lane & 7), mine = hist[side][digit];
+        incl = mine;
 #pragma unroll
-          for (int j = 7; j >= 0; --j)
-            if (last == 0) {
-              if (mine[j] >= left) {
-                digit = 8 * (31 - lane) + j;
-                last = left == mine[j] ? -left : left;     // negative: all keys of the digit are wanted
-              } else {
-                left -= mine[j];
-              }
-            }
-          found[pass][0] = digit;
-          found[pass][1] = last;
+        for (int d = 1; d < 8; d <<= 1) {
+          const int o = __shfl_up_sync(~0u, incl, d);
+          if ((lane & 7) >= d) incl += o;
         }
+        incl += above;
+        if (lane < 8 && incl >= need && incl - mine < need) {
+          digit_of = digit;
+          need_of = need - (incl - mine);
+          left_of = mine;
+        }
+      } else {
+        for (int i = tid - 32; i < 256; i += kThreads - 32) hist[side ^ 1][i] = 0;
       }
       __syncthreads();
-      cut |= static_cast<uint32_t>(found[pass][0]) << shift;
-      need = found[pass][1];
-      if (need < 0) {
-        ties = -1;
+      cut |= static_cast<unsigned long long>(digit_of) << shift;
+      need = need_of;
+      if (need == left_of) break;                           // all from the cut up
+      top = shift == 32 ? tail : shift - 1;
+      if (left_of <= kFewLeft) {
+        const int stays = shift;
+#pragma unroll kUnroll
+        for (int e = 0; e < steps; ++e) {
+          const int p = base + 32 * e;
+          const uint32_t k = key_at(p);
+          const unsigned long long c = composite(k, p);
+          if (k && (c ^ cut) >> stays == 0) rest[atomicAdd(&few, 1)] = c;
+        }
+        __syncthreads();
+        if (tid < few) {
+          const unsigned long long mine = rest[tid];
+          int rank = 0;
+          for (int j = 0; j < few; ++j) rank += rest[j] > mine;
+          if (rank == need - 1) cut_of = mine;
+        }
+        __syncthreads();
+        cut = cut_of;
         break;
       }
-      top = shift - 1;
     }
-    if (ties == 0) ties = need;
   }
 
-  // equal keys before this warp's run
-  int tied = 0;
-  if (ties > 0) {
-    int c = 0;
-    each([&](int, uint32_t k) { c += k == cut; });
-    c = __reduce_add_sync(~0u, c);
-    if (lane == 0) same_keys[warp] = c;
-    __syncthreads();
-    tied = __reduce_add_sync(~0u, lane < warp ? same_keys[lane] : 0);
-  }
-  // kept pages, a bit per step in `mine`, and how many before this warp's run
-  auto keeps = [&](int e, uint32_t k, int& tied_) {
-    const int p = base + 32 * e;
-    bool kept = p < lo || (p >= hi && p < n) || k > cut || (ties < 0 && k == cut);
-    if (ties > 0) {
-      const uint32_t same = __ballot_sync(~0u, k == cut);
-      kept |= k == cut && tied_ + __popc(same & below) < ties;
-      tied_ += __popc(same);
-    }
-    return kept;
-  };
-  int c = 0, tied1 = tied;
-  each([&](int e, uint32_t k) { c += keeps(e, k, tied1); });
+  // kept pages of this warp's run, and of the warps before it
+  auto keeps = [&](int p) { return p < lo || (p >= hi && p < n) || (p < hi && composite(key_at(p), p) >= cut); };
+  int c = 0;
+#pragma unroll kUnroll
+  for (int e = 0; e < steps; ++e) c += keeps(base + 32 * e);
   c = __reduce_add_sync(~0u, c);
   if (lane == 0) places[warp] = c;
   __syncthreads();
   int place = __reduce_add_sync(~0u, lane < warp ? places[lane] : 0);
   if (c == 0) return;
-  each([&](int e, uint32_t k) {
-    const bool kept = keeps(e, k, tied);
+#pragma unroll kUnroll
+  for (int e = 0; e < steps; ++e) {
+    const int p = base + 32 * e;
+    const bool kept = keeps(p);
     const uint32_t who = __ballot_sync(~0u, kept);
-    if (kept) out[place + __popc(who & below)] = pages[base + 32 * e];
+    if (kept) out[place + __popc(who & ((1u << lane) - 1))] = pages[p];
     place += __popc(who);
-  });
+  }
 }
 
 }  // namespace
@@ -622,14 +625,17 @@ extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stri
   a.sel_indptr = sel_indptr;
   a.sel_indices = sel_indices;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (rows == 0)
-    e = cudaMemsetAsync(sel_indptr, 0, sizeof(int32_t), s);
-  else if (score_stride <= 4096)   // lists can be no longer than a row of scores
-    e = launch_dependent(select_kernel<256, 16>, rows, 256, 0, 1, s, a);
-  else if (score_stride <= 16384)
-    e = launch_dependent(select_kernel<1024, 16>, rows, 1024, 0, 1, s, a);
-  else
-    e = launch_dependent(select_kernel<1024, 0>, rows, 1024, 0, 1, s, a);
+  // (a list is no longer than a row of scores; a run of 32 pages to a warp)
+  const int few = 256, many = 1024;
+  const bool wide = score_stride > kNarrow, staged = score_stride <= kStagedPages;
+  const int threads = wide ? many : few;
+  const size_t smem = staged ? (score_stride + threads - 1) / threads * threads * sizeof(uint32_t) : 0;
+  cudaError_t e = cudaSuccess;
+  auto kernel = !wide ? select_kernel<few, true> : staged ? select_kernel<many, true> : select_kernel<many, false>;
+  if (smem > 32 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess)
+    e = rows == 0 ? cudaMemsetAsync(sel_indptr, 0, sizeof(int32_t), s)
+                  : launch_dependent(kernel, rows, threads, smem, 1, s, a);
   return finish_call(e, &g_select_err, check_status, s);
 }

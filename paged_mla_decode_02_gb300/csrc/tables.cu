@@ -82,15 +82,17 @@ __global__ void __launch_bounds__(kThreads, 1) tables_kernel(const TablesArgs a)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ int sm[];
   __shared__ Sums warp_sums[32];
+  __shared__ int refusal;   // 1: invalid, 2: over a capacity
   const int B = a.batch, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* page_at = sm;                 // [B + 1] each: prefix sums
   int* fresh_at = page_at + B + 1;
   int* freed_at = fresh_at + B + 1;
   int* token_at = freed_at + B + 1;
   int* len = token_at + B + 1;       // [B]: the lengths before the step
-  const unsigned rank = kCtas > 1 ? tc::cluster_ctarank() : 0;
+  const int rank = tc::cluster_ctarank();
   const int P = 1 << a.page_shift;
   const int fc = *a.free_count;
+  if (tid == 0) refusal = 0;
 
   // thread t scans requests [t * per, (t + 1) * per)
   const int per = (B + kThreads - 1) / kThreads;
@@ -121,11 +123,15 @@ __global__ void __launch_bounds__(kThreads, 1) tables_kernel(const TablesArgs a)
     mine[i] = s;
     sum = sum + s;
   }
+  // (warps past the batch take no part, and leave the others the SM)
+  const int warps = (B + 32 * per - 1) / max(32 * per, 1);
   Sums incl = sum;
+  if (warp < warps) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const Sums o = shfl_up(incl, d);
-    if (lane >= d) incl = incl + o;
+    for (int d = 1; d < 32; d <<= 1) {
+      const Sums o = shfl_up(incl, d);
+      if (lane >= d) incl = incl + o;
+    }
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
@@ -160,21 +166,28 @@ __global__ void __launch_bounds__(kThreads, 1) tables_kernel(const TablesArgs a)
   const long long top = static_cast<long long>(fc) + total.freed;   // the stack's height before pages are taken
   invalid = invalid || top > a.num_pages;
   over = over || total.fresh > top || total.pages > a.indices_cap || total.tokens > a.max_tokens;
-  const int refused = __syncthreads_or((invalid ? 1 : 0) | (over ? 2 : 0));   // also publishes the sums
-  const bool any_invalid = __syncthreads_or(invalid);
+  if (invalid) atomicOr(&refusal, 1);
+  if (over) atomicOr(&refusal, 2);
+  __syncthreads();                                  // also publishes the sums
+  const int refused = refusal;
   if (rank == 0 && tid == 0)
-    *a.status = any_invalid ? MLA_ERR_INVALID_ARG : refused ? MLA_ERR_CAPACITY : MLA_OK;
-  // every CTA has read the lengths and the count: they may be written now
-  // (and the status by any thread that finds a bad page id)
-  if (kCtas > 1) tc::cluster_sync_all(); else __syncthreads();
+    *a.status = refused & 1 ? MLA_ERR_INVALID_ARG : refused ? MLA_ERR_CAPACITY : MLA_OK;
+  // Once every CTA has arrived here, all have read the lengths and the count:
+  // they may be written in place, and the status by a thread that finds a bad
+  // page id.
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  auto all_have_read = [] { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); };
 
-  const long long gid = static_cast<long long>(rank) * kThreads + tid;
+  // warps in turn over the CTAs, so that few elements use all of them
+  const int gwarp = warp * kCtas + rank;
+  const long long gid = 32ll * gwarp + lane;
   constexpr int kAll = kCtas * kThreads;
   if (refused) {
     for (long long t = gid; t < a.max_tokens; t += kAll) {
       a.slots[t] = -1;
       a.positions[t] = 0;
     }
+    all_have_read();
     for (long long b = gid; b < B; b += kAll) a.kv_len_out[b] = len[b];
     if (gid == 0) *a.free_count_out = fc;
     return;
@@ -195,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) tables_kernel(const TablesArgs a)
   {
     constexpr int kWarps = kAll / 32;
     const long long run = ((total.pages + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const long long lo = (rank * 32 + warp) * run;
+    const long long lo = gwarp * run;
     const int e1 = static_cast<int>(lo + run < total.pages ? lo + run : total.pages);
     int e = static_cast<int>(lo < total.pages ? lo : total.pages);
     if (e < e1) {
@@ -252,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) tables_kernel(const TablesArgs a)
     a.positions[t] = pos;
   }
 
+  all_have_read();
   for (long long b = gid; b <= B; b += kAll) {
     a.kv_indptr[b] = page_at[b];
     a.q_indptr[b] = token_at[b];
