@@ -310,19 +310,20 @@ def _check_layouts(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, page_size=None)
     through the raw pointers: the cache [pages, page_size, 512] and [pages,
     page_size, 64] of one dtype, q [..., 512] / [..., 64], out [..., 512] and
     lse [...] over the same leading dims."""
-    if ckv_cache.dim() != 3 or ckv_cache.shape[2] != 512:
-        raise ValueError(f"ckv_cache must be [num_pages, page_size, 512], got {tuple(ckv_cache.shape)}")
-    if tuple(kpe_cache.shape) != (ckv_cache.shape[0], ckv_cache.shape[1], 64):
+    cache, q = ckv_cache.shape, q_nope.shape
+    if len(cache) != 3 or cache[2] != 512:
+        raise ValueError(f"ckv_cache must be [num_pages, page_size, 512], got {tuple(cache)}")
+    if kpe_cache.shape != (cache[0], cache[1], 64):
         raise ValueError(f"kpe_cache must be [num_pages, page_size, 64] like ckv_cache, "
                          f"got {tuple(kpe_cache.shape)}")
     if kpe_cache.dtype != ckv_cache.dtype:
         raise ValueError("ckv_cache and kpe_cache must have the same dtype")
-    if page_size is not None and ckv_cache.shape[1] != page_size:
-        raise ValueError(f"the cache holds pages of {ckv_cache.shape[1]} tokens, the plan {page_size}")
-    lead = tuple(q_nope.shape[:-1])
-    if q_nope.shape[-1] != 512 or tuple(q_pe.shape) != lead + (64,):
+    if page_size is not None and cache[1] != page_size:
+        raise ValueError(f"the cache holds pages of {cache[1]} tokens, the plan {page_size}")
+    lead = tuple(q[:-1])
+    if q[-1] != 512 or q_pe.shape != lead + (64,):
         raise ValueError("q_nope must be [..., 512] and q_pe [..., 64] over the same leading dims")
-    if tuple(out.shape) != lead + (512,) or tuple(lse.shape) != lead:
+    if out.shape != q or lse.shape != lead:
         raise ValueError("out must be [..., 512] and lse [...] over q_nope's leading dims")
 
 
@@ -440,11 +441,9 @@ def mla_plan_partition_host(kv_indptr, kv_len, num_workers: int, tile_tokens: in
 # Around the decode (include/mla_paging.h)
 # ---------------------------------------------------------------------------
 
-def _on_device(dtype, names: str, *tensors, contiguous: bool = True) -> None:
-    """Each tensor (named in order in ``names``) is on the current CUDA device,
-    of ``dtype`` and (by default) contiguous."""
-    import torch
-    device = torch.cuda.current_device()
+def _on_device(device: int, dtype, names: str, *tensors, contiguous: bool = True) -> None:
+    """Each tensor (named in order in ``names``) is on CUDA device ``device``
+    (the current one), of ``dtype`` and (by default) contiguous."""
     for t in tensors:
         if t.get_device() != device or t.dtype is not dtype or (contiguous and not t.is_contiguous()):
             break
@@ -462,24 +461,24 @@ def _on_device(dtype, names: str, *tensors, contiguous: bool = True) -> None:
 def _row_stride(name: str, t, rows: int, cols=None) -> int:
     """The row stride of a [rows, cols] tensor whose rows are runs of adjacent
     entries (strides of dimensions of one entry or none say nothing)."""
-    if t.dim() != 2 or t.shape[0] != rows or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be [{rows}, {'columns' if cols is None else cols}], got {tuple(t.shape)}")
-    width = t.shape[1]
-    if width > 1 and rows > 0 and t.stride(1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{name} must be [{rows}, {'columns' if cols is None else cols}], got {tuple(shape)}")
+    if shape[1] > 1 and rows > 0 and stride[1] != 1:
         raise ValueError(f"{name} must have adjacent entries in a row")
     if rows < 2:
-        return width
-    if t.stride(0) < 0:
+        return shape[1]
+    if stride[0] < 0:
         raise ValueError(f"{name} must not have a negative stride")
-    return t.stride(0)
+    return stride[0]
 
 
-def _check_cache(ckv_cache, kpe_cache) -> int:
+def _check_cache(device: int, ckv_cache, kpe_cache) -> int:
     """The layout of a paged cache; returns its dtype code."""
     code = _dtype_code(ckv_cache, "ckv_cache")
     if code == DTYPE_FP32:
         raise ValueError("ckv_cache must be bfloat16 or float8_e4m3fn")
-    _on_device(ckv_cache.dtype, "ckv_cache kpe_cache", ckv_cache, kpe_cache)
+    _on_device(device, ckv_cache.dtype, "ckv_cache kpe_cache", ckv_cache, kpe_cache)
     shape = ckv_cache.shape
     if len(shape) != 3 or shape[2] != 512:
         raise ValueError(f"ckv_cache must be [num_pages, page_size, 512], got {tuple(shape)}")
@@ -501,11 +500,12 @@ def mla_build_tables(kv_len, new_len, block_table, free_pages, free_count, page_
         kv_len_out = kv_len
     if free_count_out is None:
         free_count_out = free_count
-    _on_device(torch.int32, "kv_len new_len kv_len_out free_pages free_count free_count_out kv_indptr kv_indices "
+    device = torch.cuda.current_device()
+    _on_device(device, torch.int32, "kv_len new_len kv_len_out free_pages free_count free_count_out kv_indptr kv_indices "
                "q_indptr positions status", kv_len, new_len, kv_len_out, free_pages, free_count, free_count_out,
                kv_indptr, kv_indices, q_indptr, positions, status)
-    _on_device(torch.int32, "block_table", block_table, contiguous=False)
-    _on_device(torch.int64, "slots", slots)
+    _on_device(device, torch.int32, "block_table", block_table, contiguous=False)
+    _on_device(device, torch.int64, "slots", slots)
     batch = kv_len.numel()
     stride = _row_stride("block_table", block_table, batch)
     if new_len.numel() != batch or kv_len_out.numel() != batch:
@@ -549,12 +549,13 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
     ckv [T, 512], kpe [T, 64] bf16 (rows may be strided), norm_weight bf16
     [512] or None.  Returns (or fills) q_pe_out, contiguous."""
     import torch
-    code = _check_cache(ckv_cache, kpe_cache)
+    device = torch.cuda.current_device()
+    code = _check_cache(device, ckv_cache, kpe_cache)
     if positions.dim() == 1:
         positions = positions[None]
-    _on_device(torch.int32, "positions", positions, contiguous=False)
-    _on_device(torch.int64, "slots", slots)
-    _on_device(torch.bfloat16, "ckv kpe", ckv, kpe, contiguous=False)
+    _on_device(device, torch.int32, "positions", positions, contiguous=False)
+    _on_device(device, torch.int64, "slots", slots)
+    _on_device(device, torch.bfloat16, "ckv kpe", ckv, kpe, contiguous=False)
     T = slots.numel()
     n_axes = rope.n_axes
     if positions.dim() != 2 or positions.shape[0] < n_axes:
@@ -562,12 +563,12 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
     axis_stride = _row_stride("positions", positions, positions.shape[0], T)
     ckv_stride, kpe_stride = _row_stride("ckv", ckv, T, 512), _row_stride("kpe", kpe, T, 64)
     if norm_weight is not None:
-        _on_device(torch.bfloat16, "norm_weight", norm_weight)
+        _on_device(device, torch.bfloat16, "norm_weight", norm_weight)
         if norm_weight.numel() != 512:
             raise ValueError("norm_weight must have 512 entries")
     H, q_ptr, q_t, q_h, out_ptr = 0, None, 0, 0, None
     if q_pe is not None:
-        _on_device(torch.bfloat16, "q_pe", q_pe, contiguous=False)
+        _on_device(device, torch.bfloat16, "q_pe", q_pe, contiguous=False)
         if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != 64 or (q_pe.numel() and q_pe.stride(2) != 1):
             raise ValueError("q_pe must be [tokens, heads, 64] with adjacent dims")
         H = q_pe.shape[1]
@@ -575,7 +576,7 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
         if q_pe_out is None:
             q_pe_out = torch.empty((T, H, 64), dtype=torch.bfloat16, device=q_pe.device)
         else:
-            _on_device(torch.bfloat16, "q_pe_out", q_pe_out)
+            _on_device(device, torch.bfloat16, "q_pe_out", q_pe_out)
             if q_pe_out.shape != q_pe.shape:
                 raise ValueError("q_pe_out must have the shape of q_pe")
         q_ptr, out_ptr = q_pe.data_ptr(), q_pe_out.data_ptr()
@@ -596,9 +597,10 @@ def mla_summarize_pages(slots, ckv_cache, kpe_cache, summaries, kv_scale: float 
     """Mean rows of the pages that the tokens at ``slots`` completed, into
     summaries bf16 [num_pages, 576] (see mla_paging.h)."""
     import torch
-    code = _check_cache(ckv_cache, kpe_cache)
-    _on_device(torch.int64, "slots", slots)
-    _on_device(torch.bfloat16, "summaries", summaries)
+    device = torch.cuda.current_device()
+    code = _check_cache(device, ckv_cache, kpe_cache)
+    _on_device(device, torch.int64, "slots", slots)
+    _on_device(device, torch.bfloat16, "summaries", summaries)
     if summaries.shape != (ckv_cache.shape[0], 576):
         raise ValueError("summaries must be [num_pages, 576]")
     st = load_library().mla_summarize_pages(slots.data_ptr(), slots.numel(), ckv_cache.data_ptr(),
@@ -616,9 +618,10 @@ def mla_page_scores(q_nope, q_pe, summaries, kv_indptr, kv_indices, scores, chec
     kv_indptr / kv_indices int32 device tensors, scores fp32 [R, >= longest
     list] (rows may be strided)."""
     import torch
-    _on_device(torch.bfloat16, "q_nope q_pe summaries", q_nope, q_pe, summaries)
-    _on_device(torch.int32, "kv_indptr kv_indices", kv_indptr, kv_indices)
-    _on_device(torch.float32, "scores", scores, contiguous=False)
+    device = torch.cuda.current_device()
+    _on_device(device, torch.bfloat16, "q_nope q_pe summaries", q_nope, q_pe, summaries)
+    _on_device(device, torch.int32, "kv_indptr kv_indices", kv_indptr, kv_indices)
+    _on_device(device, torch.float32, "scores", scores, contiguous=False)
     rows = kv_indptr.numel() - 1
     lead = q_nope.shape[:-1]
     if len(lead) < 2 or lead[0] != rows or q_nope.shape[-1] != 512 or q_pe.shape != lead + (64,):
@@ -642,9 +645,10 @@ def mla_select_pages(scores, kv_indptr, kv_indices, top_k: int, keep_first: int,
     keep_first, the last keep_last and the best scoring others, min(top_k, n)
     in all, in their order (see mla_paging.h)."""
     import torch
-    _on_device(torch.int32, "kv_indptr kv_indices sel_indptr sel_indices", kv_indptr, kv_indices, sel_indptr,
+    device = torch.cuda.current_device()
+    _on_device(device, torch.int32, "kv_indptr kv_indices sel_indptr sel_indices", kv_indptr, kv_indices, sel_indptr,
                sel_indices)
-    _on_device(torch.float32, "scores", scores, contiguous=False)
+    _on_device(device, torch.float32, "scores", scores, contiguous=False)
     rows = kv_indptr.numel() - 1
     stride = _row_stride("scores", scores, rows)
     if stride < scores.shape[1]:
@@ -748,8 +752,7 @@ class MLASparseDecoder:
         self._sel_indptr = torch.zeros(self.max_batch + 1, dtype=torch.int32, device=dev)
         self._kv_indptr = torch.zeros(self.max_batch + 1, dtype=torch.int32, device=dev)
         self._scores = torch.empty((self.max_batch, self.max_pages), dtype=torch.float32, device=dev)
-        self._kv_indices = None
-        self.batch = 0
+        self._kv_indices, self.sel_indptr, self.batch = None, None, 0
 
     def plan(self, kv_indptr, kv_indices, kv_len, page_size: int, sm_scale: float, stream=None,
              q_len: int = 0) -> None:
@@ -767,7 +770,7 @@ class MLASparseDecoder:
             raise ValueError("kv_indptr must count ceil(kv_len / page_size) pages for each request")
         if batch > self.max_batch or np.any(pages > self.max_pages):
             raise MLAError(ERR_CAPACITY, "the batch exceeds the decoder's max_batch or max_pages")
-        _on_device(torch.int32, "kv_indices", kv_indices)
+        _on_device(torch.cuda.current_device(), torch.int32, "kv_indices", kv_indices)
         if kv_indices.numel() < indptr[-1]:
             raise ValueError("kv_indices is shorter than kv_indptr says")
         if q_len * self.decoder.num_heads > 128:
@@ -789,11 +792,9 @@ class MLASparseDecoder:
         with torch.cuda.stream(stream):
             self._kv_indptr.copy_(torch.from_numpy(whole))
         self._kv_indices, self.batch = kv_indices, batch   # keep the borrowed page list alive
-
-    @property
-    def sel_indptr(self):
-        """Device offsets of each request's selected pages in ``sel_indices``, after a run."""
-        return self._sel_indptr[:self.batch + 1]
+        # (slices of the decoder's buffers: made here, once, as each costs the host some microseconds)
+        self._lists, self._rows = self._kv_indptr[:batch + 1], self._scores[:batch]
+        self.sel_indptr = self._sel_indptr[:batch + 1]   # device offsets of the selected pages, after a run
 
     def run(self, q_nope, q_pe, ckv_cache, kpe_cache, summaries, out=None, lse=None, kv_scale: float = 1.0,
             out_dtype=None, stream=None):
@@ -801,10 +802,9 @@ class MLASparseDecoder:
         the cache and its page summaries [num_pages, 576]; returns out, lse."""
         if self._kv_indices is None:
             raise MLAError(ERR_NOT_PLANNED, "MLASparseDecoder.run before plan")
-        n = self.batch
-        indptr, scores = self._kv_indptr[:n + 1], self._scores[:n]
-        mla_page_scores(q_nope, q_pe, summaries, indptr, self._kv_indices, scores, stream=stream)
-        mla_select_pages(scores, indptr, self._kv_indices, self.top_k, self.keep_first, self.keep_last,
+        stream = _stream_handle(stream)
+        mla_page_scores(q_nope, q_pe, summaries, self._lists, self._kv_indices, self._rows, stream=stream)
+        mla_select_pages(self._rows, self._lists, self._kv_indices, self.top_k, self.keep_first, self.keep_last,
                          self.sel_indptr, self.sel_indices, stream=stream)
         return self.decoder.run(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale, out_dtype, stream)
 
