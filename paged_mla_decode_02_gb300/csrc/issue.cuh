@@ -6,7 +6,9 @@
 // issue, whatever its size (measured: M 128, K 16, N 16 to 128).  With the
 // lane elected inside the instruction's own block, in a warp whose index came
 // through a shuffle, it is 39 cycles for N = 16 and 64 for N = 128, the
-// tensor core's own time.
+// tensor core's own time; votes and exits between the MMAs add to that (four
+// MMAs, N = 128, with two waits and two commits: 411 cycles in a loop that
+// leaves on a failed wait, 260 unrolled with waits that do not).
 #pragma once
 #include "tc_utils.cuh"
 
@@ -20,6 +22,24 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
   return one != 0;
+}
+
+// Bounded wait of a converged warp, without the vote and the early return of
+// mbar_wait_warp: code after it stays one straight line, in which the operands
+// of the instructions below are known to be uniform.  False when the wait ran
+// out or another role gave up (the caller goes on to its next check).
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++i) {
+    if ((i & 63u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) *abort_flag = 1;
+      if (*abort_flag) return false;
+    }
+  }
+  return true;
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16.
@@ -57,6 +77,45 @@ __device__ __forceinline__ void tma_load_2d_elect(uint32_t dst, const void* tmap
       " [%0], [%1, {%2, %3}], [%4];\n"
       "}\n" ::"r"(dst),
       "l"(tmap), "r"(x), "r"(y), "r"(bar), "r"(bytes)
+      : "memory");
+}
+
+// The same over a CTA pair (cta_group::2), issued in its even CTA.
+__device__ __forceinline__ void mma_pair_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One arrive on the mbarrier at this offset in the CTAs of the pair that `ctas`
+// has a bit for.
+__device__ __forceinline__ void commit_pair_elect(uint32_t bar, int ctas) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n"
+      "}\n" ::"r"(bar),
+      "h"(static_cast<uint16_t>(ctas))
+      : "memory");
+}
+// Load the box at {x, y}, completing on an mbarrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair_elect(uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                                       uint32_t cluster_bar) {
+  asm volatile(
+      "{\n"
+      ".reg .pred q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "@q cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];\n"
+      "}\n" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
 }
 

@@ -43,18 +43,24 @@ __device__ __forceinline__ int list_of(const Lists& l, int r, int* first) {
 //
 // A row's scores are the row maxima of S = summaries[pages] . q^T, a product
 // of M = pages, N = heads, K = 576 that reads 1152 bytes per page: bound by
-// HBM, and next by what passes from L2 to the SMs.  The pages of all rows in
-// a line (the page lists laid end to end) are cut into one even run for each
-// SM; a CTA takes its run in tiles of up to 128 pages of one row.
+// HBM, and next by what passes from L2 to the SMs.  The rows' lists are cut
+// into tiles of up to 128 pages, and each CTA takes an even share of the tiles
+// in order.  (Few or short lists make smaller tiles, so that all SMs take
+// part: the size, of four, with the least estimated time of the fullest CTA.)
 // - One warp copies a row's queries into shared memory by TMA, in nine panels
 //   of 64 dims that stay for all tiles of the row (and make way one by one for
 //   the next row's).
-// - Four warps copy the pages' rows, a 64-dim chunk at a time, through a ring
-//   of panels with cp.async.  (As tile::gather4 copies the TMA took 90 cycles
-//   for four 128-byte rows, half the speed.)
-// - One thread issues the tcgen05 MMAs into one of two TMEM accumulators.
+// - Two sets of four warps copy the pages' rows, a 64-dim chunk at a time,
+//   through a ring of panels with cp.async.  (As tile::gather4 copies the TMA
+//   took 90 cycles for four 128-byte rows, half the speed.)
+// - One warp issues the tcgen05 MMAs into one of two TMEM accumulators.
 // - Four warps read the other: a TMEM lane holds one page's products with
 //   all heads, so a thread takes its page's maximum without any exchange.
+// With more than 48 heads the queries would leave room for four panels of the
+// nine of a tile, too few to cover the latency of memory, so a run is shared by a CTA pair
+// (kPair, cta_group::2): a tile's pages are halved between the two CTAs, as
+// are the heads of the queries that each holds, and the even CTA issues MMAs
+// of M = 256 that read both.
 struct ScoreArgs {
   const char* summaries;
   int num_pages;
@@ -69,25 +75,29 @@ constexpr int kCopyWarps = 4;           // of each of two sets that take turns
 constexpr int kTilePages = 128;         // the MMA's M
 constexpr int kChunks = kD / 64;        // panels of 64 dims
 constexpr int kPanelBytes = kTilePages * 128;
-constexpr int kMinRun = 32;             // pages of a CTA's run, at least
-// Panels of the ring: with few heads a whole tile's, so that a short run
-// waits for memory once; with more, what the queries leave room for.
-constexpr int kFewHeads = 48, kStagesFew = kChunks, kStagesMany = 4;
-template <int kStages>
-struct ScoreBars {
+constexpr int kSizes = 4;               // tile sizes to choose from: quarters of the largest
+constexpr unsigned kMostTiles = (1u << 26) + 1024;   // 2^31 pages of kv_indices in tiles of 32, and a part for each row
+constexpr int kTileCost = 48;           // what a tile costs beyond its pages, in pages
+constexpr int kFewHeads = 48;           // as many as one CTA serves
+constexpr int kScoreRows = 640;         // rows of a launch: their lists' places are in shared memory
+template <bool kPair>
+struct ScoreForm {
+  static constexpr int kCtas = kPair ? 2 : 1, kStages = kChunks;   // panels of the ring: a tile's
+  // full (pages, queries) and accumulator-free barriers count in the even CTA
   enum { kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + kChunks, kTFull = kQEmpty + kChunks,
-         kTEmpty = kTFull + 2, kFinal = kTEmpty + 2, kCount };
+         kTEmpty = kTFull + 2, kFinal = kTEmpty + 2, kBars };
+  // heads that a CTA holds (the MMA's N over the CTAs, each a multiple of 16)
+  __host__ __device__ static constexpr int heads_held(int heads) {
+    return (heads + 16 * kCtas - 1) / (16 * kCtas) * 16;
+  }
+  __host__ __device__ static constexpr int smem(int heads, int rows) {
+    return kStages * kPanelBytes + kChunks * heads_held(heads) * 128 + 8 * kBars + 16 + 4 * (3 * rows + 1) + 1024;
+  }
 };
-
-template <int kStages>
-constexpr int scores_smem(int heads, int rows) {
-  return kStages * kPanelBytes + kChunks * ((heads + 15) / 16 * 16) * 128 + 8 * ScoreBars<kStages>::kCount + 16 +
-         4 * (rows + 1) + 1024;
-}
 
 struct Tile {
   int row, page0, pages;   // pages page0 .. page0 + pages - 1 of the row's list
-  bool enters, leaves;     // the first, the last tile of the row in this run
+  bool enters, leaves;     // the first, the last tile of the row in this share
 };
 
 // 16 bytes into shared memory, the 256 around them into L2: the next chunk of
@@ -96,98 +106,155 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-template <int kStages>
+template <bool kPair>
 __global__ void __launch_bounds__(kScoreThreads, 1)
     scores_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qp,
                   const ScoreArgs a) {
   using namespace tc;
-  using Bars = ScoreBars<kStages>;
+  using F = ScoreForm<kPair>;
+  constexpr int kStages = F::kStages;
   constexpr int kCopiesAhead = kStages / 2 - 1;   // chunks of pages a copying thread leaves in flight
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int heads16 = (a.heads + 15) & ~15;
-  const int q_panel = heads16 * 128;                     // bytes of a panel of queries
+  const int held = F::heads_held(a.heads);               // heads whose queries this CTA holds
+  const int q_panel = held * 128;                        // bytes of a panel of them
   const int used = kStages * kPanelBytes + kChunks * q_panel;
   const uint32_t base = smem_u32(sm), q_base = base + kStages * kPanelBytes;
   const uint32_t bars = base + used;
   auto bar = [&](int i) { return bars + 8 * i; };
-  unsigned char* after = sm + used + 8 * Bars::kCount;
+  unsigned char* after = sm + used + 8 * F::kBars;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(after);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(after + 4);
-  int* at = reinterpret_cast<int*>(after + 16);          // [rows + 1]: pages before each row
-  __shared__ long long warp_sum[kScoreThreads / 32];
+  int* at = reinterpret_cast<int*>(after + 16);          // [rows + 1]: tiles before each row
+  int* first_of = at + a.rows + 1;                       // [rows]: where its list begins, and its pages
+  int* len_of = first_of + a.rows;
+  __shared__ int warp_sum[kScoreThreads / 32];
+  __shared__ unsigned size_sum[kSizes][kScoreThreads / 32];
   const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
-  auto run_of = [](int64_t pages) {   // pages of a CTA's run
-    const int64_t even = (pages + gridDim.x - 1) / gridDim.x;
-    return even > kMinRun ? even : static_cast<int64_t>(kMinRun);
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+  auto wait = [&](int i, int parity) {
+    return kPair ? mbar_wait_cl_warp(bar(i), parity, abort_flag) : mbar_wait_warp(bar(i), parity, abort_flag);
+  };
+  auto spin = [&](int i, int parity) { return mbar_spin<kPair>(bar(i), parity, abort_flag); };
+  auto arrive_even = [&](int i) {   // at the even CTA's barrier
+    if (kPair) mbar_arrive_remote(map_to_rank(bar(i), 0)); else mbar_arrive(bar(i));
+  };
+  auto commit = [&](int i, int ctas = 3) {   // at the CTAs' barriers (a bit for each)
+    if (kPair) commit_pair_elect(bar(i), ctas); else mma_commit_elect(bar(i));
   };
   if (tid == 0) *abort_flag = 0;
-  if (tid < Bars::kCount) {
-    mbar_init(bar(tid), tid < Bars::kEmpty ? kCopyWarps : tid == Bars::kTEmpty || tid == Bars::kTEmpty + 1 ? 4 : 1);
+  if (tid < F::kBars) {
+    mbar_init(bar(tid), tid < F::kEmpty                                ? kCopyWarps * F::kCtas
+                        : tid == F::kTEmpty || tid == F::kTEmpty + 1 ? 4 * F::kCtas
+                                                                     : 1);
     fence_barrier_init();
   }
-  if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 2 * kMaxHeads);
+  if (warp == 0) {
+    if (kPair) tmem_alloc_pair(smem_u32(tmem_slot), 2 * kMaxHeads);
+    else tmem_alloc(smem_u32(tmem_slot), 2 * kMaxHeads);
+  }
   // (what came before touches no memory of the previous kernel's)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // pages before each row, over the rows' lists as far as they are sound
-  long long all;
-  {
-    const int per = (a.rows + kScoreThreads - 1) / kScoreThreads;
-    long long sum = 0;
-    int first;
-#pragma unroll 1
-    for (int i = 0; i < per; ++i) {
-      const int r = tid * per + i;
-      if (r < a.rows) sum += list_of(a.lists, r, &first);
-      if (r < a.rows) at[r + 1] = static_cast<int>(sum);
+  // how many tiles of each size the lists make (32 bits hold a warp's)
+  constexpr int kPer = (kScoreRows + kScoreThreads - 1) / kScoreThreads;   // rows of a thread
+  constexpr int kQuarter = kTilePages * F::kCtas / kSizes;
+  const int units = gridDim.x / F::kCtas;
+  unsigned len[kPer], sum[kSizes] = {};
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int r = tid * kPer + i;
+    int first = 0;
+    len[i] = r < a.rows ? list_of(a.lists, r, &first) : 0;
+    if (r < a.rows) first_of[r] = first;
+#pragma unroll
+    for (int k = 0; k < kSizes; ++k) sum[k] += (len[i] + (k + 1) * kQuarter - 1) / ((k + 1) * kQuarter);
+  }
+#pragma unroll
+  for (int k = 0; k < kSizes; ++k) {
+    sum[k] = __reduce_add_sync(~0u, sum[k]);
+    if (lane == 0) size_sum[k][warp] = sum[k];
+  }
+  __syncthreads();
+  int quarters = kSizes, total = 0;
+  float least = 0.f;
+  bool sound = true;
+#pragma unroll
+  for (int k = kSizes; k > 0; --k) {
+    const unsigned some = lane < kScoreThreads / 32 ? size_sum[k - 1][lane] : 0;
+    // a warp's rows make no more tiles than kv_indices can hold, or their
+    // lists overlap (kv_indptr goes back)
+    sound &= !__any_sync(~0u, some > kMostTiles);
+    const int n = __reduce_add_sync(~0u, some);
+    const float cost = ceilf(static_cast<float>(n) / units) * (k * kQuarter + kTileCost);
+    if (k == kSizes || cost < least) {
+      quarters = k;
+      least = cost;
+      total = n;
     }
-    long long incl = sum;
+  }
+  const int tile = quarters * kQuarter;
+  auto tiles_of = [&](unsigned pages) -> int {   // of a list
+    const unsigned t = (pages + kQuarter - 1) / kQuarter;
+    return quarters == 1 ? t : quarters == 2 ? (t + 1) >> 1 : quarters == 3 ? (t + 2) / 3 : (t + 3) >> 2;
+  };
+  if (!sound) {
+    if (tid == 0) report_error(&g_select_err, kErrBounds);
+    total = 0;
+  }
+  // tiles before each row
+  {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) mine += tiles_of(len[i]);
+    int incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(~0u, incl, d);
+      const int o = __shfl_up_sync(~0u, incl, d);
       if (lane >= d) incl += o;
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    long long before = incl - sum;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-#pragma unroll 1
-    for (int i = 0; i < per; ++i)
-      if (tid * per + i < a.rows) at[tid * per + i + 1] += static_cast<int>(before);
+    int before = incl - mine + __reduce_add_sync(~0u, lane < warp ? warp_sum[lane] : 0);
     if (tid == 0) at[0] = 0;
-    all = 0;
-    for (int w = 0; w < kScoreThreads / 32; ++w) all += warp_sum[w];
-    // more than kv_indices can hold: lists that overlap (kv_indptr goes back)
-    if (all > INT32_MAX && tid == 0) report_error(&g_select_err, kErrBounds);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      before += tiles_of(len[i]);
+      if (tid * kPer + i < a.rows) at[tid * kPer + i + 1] = before;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (tid * kPer + i < a.rows) len_of[tid * kPer + i] = len[i];
   }
   tc_fence_before();
-  __syncthreads();
+  if (kPair) cluster_sync_all(); else __syncthreads();   // (a pair: both CTAs' barriers are there)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  // this CTA's run of the line of pages
-  const int total = all > INT32_MAX ? 0 : static_cast<int>(all);
-  const int64_t run = run_of(total), lo = blockIdx.x * run;
-  const int begin = static_cast<int>(lo < total ? lo : total);
-  int pos = begin;
-  const int end = static_cast<int>(lo + run < total ? lo + run : total);
-  int row = 0;
-  if (pos < end) {   // the row that holds page pos
+  // this CTA's (pair's) share of them
+  const int unit = blockIdx.x / F::kCtas;
+  const int each = total / units, more = total % units;
+  const int begin = unit * each + min(unit, more), end = begin + each + (unit < more);
+  int pos = begin, row = 0;
+  if (pos < end) {   // the row that holds tile pos
     int hi = a.rows;
     while (hi - row > 1) {
       const int mid = (row + hi) >> 1;
       if (at[mid] <= pos) row = mid; else hi = mid;
     }
   }
-  // the tiles of the run, in order (every role walks the same ones)
+  // the tiles of the share, in order (every role walks the same ones)
   auto next = [&](Tile& t) {
     if (pos >= end) return false;
     while (at[row + 1] <= pos) ++row;
-    const int stop = at[row + 1] < end ? at[row + 1] : end;
-    const int n = stop - pos < kTilePages ? stop - pos : kTilePages;
-    t = {row, pos - at[row], n, pos == at[row] || pos == begin, pos + n == stop};
-    pos += n;
+    const int page0 = (pos - at[row]) * tile, n = min(tile, len_of[row] - page0);
+    t = {row, page0, n, pos == at[row] || pos == begin, pos + 1 == at[row + 1] || pos + 1 == end};
+    if (kPair) {   // this CTA's half (of a single page: none)
+      const int half = (n + 1) >> 1;
+      t.pages = rank ? n - half : half;
+      if (rank && t.pages) t.page0 += half;
+    }
+    ++pos;
     return true;
   };
   bool ok = true;
@@ -196,25 +263,33 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (warp == 0) {
     // ---------------- queries ----------------
     // (here and below, votes make the loops' conditions uniform to the compiler)
-    int n = 0, visit = 0;   // panels copied, rows entered
+    int visit = 0;   // rows entered
     while (ok && __any_sync(~0u, next(t))) {
       if (!__any_sync(~0u, t.enters)) continue;
-      const int y = t.row * a.heads, bytes = a.heads * 128;
-#pragma unroll 1
-      for (int c = 0; c < kChunks - 1; ++c, ++n) {
-        if (!(ok = mbar_wait_warp(bar(Bars::kQEmpty + c), (visit & 1) ^ 1, abort_flag))) break;
-        tma_load_2d_elect(q_base + c * q_panel, &map_qn, 64 * c, y, bar(Bars::kQFull + c), bytes);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        ok &= spin(F::kQEmpty + c, (visit & 1) ^ 1);
+        const bool pe = c == kChunks - 1;
+        const void* map = pe ? &map_qp : &map_qn;
+        const int x = pe ? 0 : 64 * c, y = t.row * a.heads + rank * held, full = F::kQFull + c;
+        if (kPair) {
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(full), 2 * q_panel);
+          __syncwarp();
+          tma_load_2d_pair_elect(q_base + c * q_panel, map, x, y, map_to_rank(bar(full), 0));
+        } else {
+          tma_load_2d_elect(q_base + c * q_panel, map, x, y, bar(full), a.heads * 128);
+        }
       }
-      if (!ok || !(ok = mbar_wait_warp(bar(Bars::kQEmpty + kChunks - 1), (visit & 1) ^ 1, abort_flag))) break;
-      tma_load_2d_elect(q_base + (kChunks - 1) * q_panel, &map_qp, 0, y, bar(Bars::kQFull + kChunks - 1), bytes);
-      ++n;
+      ok = __all_sync(~0u, ok);
       ++visit;
     }
     if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
-    if (lane == 0) {   // every copy issued has landed before the CTA leaves
+    if (rank == 0 && lane == 0) {   // every copy issued has landed before the CTA leaves
 #pragma unroll 1
-      for (int k = 1; k <= kChunks && k <= n; ++k)
-        mbar_wait_drain(bar(Bars::kQFull + (n - k) % kChunks), ((n - k) / kChunks) & 1);
+      for (int c = 0; c < kChunks && visit > 0; ++c) {
+        const uint32_t b = bar(F::kQFull + c), parity = (visit - 1) & 1;
+        if (kPair) mbar_wait_cl_drain(b, parity); else mbar_wait_drain(b, parity);
+      }
     }
     __syncwarp();
   } else if (warp >= 6) {
@@ -224,7 +299,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int set = (warp - 6) / kCopyWarps, i = (tid - 6 * 32) % (32 * kCopyWarps), col = i & 7, row0 = i >> 3;
     const uint32_t dst = base + row0 * 128 + ((col ^ (row0 & 7)) << 4);
     auto row_of = [&](const Tile& x, int p) {   // page p of the tile (a wrong id reads page 0; scored -inf below)
-      const int id = a.lists.indices[a.lists.indptr[x.row] + x.page0 + (p < x.pages ? p : x.pages - 1)];
+      const int id = a.lists.indices[first_of[x.row] + x.page0 + (p < x.pages ? p : x.pages ? x.pages - 1 : 0)];
       return a.summaries + static_cast<int64_t>(id < 0 || id >= a.num_pages ? 0 : id) * (2 * kD);
     };
     int turn = set, slot = set % kStages, phase = 1;        // the set's next chunk: its number, slot and phase
@@ -232,7 +307,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     auto land = [&]() {   // the set's oldest chunk in flight is in place
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Bars::kFull + landing));
+      if (lane == 0) arrive_even(F::kFull + landing);
       landing += 2;
       if (landing >= kStages) landing -= kStages;
       --pending;
@@ -244,7 +319,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int rows16 = (t.pages + 15) >> 4;
 #pragma unroll 1
       for (; turn < first + kChunks; turn += 2) {
-        if (!(ok = mbar_wait_warp(bar(Bars::kEmpty + slot), phase, abort_flag))) break;
+        if (!(ok = wait(F::kEmpty + slot, phase))) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (j < rows16) copy16(dst + slot * kPanelBytes + j * 2048, src[j]);
@@ -267,37 +342,39 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     while (ok && pending > 0) land();
     if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
   } else if (warp == 1) {
-    // ---------------- MMAs ----------------
-    const uint32_t idesc = idesc_bf16_f32(kTilePages, heads16, false, false);
-    int slot = 0, phase = 0, n = 0, visit = -1;   // visit: rows entered before this one
-    for (; ok && __any_sync(~0u, next(t)); ++n) {
+    // ---------------- MMAs (a pair: in its even CTA) ----------------
+    const uint32_t idesc = idesc_bf16_f32(kTilePages * F::kCtas, held * F::kCtas, false, false);
+    int n = 0, visit = -1;   // tiles, and rows entered, before this one
+    for (; rank == 0 && ok && __any_sync(~0u, next(t)); ++n) {
       const int acc = n & 1;
       const bool enters = __any_sync(~0u, t.enters), leaves = __any_sync(~0u, t.leaves);
       visit += enters;
-      if (!(ok = mbar_wait_warp(bar(Bars::kTEmpty + acc), ((n >> 1) & 1) ^ 1, abort_flag))) break;
-#pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        if (enters && !(ok = mbar_wait_warp(bar(Bars::kQFull + c), visit & 1, abort_flag))) break;
-        if (!(ok = mbar_wait_warp(bar(Bars::kFull + slot), phase, abort_flag))) break;
+      ok &= spin(F::kTEmpty + acc, ((n >> 1) & 1) ^ 1);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {   // panel c of the ring holds chunk c of every tile
+        if (enters) ok &= spin(F::kQFull + c, visit & 1);
+        ok &= spin(F::kFull + c, n & 1);
         tc_fence_after();
-        const uint64_t da = smem_desc(base + slot * kPanelBytes, 16, 1024, kSw128);
+        const uint64_t da = smem_desc(base + c * kPanelBytes, 16, 1024, kSw128);
         const uint64_t dq = smem_desc(q_base + c * q_panel, 16, 1024, kSw128);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss_elect(tmem + acc * kMaxHeads, da + 2 * kk, dq + 2 * kk, idesc, (c | kk) != 0);
-        mma_commit_elect(bar(Bars::kEmpty + slot));
-        if (leaves) mma_commit_elect(bar(Bars::kQEmpty + c));
-        if (++slot == kStages) {
-          slot = 0;
-          phase ^= 1;
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kPair) mma_pair_elect(tmem + acc * kMaxHeads, da + 2 * kk, dq + 2 * kk, idesc, (c | kk) != 0);
+          else mma_ss_elect(tmem + acc * kMaxHeads, da + 2 * kk, dq + 2 * kk, idesc, (c | kk) != 0);
         }
+        commit(F::kEmpty + c);
+        if (leaves) commit(F::kQEmpty + c);
       }
-      if (!ok) break;
-      mma_commit_elect(bar(Bars::kTFull + acc));
+      commit(F::kTFull + acc);
+      ok = __all_sync(~0u, ok);
     }
     if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
-    mma_commit_elect(bar(Bars::kFinal));   // every MMA issued completes before TMEM is freed
-    if (lane == 0) mbar_wait_drain(bar(Bars::kFinal), 0);
+    if (rank == 0) {
+      commit(F::kFinal, 1);   // every MMA issued completes before TMEM is freed
+      if (lane == 0) {
+        if (kPair) mbar_wait_cl_drain(bar(F::kFinal), 0); else mbar_wait_drain(bar(F::kFinal), 0);
+      }
+    }
     __syncwarp();
   } else {
     // ---------------- maxima: page 32 quad + lane of the tile ----------------
@@ -305,13 +382,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     for (int n = 0; ok && next(t); ++n) {
       const int acc = n & 1, p = 32 * quad + lane;
       int id = -1;
-      if (p < t.pages) id = a.lists.indices[a.lists.indptr[t.row] + t.page0 + p];
-      if (!(ok = mbar_wait_warp(bar(Bars::kTFull + acc), (n >> 1) & 1, abort_flag))) break;
+      if (p < t.pages) id = a.lists.indices[first_of[t.row] + t.page0 + p];
+      if (!(ok = wait(F::kTFull + acc, (n >> 1) & 1))) break;
       tc_fence_after();
       float best = -INFINITY;
       if (32 * quad < t.pages) {
 #pragma unroll 1
-        for (int c = 0; c < heads16; c += 32) {
+        for (int c = 0; c < a.heads; c += 32) {
           uint32_t v[32];
           tmem_ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + acc * kMaxHeads + c, v);
           tmem_ld_wait();
@@ -322,7 +399,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Bars::kTEmpty + acc));
+      if (lane == 0) arrive_even(F::kTEmpty + acc);
       if (p < t.pages) {
         if (id < 0 || id >= a.num_pages) {
           report_error(&g_select_err, kErrBounds);
@@ -334,10 +411,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
   }
   tc_fence_before();
-  __syncthreads();
+  if (kPair) cluster_sync_all(); else __syncthreads();   // (a pair: neither reads the other's memory any more)
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * kMaxHeads);
+    if (kPair) tmem_dealloc_pair(tmem, 2 * kMaxHeads);
+    else tmem_dealloc(tmem, 2 * kMaxHeads);
   }
 }
 
@@ -577,26 +655,29 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
   a.scores = scores;
   a.stride = score_stride;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (rows > 0) {
+  // one CTA to a run of pages with few heads, else a pair
+  const bool pair = num_heads > kFewHeads;
+  const int ctas = pair ? 2 : 1, box = pair ? ScoreForm<true>::heads_held(num_heads) : num_heads;
+  static_assert(ScoreForm<false>::smem(kFewHeads, kScoreRows) <= 227 * 1024 - 128 &&
+                ScoreForm<true>::smem(kMaxHeads, kScoreRows) <= 227 * 1024 - 128, "shared memory of a CTA");
+  auto kernel = pair ? scores_kernel<true> : scores_kernel<false>;
+  int sms = 0;
+  cudaError_t e = rows > 0 ? current_sms(&sms) : cudaSuccess;
+  for (int r0 = 0; r0 < rows && e == cudaSuccess; r0 += kScoreRows) {
+    a.rows = rows - r0 < kScoreRows ? rows - r0 : kScoreRows;
+    a.lists.indptr = kv_indptr + r0;
+    a.scores = scores + r0 * score_stride;
+    const int64_t first = static_cast<int64_t>(r0) * num_heads, q_rows = static_cast<int64_t>(a.rows) * num_heads;
     CUtensorMap mn, mp;
-    const int64_t q_rows = static_cast<int64_t>(rows) * num_heads;
-    if (!encode_rows(&mn, q_nope, q_rows, kDCkv, num_heads) ||
-        !encode_rows(&mp, q_pe, q_rows, kDKpe, num_heads))
+    if (!encode_rows(&mn, static_cast<const char*>(q_nope) + first * kDCkv * 2, q_rows, kDCkv, box) ||
+        !encode_rows(&mp, static_cast<const char*>(q_pe) + first * kDKpe * 2, q_rows, kDKpe, box))
       return MLA_ERR_CUDA;
-    int sms = 0;
-    e = current_sms(&sms);
-    const bool few = num_heads <= kFewHeads;
-    auto kernel = few ? scores_kernel<kStagesFew> : scores_kernel<kStagesMany>;
-    const int smem = few ? scores_smem<kStagesFew>(num_heads, rows) : scores_smem<kStagesMany>(num_heads, rows);
-    static_assert(scores_smem<kStagesFew>(kFewHeads, kMaxRows) <= 227 * 1024 - 128 &&
-                  scores_smem<kStagesMany>(kMaxHeads, kMaxRows) <= 227 * 1024 - 128, "shared memory of a CTA");
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    // no more CTAs than the lists have runs of the least length
-    const int64_t runs = (n_indices + kMinRun - 1) / kMinRun;
-    const int grid = static_cast<int>(runs < 1 ? 1 : runs < sms ? runs : sms);
-    if (e == cudaSuccess)
-      e = launch_dependent(kernel, grid, kScoreThreads, smem, 1, s, mn, mp, a);
+    const int smem = pair ? ScoreForm<true>::smem(num_heads, a.rows) : ScoreForm<false>::smem(num_heads, a.rows);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // no more CTAs than the lists can have tiles of the smallest size
+    const int64_t tiles = n_indices / (kTilePages * ctas / kSizes) + a.rows, most = sms / ctas;
+    const int grid = ctas * static_cast<int>(tiles < most ? tiles : most);
+    if (e == cudaSuccess) e = launch_dependent(kernel, grid, kScoreThreads, smem, ctas, s, mn, mp, a);
   }
   return finish_call(e, &g_select_err, check_status, s);
 }
