@@ -150,12 +150,15 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                                                                      : 1);
     fence_barrier_init();
   }
+  // (what came before touches no memory of the previous kernel's)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Tensor memory is taken before the next kernel may be scheduled and after
+  // the previous one is done: a CTA that shares the SM with one of theirs can
+  // neither hold what that one waits for nor wait for it.
   if (warp == 0) {
     if (kPair) tmem_alloc_pair(smem_u32(tmem_slot), 2 * kMaxHeads);
     else tmem_alloc(smem_u32(tmem_slot), 2 * kMaxHeads);
   }
-  // (what came before touches no memory of the previous kernel's)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // how many tiles of each size the lists make (32 bits hold a warp's)
   constexpr int kPer = (kScoreRows + kScoreThreads - 1) / kScoreThreads;   // rows of a thread

@@ -217,7 +217,8 @@ def bits(t):
     (1, 128, 1, True, False, 64, True, False), (1, 1, 3, False, True, 16, True, True),
     (7, 3, 2, False, False, 32, False, True), (65, 20, 3, True, True, 64, True, False),
     (300, 16, 1, False, True, 32, True, True), (129, 128, 3, False, False, 16, True, True),
-    (40, 0, 1, True, False, 64, True, True), (33, 130, 1, True, False, 64, False, False)])
+    (40, 0, 1, True, False, 64, True, True), (33, 130, 1, True, False, 64, False, False),
+    (5, 1024, 2, False, True, 32, True, False), (1300, 128, 1, True, False, 64, True, True)])
 def test_append_matches_oracle(T, H, axes, inter, fp8, P, normed, split):
     rng = rng_of(T, H, axes)
     pages, scale, kv_scale = T // P + 4, 1.25, 0.3 if fp8 else 1.0
@@ -393,7 +394,9 @@ def lists_of(rng, counts, num_pages):
 
 @pytest.mark.parametrize("counts, H", [
     ([1], 1), ([5, 0, 130], 16), ([128, 127, 129, 0, 1], 20), ([1000], 128), ([33] * 40, 128), ([300, 2, 77], 7),
-    ([0, 0], 16), ([4, 3, 2, 1] * 100, 8), ([513, 64], 40), ([2100], 16), ([700, 701, 1, 699], 100)])
+    ([0, 0], 16), ([4, 3, 2, 1] * 100, 8), ([513, 64], 40), ([2100], 16), ([700, 701, 1, 699], 100),
+    ([300, 1, 5], 49), ([257, 256, 255, 513], 65), ([40, 0, 90], 97), ([129], 127), ([3, 0, 70] * 230, 48),
+    ([1, 2, 0, 33, 5] * 200, 56)])
 def test_scores_match_oracle(counts, H):
     rng = rng_of(len(counts), sum(counts), H)
     R, num_pages = len(counts), 61
@@ -635,6 +638,85 @@ def test_sparse_decoder_checks():
                 dec.plan(*args, **kw)
     finally:
         dec.close()
+
+
+def test_calls_on_another_stream():
+    """Every operator queued on a stream that is not the current one, while the current one is held up."""
+    side = torch.cuda.Stream()
+    rng = rng_of(41)
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(torch.bfloat16).cuda()  # noqa: E731
+    q, kv, pos, slots = bf(9, 16, 64), bf(9, 576), i32(range(9)), dev(np.arange(7, 16))
+    cc, kc = cache_of(rng, 2, 16, False)
+    summaries = torch.full((2, 576), math.nan, dtype=torch.bfloat16, device="cuda")
+    scores = torch.full((1, 2), math.nan, device="cuda")
+    si, sp, indptr, indices = i32([-1, -1]), i32([-1, -1]), i32([0, 2]), i32([1, 0])
+    qn = bf(1, 16, 512)
+    s = tables_state(rng, [5], 16, 4, spare=2)
+    t = [i32(s["lens"]), i32([3]), dev(s["table"]), dev(s["free"]), i32([2])]
+    o = [i32([-1] * 2), i32([-1] * 4), i32([-1] * 2), dev(np.full(4, -9)), i32([-1] * 4), i32([-1])]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                        # about 0.1 s on the current stream
+    out = mla.mla_rope_append(mla.rope_spec(FREQ), pos, slots, q, kv[:, :512], kv[:, 512:], None, 0.0, cc, kc,
+                              torch.empty_like(q), stream=side)
+    mla.mla_summarize_pages(slots, cc, kc, summaries, stream=side)
+    mla.mla_summarize_pages(dev_on(side, np.array([31])), cc, kc, summaries, stream=side)
+    mla.mla_page_scores(qn, q[:1], summaries, indptr, indices, scores, stream=side)
+    mla.mla_select_pages(scores, indptr, indices, 1, 0, 1, si, sp, stream=side)
+    mla.mla_build_tables(*t[:2], *t[2:5], 16, *o[:5], o[5], stream=side)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        assert not summaries.isnan().any() and not scores.isnan().any()
+        assert si.tolist() == [0, 1] and sp.tolist() == [0, -1] and o[5].tolist() == [0] and t[0].tolist() == [8]
+        ref = O.page_mean(f64(cc[0]), f64(kc[0]))
+        assert np.abs(f64(summaries[0]) - ref).max() < 0.05
+    torch.cuda.synchronize()
+
+
+def dev_on(stream, a):
+    with torch.cuda.stream(stream):
+        return dev(a)
+
+
+def test_sparse_decoder_replays_smaller_plans():
+    """A run captured for three requests replays a later plan of two, and the three again."""
+    rng = rng_of(51)
+    B, H, P, W = 3, 16, 16, 40
+    lens = [300, 17, 620]
+    cc, kc = cache_of(rng, B * W, P, False)
+    summaries = torch.cat([cc.float().mean(1), kc.float().mean(1)], 1).to(torch.bfloat16)
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(torch.bfloat16).cuda()  # noqa: E731
+    qn, qp = bf(B, H, 512), bf(B, H, 64)
+    pages = i32(rng.permutation(B * W))
+    out = torch.zeros((B, H, 512), device="cuda")
+    lse = torch.zeros((B, H), device="cuda")
+    dec, ref = mla.MLASparseDecoder(B, H, W, 9, 1, 1), mla.MLASparseDecoder(B, H, W, 9, 1, 1)
+
+    def indptr_of(n):
+        return np.concatenate([[0], np.cumsum([-(-x // P) for x in n])]).astype(np.int32)
+
+    def expect(n, k):
+        ref.plan(indptr_of(n), pages, n, P, 0.07)
+        return ref.run(qn[:k].contiguous(), qp[:k].contiguous(), cc, kc, summaries, out_dtype=torch.float32)
+
+    try:
+        dec.plan(indptr_of(lens), pages, lens, P, 0.07)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            dec.run(qn, qp, cc, kc, summaries, out, lse)
+        for n in (lens, [639, 5], [16, 640], [0], lens):
+            dec.plan(indptr_of(n), pages, n, P, 0.07)
+            out.fill_(math.nan)
+            g.replay()
+            o, l = expect(n, len(n))
+            assert torch.equal(out[:len(n)], o) and torch.equal(lse[:len(n)], l)
+            assert bool(out[len(n):].isnan().all())              # rows past the batch stay as they were
+        with pytest.raises(mla.MLAError):
+            dec.plan([0], pages, [], P, 0.07)                    # a batch of none, as for MLADecoder
+        dec.check_status()
+    finally:
+        dec.close()
+        ref.close()
 
 
 def test_steps_together_from_a_graph():
