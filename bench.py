@@ -8,7 +8,9 @@ permuted over the pool.  Other modes (``--config``): ragged, long_b1,
 long_b4, fp8, deepseek_mtp2 (two query tokens per request), long_b4_mtp4
 (four query tokens per request of 16 heads, packed into one request's
 rows), deepseek_absorbed (W_UK absorb + decode + W_UV projection),
-deepseek_cascade (shared prefix + own suffix + state merge).
+deepseek_cascade (shared prefix + own suffix + state merge), deepseek_sparse
+(a serving step over long caches: page tables, rope append, page summaries, and
+the decode over the best scoring pages).
 
 Prints one JSON line.  ``value`` is microseconds per batch (device time of
 the timed steps, CUDA events on the launching stream).  The inputs are larger
@@ -579,6 +581,132 @@ def run_absorbed(args) -> None:
     dec.close()
 
 
+SPARSE_BATCH, SPARSE_TOKENS, SPARSE_TOP = 64, 32760, 64
+
+
+def run_sparse(args) -> None:
+    """One serving step over long caches: page tables from the lengths, rope
+    append of the new tokens, summaries of the pages they complete, then the
+    sparse decode (page scores, selection, decode over the selected pages) of
+    64 requests x 32768 tokens, 128 heads, 64 of 512 pages read."""
+    import torch
+    from paged_mla_decode_02_gb300 import build as B
+    from paged_mla_decode_02_gb300 import mla
+    Bq, H, P, top = SPARSE_BATCH, 128, 64, SPARSE_TOP
+    new = 8                                            # tokens of the step, of which the last is decoded
+    pages = (SPARSE_TOKENS + new) // P
+    torch.cuda.set_device(0)
+    B.build()
+    dev = torch.device("cuda", 0)
+    g = torch.Generator(device=dev).manual_seed(0)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=g, device=dev, dtype=torch.bfloat16)
+
+    def ints(*shape, dtype=torch.int32):
+        return torch.zeros(shape, dtype=dtype, device=dev)
+
+    table = torch.randperm(Bq * pages, generator=g, device=dev).to(torch.int32).reshape(Bq, pages)
+    ckv, kpe = randn(Bq * pages, P, 512), randn(Bq * pages, P, 64)
+    summaries = torch.cat([ckv.mean(1, dtype=torch.float32), kpe.mean(1, dtype=torch.float32)], 1).to(torch.bfloat16)
+    kv_len, n_new = ints(Bq) + SPARSE_TOKENS, ints(Bq) + new
+    kv_out, free, count, count_out = ints(Bq), ints(Bq * pages), ints(1), ints(1)
+    indptr, indices, q_indptr = ints(Bq + 1), ints(Bq * pages), ints(Bq + 1)
+    slots, positions, status = ints(Bq * new, dtype=torch.int64), ints(Bq * new), ints(1)
+    weight = torch.ones(512, dtype=torch.bfloat16, device=dev)
+    kv_new, q_nope, q_rope = randn(Bq * new, 576), randn(Bq, H, 512), randn(Bq * new, H, 64)
+    q_pe = torch.empty_like(q_rope)
+    q_last = torch.empty((Bq, H, 64), dtype=torch.bfloat16, device=dev)
+    out = torch.empty((Bq, H, 512), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((Bq, H), dtype=torch.float32, device=dev)
+    rope = mla.rope_spec(10000.0 ** (-np.arange(32) / 32))
+    sm_scale = 1.0 / math.sqrt(192.0)
+    flush = L2Flush(dev)
+    stream = torch.cuda.Stream(device=dev)
+    dec = mla.MLASparseDecoder(Bq, H, pages, top, 1, 2)
+    host_indptr = np.arange(Bq + 1, dtype=np.int32) * pages
+    dec.plan(host_indptr, indices, np.full(Bq, SPARSE_TOKENS + new, np.int32), P, sm_scale, stream=stream)
+
+    def step():
+        mla.mla_build_tables(kv_len, n_new, table, free, count, P, indptr, indices, q_indptr, slots, positions, status,
+                             kv_len_out=kv_out, free_count_out=count_out, stream=stream)
+        mla.mla_rope_append(rope, positions, slots, q_rope, kv_new[:, :512], kv_new[:, 512:], weight, 1e-6, ckv, kpe,
+                            q_pe_out=q_pe, stream=stream)
+        mla.mla_summarize_pages(slots, ckv, kpe, summaries, stream=stream)
+        q_last.copy_(q_pe.view(Bq, new, H, 64)[:, -1])
+        dec.run(q_nope, q_last, ckv, kpe, summaries, out, lse, stream=stream)
+
+    with torch.cuda.stream(stream):
+        for _ in range(args.warmup):
+            flush.zero_()
+            step()
+    stream.synchronize()
+    dec.check_status()
+    assert int(status) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step()
+    ev = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)) for _ in range(args.steps)]
+    clocks = ClockSampler(0)
+    with torch.cuda.stream(stream):
+        for e0, e1 in ev:
+            flush.zero_()
+            e0.record(stream)
+            graph.replay()
+            e1.record(stream)
+    stream.synchronize()
+    clk = clocks.stop()
+    dec.check_status()
+    us = statistics.mean(a.elapsed_time(b) for a, b in ev) * 1000.0
+
+    # end to end: the step's queries and latent rows from pinned host memory in, output and lse back
+    ins = [(t, t.cpu().pin_memory()) for t in (kv_new, q_nope, q_rope)]
+    out_h, lse_h = (torch.empty(t.shape, dtype=t.dtype).pin_memory() for t in (out, lse))
+    e2e = []
+    for i in range(args.steps + 2):
+        flush.zero_()
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        with torch.cuda.stream(stream):
+            for d, h in ins:
+                d.copy_(h, non_blocking=True)
+            step()
+            out_h.copy_(out, non_blocking=True)
+            lse_h.copy_(lse, non_blocking=True)
+        stream.synchronize()
+        if i >= 2:
+            e2e.append((time.perf_counter() - t0) * 1e6)
+
+    tok, rows = Bq * top * P, Bq * H
+    nbytes = (Bq * pages * (1152 + 8) + tok * 1152 + rows * (576 * 2 + 512 * 2 + 4)       # choice and decode
+              + Bq * new * (H * 64 * 4 + 576 * 4 + 24) + Bq * (P * 1152 + 1152))           # append, summaries
+    flops = 2.0 * Bq * pages * 576 * H + float(tok) * H * FLOP_PER_TOKEN_HEAD
+    hbm, bf, _, peak_src = peaks()
+    t_hbm, t_tc = nbytes / (hbm * 1e9) * 1e6, flops / (bf * 1e12) * 1e6
+    bound = "hbm" if t_hbm >= t_tc else "tensor"
+    achieved = nbytes / (us * 1e-6) / 1e9 if bound == "hbm" else flops / (us * 1e-6) / 1e12
+    peak = hbm if bound == "hbm" else bf
+    line = {"metric": METRIC, "value": us, "unit": UNIT, "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+            "ms_per_step": us / 1000.0, "higher_is_better": False, "scaling": "weak", "vs_baseline": None,
+            "dtype": "bf16", "data": "synthetic",
+            "config": {"workload": f"serving step over long caches: {Bq} requests x {SPARSE_TOKENS + new} tokens, {H} "
+                                   f"heads, page {P}, bf16; {new} new tokens each: page tables, rope append, page "
+                                   f"summaries, then decode over the {top} of {pages} pages that score best",
+                       "batch": Bq, "num_heads": H, "page_size": P, "l2": L2_NOTE},
+            "roofline": {"bound": bound, "achieved": achieved, "peak": peak,
+                         "unit": "GB/s" if bound == "hbm" else "TFLOP/s", "frac": achieved / peak, "traffic": None,
+                         "peak_source": peak_src, "kernel": "whole step (seven launches and a copy)",
+                         "algorithmic_bytes": nbytes, "algorithmic_flops": flops,
+                         "roofline_time_us": max(t_hbm, t_tc)},
+            "clocks": clk,
+            "e2e": {"value": statistics.mean(e2e), "unit": UNIT,
+                    "h2d_bytes_per_step": int(sum(h.numel() * h.element_size() for _, h in ins)),
+                    "d2h_bytes_per_step": int(out.numel() * 2 + lse.numel() * 4)},
+            "gpu_launches": (5 + RUN_LAUNCHES[dec.decoder.info()["kernel"]]) * args.steps, "cuda_graph": True}
+    print(json.dumps(line), flush=True)
+    dec.close()
+
+
 def main() -> None:
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -600,6 +728,13 @@ def main() -> None:
                               "the oracle arm is timed on the single-level configs"}))
             return
         run_absorbed(args)
+        return
+    if args.config == "deepseek_sparse":
+        if args.impl == "reference":
+            print(json.dumps({"impl": "reference", "unavailable":
+                              "the oracle arm is timed on the single-level configs"}))
+            return
+        run_sparse(args)
         return
     if args.config == "deepseek_cascade":
         if args.impl == "reference":
