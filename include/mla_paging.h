@@ -118,6 +118,7 @@ typedef struct {
  *   kpe_cache[slots[t]]      = round(scale * rotate(kpe[t]) / kv_scale)
  * computed in fp32 (angles reduced exactly to one turn first) and rounded
  * once to the cache's type; an e4m3 cache saturates at +-448 and keeps NaN.
+ * (The squares are summed in fp32: latent values past about 1e17 overflow it.)
  * A token with slots[t] < 0 is padding: nothing of it is written.  A slot
  * past the cache is reported (MLA_ERR_DEVICE_BOUNDS) and nothing of its token
  * is written either.  No two tokens may have the same slot.

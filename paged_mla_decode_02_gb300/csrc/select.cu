@@ -57,10 +57,13 @@ __device__ __forceinline__ int list_of(const Lists& l, int r, int* first) {
 // - Four warps read the other: a TMEM lane holds one page's products with
 //   all heads, so a thread takes its page's maximum without any exchange.
 // With more than 48 heads the queries would leave room for four panels of the
-// nine of a tile, too few to cover the latency of memory, so a run is shared by a CTA pair
-// (kPair, cta_group::2): a tile's pages are halved between the two CTAs, as
-// are the heads of the queries that each holds, and the even CTA issues MMAs
-// of M = 256 that read both.
+// nine of a tile, too few to cover the latency of memory, so a share is taken
+// by a CTA pair (kPair, cta_group::2): tiles have up to 256 pages, halved
+// between the two CTAs, as are the heads of the queries that each holds, and
+// the even CTA issues MMAs of M = 256 that read both.
+// Measured: 64 rows x 1024 pages x 128 heads, 85 MB, 21.6 us (3.9 TB/s; 6200
+// cycles a tile, the rate of HBM, once the rings have filled); 4 rows x 100
+// pages x 16 heads 6.5 us.
 struct ScoreArgs {
   const char* summaries;
   int num_pages;
@@ -454,6 +457,12 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Rows of scores up to this long take a CTA of 256 threads, longer ones of 1024
+// (256 rows of 1024 pages: 5.5 us against 6.6; 64 rows of 2048: 6.8 against 5.5).
+constexpr int64_t kNarrow = 1024;
+constexpr int kFewLeft = 128;            // pages ranked against each other
+constexpr int kStagedPages = 49152;      // keys that fit a CTA's shared memory
+
 // One CTA per row.  The middle pages are ordered by key, then by position:
 // the composite of a page is its key above its distance from the row's end, so
 // no two are equal and the want-th highest composite, the cut, parts kept from
@@ -468,19 +477,14 @@ __device__ __forceinline__ uint32_t key_of(float s) {
 // from L2 in each pass.  What bounds the kernel is latency -- three dependent
 // reads of memory, two barriers a pass -- and its code: loops stay rolled, as
 // most of their lines run once or twice.
-// Rows of scores up to this long take a CTA of 256 threads, longer ones of 1024
-// (256 rows of 1024 pages: 5.5 us against 6.6; 64 rows of 2048: 6.8 against 5.5).
-constexpr int64_t kNarrow = 1024;
-constexpr int kFewLeft = 128;            // pages ranked against each other
-constexpr int kStagedPages = 49152;      // keys that fit a CTA's shared memory
-
 template <int kThreads, bool kStaged>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kWarps = kThreads / 32, kUnroll = kStaged ? 2 : 8;
   extern __shared__ uint32_t staged[];
-  __shared__ int sums[kWarps], places[kWarps], hist[2][256], digit_of, need_of, left_of, few;
+  __shared__ __align__(16) int hist[2][256];             // read four at a time
+  __shared__ int sums[kWarps], places[kWarps], digit_of, need_of, left_of, few;
   __shared__ uint32_t ors[kWarps], ands[kWarps];
   __shared__ unsigned long long rest[kFewLeft], cut_of;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x;
@@ -666,6 +670,10 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
   auto kernel = pair ? scores_kernel<true> : scores_kernel<false>;
   int sms = 0;
   cudaError_t e = rows > 0 ? current_sms(&sms) : cudaSuccess;
+  // (the same limit in every call: calls may run at once on several threads)
+  if (rows > 0 && e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             pair ? ScoreForm<true>::smem(kMaxHeads, kScoreRows) : ScoreForm<false>::smem(kFewHeads, kScoreRows));
   for (int r0 = 0; r0 < rows && e == cudaSuccess; r0 += kScoreRows) {
     a.rows = rows - r0 < kScoreRows ? rows - r0 : kScoreRows;
     a.lists.indptr = kv_indptr + r0;
@@ -676,11 +684,10 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
         !encode_rows(&mp, static_cast<const char*>(q_pe) + first * kDKpe * 2, q_rows, kDKpe, box))
       return MLA_ERR_CUDA;
     const int smem = pair ? ScoreForm<true>::smem(num_heads, a.rows) : ScoreForm<false>::smem(num_heads, a.rows);
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     // no more CTAs than the lists can have tiles of the smallest size
     const int64_t tiles = n_indices / (kTilePages * ctas / kSizes) + a.rows, most = sms / ctas;
     const int grid = ctas * static_cast<int>(tiles < most ? tiles : most);
-    if (e == cudaSuccess) e = launch_dependent(kernel, grid, kScoreThreads, smem, ctas, s, mn, mp, a);
+    e = launch_dependent(kernel, grid, kScoreThreads, smem, ctas, s, mn, mp, a);
   }
   return finish_call(e, &g_select_err, check_status, s);
 }
@@ -716,8 +723,10 @@ extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stri
   const size_t smem = staged ? (score_stride + threads - 1) / threads * threads * sizeof(uint32_t) : 0;
   cudaError_t e = cudaSuccess;
   auto kernel = !wide ? select_kernel<few, true> : staged ? select_kernel<many, true> : select_kernel<many, false>;
+  // (the same limit in every call: calls may run at once on several threads)
   if (smem > 32 * 1024)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kStagedPages * static_cast<int>(sizeof(uint32_t)));
   if (e == cudaSuccess)
     e = rows == 0 ? cudaMemsetAsync(sel_indptr, 0, sizeof(int32_t), s)
                   : launch_dependent(kernel, rows, threads, smem, 1, s, a);

@@ -318,9 +318,11 @@ extern "C" mla_status_t mla_build_tables(const int32_t* kv_len, const int32_t* n
   a.max_tokens = max_tokens;
   a.status = status;
   const size_t smem = sizeof(int) * (5 * static_cast<size_t>(batch) + 4);
+  // (the same limits in every call: calls may run at once on several threads)
   cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && smem > 48 * 1024 - 1024)
-    e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess && smem > 32 * 1024)
+    e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sizeof(int)) * (5 * kMaxBatch + 4));
   if (e == cudaSuccess)
     e = launch_dependent(tables_kernel, kCtas, kThreads, smem, kCtas, static_cast<cudaStream_t>(stream), a);
   return finish_call(e, nullptr, 0, nullptr);

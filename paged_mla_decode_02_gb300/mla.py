@@ -624,7 +624,7 @@ def mla_page_scores(q_nope, q_pe, summaries, kv_indptr, kv_indices, scores, chec
     _on_device(device, torch.float32, "scores", scores, contiguous=False)
     rows = kv_indptr.numel() - 1
     lead = q_nope.shape[:-1]
-    if len(lead) < 2 or lead[0] != rows or q_nope.shape[-1] != 512 or q_pe.shape != lead + (64,):
+    if len(lead) not in (2, 3) or lead[0] != rows or q_nope.shape[-1] != 512 or q_pe.shape != lead + (64,):
         raise ValueError("q_nope must be [rows, ..., 512] and q_pe [rows, ..., 64], kv_indptr [rows + 1]")
     if summaries.dim() != 2 or summaries.shape[1] != 576:
         raise ValueError("summaries must be [num_pages, 576]")

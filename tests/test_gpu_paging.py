@@ -677,6 +677,50 @@ def dev_on(stream, a):
         return dev(a)
 
 
+def test_calls_at_once_on_several_threads():
+    """Calls of different sizes at the same time from several host threads, each on its own stream: the results of
+    the calls one by one."""
+    import threading
+    rng = rng_of(61)
+    s = torch.from_numpy(rng.standard_normal((900, 576)).astype(np.float32) * 0.3).to(torch.bfloat16).cuda()
+    jobs = []
+    for counts, H, k in (([90, 3], 16, 8), ([3] * 600, 128, 2), ([400], 128, 64), ([12000, 9000], 40, 100)):
+        q = torch.from_numpy(rng.standard_normal((len(counts), H, 576)).astype(np.float32)).to(torch.bfloat16).cuda()
+        indptr, indices = lists_of(rng, counts, 900)
+        jobs.append(dict(qn=q[..., :512].contiguous(), qp=q[..., 512:].contiguous(), indptr=dev(indptr),
+                         indices=dev(indices), k=k, n=len(counts), w=max(counts)))
+
+    def call(j, stream):
+        scores = torch.zeros((j["n"], j["w"]), device="cuda")
+        si, sp = i32([0] * (j["n"] + 1)), i32([0] * (j["n"] * j["k"]))
+        torch.cuda.synchronize()
+        for _ in range(60):
+            mla.mla_page_scores(j["qn"], j["qp"], s, j["indptr"], j["indices"], scores, stream=stream)
+            mla.mla_select_pages(scores, j["indptr"], j["indices"], j["k"], 0, 1, si, sp, stream=stream)
+        return scores, si, sp
+
+    streams = [torch.cuda.Stream() for _ in jobs]
+    alone = [call(j, st) for j, st in zip(jobs, streams)]
+    torch.cuda.synchronize()
+    got, failed = [None] * len(jobs), []
+
+    def work(i):
+        try:
+            got[i] = call(jobs[i], streams[i])
+        except Exception as e:                                # a refused launch, say
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_sparse_decoder_replays_smaller_plans():
     """A run captured for three requests replays a later plan of two, and the three again."""
     rng = rng_of(51)
