@@ -176,15 +176,30 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(t, what: str) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    if t.dtype == torch.float32:
-        return DTYPE_FP32
-    if t.dtype in (torch.float8_e4m3fn, torch.uint8):
-        return DTYPE_FP8_E4M3
-    raise ValueError(f"{what}: unsupported dtype {t.dtype}")
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32,
+                             torch.float8_e4m3fn: DTYPE_FP8_E4M3, torch.uint8: DTYPE_FP8_E4M3})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _on_cuda(names: str, *tensors) -> None:
+    """Each tensor (named in order in ``names``) is a contiguous CUDA tensor."""
+    for t in tensors:
+        if not t.is_cuda or not t.is_contiguous():
+            break
+    else:
+        return
+    for name, t in zip(names.split(), tensors):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
 # ---------------------------------------------------------------------------
@@ -331,17 +346,14 @@ def mla_decode_run(plan, q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale:
                    stream=None, page_size=None) -> None:
     """Run the planned batch on device tensors (see mla_decode.h for layouts)."""
     lib = load_library()
-    for name, t in (("q_nope", q_nope), ("q_pe", q_pe), ("ckv_cache", ckv_cache),
-                    ("kpe_cache", kpe_cache), ("out", out), ("lse", lse)):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    _on_cuda("q_nope q_pe ckv_cache kpe_cache out lse", q_nope, q_pe, ckv_cache, kpe_cache, out, lse)
     _check_layouts(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, page_size)
-    num_pages = int(ckv_cache.shape[0])
-    st = lib.mla_decode_run(plan, _ptr(q_nope), _ptr(q_pe), _dtype_code(q_nope, "q_nope"),
-                            _ptr(ckv_cache), _ptr(kpe_cache), _dtype_code(ckv_cache, "ckv_cache"),
-                            float(kv_scale), num_pages, _ptr(out), _dtype_code(out, "out"),
-                            _ptr(lse), _stream_handle(stream))
-    _check(st, plan, "mla_decode_run")
+    st = lib.mla_decode_run(plan, q_nope.data_ptr(), q_pe.data_ptr(), _dtype_code(q_nope, "q_nope"),
+                            ckv_cache.data_ptr(), kpe_cache.data_ptr(), _dtype_code(ckv_cache, "ckv_cache"),
+                            float(kv_scale), ckv_cache.shape[0], out.data_ptr(), _dtype_code(out, "out"),
+                            lse.data_ptr(), _stream_handle(stream))
+    if st != OK:
+        _check(st, plan, "mla_decode_run")
 
 
 def mla_decode_noalloc(kv_indptr, kv_indices, kv_len, page_size: int, sm_scale: float, q_nope,
@@ -356,10 +368,7 @@ def mla_decode_noalloc(kv_indptr, kv_indices, kv_len, page_size: int, sm_scale: 
     batch = lens.shape[0]
     if indptr.shape[0] != batch + 1:
         raise ValueError("kv_indptr must have batch + 1 entries")
-    for name, t in (("q_nope", q_nope), ("q_pe", q_pe), ("ckv_cache", ckv_cache),
-                    ("kpe_cache", kpe_cache), ("out", out), ("lse", lse)):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    _on_cuda("q_nope q_pe ckv_cache kpe_cache out lse", q_nope, q_pe, ckv_cache, kpe_cache, out, lse)
     if _dtype_code(q_nope, "q_nope") != DTYPE_BF16 or _dtype_code(ckv_cache, "ckv_cache") != DTYPE_BF16:
         raise ValueError("mla_decode_noalloc takes bf16 queries and caches")
     _check_layouts(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, int(page_size))
@@ -792,9 +801,14 @@ class MLASparseDecoder:
         with torch.cuda.stream(stream):
             self._kv_indptr.copy_(torch.from_numpy(whole))
         self._kv_indices, self.batch = kv_indices, batch   # keep the borrowed page list alive
-        # (slices of the decoder's buffers: made here, once, as each costs the host some microseconds)
-        self._lists, self._rows = self._kv_indptr[:batch + 1], self._scores[:batch]
         self.sel_indptr = self._sel_indptr[:batch + 1]   # device offsets of the selected pages, after a run
+        # the arguments of run()'s calls that stay as they are
+        lists = (self._kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(), batch)
+        self._choice = (self._scores.data_ptr(), self.max_pages)
+        self._score_args = lists
+        self._select_args = self._choice + lists + (self.top_k, self.keep_first, self.keep_last,
+                                                    self._sel_indptr.data_ptr(), self.sel_indices.data_ptr(),
+                                                    self.sel_indices.numel(), 0)
 
     def run(self, q_nope, q_pe, ckv_cache, kpe_cache, summaries, out=None, lse=None, kv_scale: float = 1.0,
             out_dtype=None, stream=None):
@@ -802,10 +816,24 @@ class MLASparseDecoder:
         the cache and its page summaries [num_pages, 576]; returns out, lse."""
         if self._kv_indices is None:
             raise MLAError(ERR_NOT_PLANNED, "MLASparseDecoder.run before plan")
-        stream = _stream_handle(stream)
-        mla_page_scores(q_nope, q_pe, summaries, self._lists, self._kv_indices, self._rows, stream=stream)
-        mla_select_pages(self._rows, self._lists, self._kv_indices, self.top_k, self.keep_first, self.keep_last,
-                         self.sel_indptr, self.sel_indices, stream=stream)
+        import torch
+        device = torch.cuda.current_device()
+        _on_device(device, torch.bfloat16, "q_nope q_pe summaries", q_nope, q_pe, summaries)
+        if self._scores.get_device() != device:
+            raise ValueError("the decoder was made on another CUDA device than the current one")
+        q, rows = q_nope.shape, summaries.shape
+        if len(q) not in (3, 4) or q[0] != self.batch or q[-1] != 512 or q_pe.shape != q[:-1] + (64,):
+            raise ValueError("q_nope must be [batch, ..., heads, 512] and q_pe [batch, ..., heads, 64]")
+        if len(rows) != 2 or rows[1] != 576:
+            raise ValueError("summaries must be [num_pages, 576]")
+        lib, stream = load_library(), _stream_handle(stream)
+        heads = q[1] if len(q) == 3 else q[1] * q[2]
+        st = lib.mla_page_scores(q_nope.data_ptr(), q_pe.data_ptr(), summaries.data_ptr(), rows[0], *self._score_args,
+                                 heads, *self._choice, 0, stream)
+        if st == OK:
+            st = lib.mla_select_pages(*self._select_args, stream)
+        if st != OK:
+            _check(st, None, "MLASparseDecoder.run")
         return self.decoder.run(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale, out_dtype, stream)
 
     def check_status(self) -> int:
