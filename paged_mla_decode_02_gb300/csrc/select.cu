@@ -551,12 +551,21 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     for (int side = 0;; side ^= 1) {
       const int shift = max(top - 7, top >= 32 ? 32 : 0);   // a digit lies within the key or the distance
       const uint32_t digits = (2u << (top - shift)) - 1;
+      if (shift >= 32) {   // a digit of the key: 32 bits are enough
+        const uint32_t have = static_cast<uint32_t>(cut >> 32);
 #pragma unroll kUnroll
-      for (int e = 0; e < steps; ++e) {
-        const int p = base + 32 * e;
-        const uint32_t k = key_at(p);
-        const unsigned long long c = composite(k, p);
-        if (k && ((c ^ cut) >> top) < 2) atomicAdd(&hist[side][static_cast<uint32_t>(c >> shift) & digits], 1);
+        for (int e = 0; e < steps; ++e) {
+          const uint32_t k = key_at(base + 32 * e);
+          if (k && ((k ^ have) >> (top - 32)) < 2) atomicAdd(&hist[side][(k >> (shift - 32)) & digits], 1);
+        }
+      } else {
+#pragma unroll kUnroll
+        for (int e = 0; e < steps; ++e) {
+          const int p = base + 32 * e;
+          const uint32_t k = key_at(p);
+          const unsigned long long c = composite(k, p);
+          if (k && ((c ^ cut) >> top) < 2) atomicAdd(&hist[side][static_cast<uint32_t>(c >> shift) & digits], 1);
+        }
       }
       __syncthreads();
       if (warp == 0) {
@@ -627,13 +636,24 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
   __syncthreads();
   int place = __reduce_add_sync(~0u, lane < warp ? places[lane] : 0);
   if (c == 0) return;
-#pragma unroll kUnroll
-  for (int e = 0; e < steps; ++e) {
-    const int p = base + 32 * e;
-    const bool kept = keeps(p);
-    const uint32_t who = __ballot_sync(~0u, kept);
-    if (kept) out[place + __popc(who & ((1u << lane) - 1))] = pages[p];
-    place += __popc(who);
+  constexpr int kBatch = 4;   // page ids read before any is written
+  for (int e0 = 0; e0 < steps; e0 += kBatch) {
+    int id[kBatch];
+    uint32_t kept = 0;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int p = base + 32 * (e0 + j);
+      if (e0 + j < steps && keeps(p)) {
+        kept |= 1u << j;
+        id[j] = pages[p];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint32_t who = __ballot_sync(~0u, kept >> j & 1);
+      if (kept >> j & 1) out[place + __popc(who & ((1u << lane) - 1))] = id[j];
+      place += __popc(who);
+    }
   }
 }
 
