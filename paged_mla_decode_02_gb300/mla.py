@@ -169,10 +169,10 @@ def _ptr(t) -> int:
     return int(t.data_ptr())
 
 
-def _stream_handle(stream) -> int:
+def _stream_handle(stream, device=None) -> int:
     import torch
     if stream is None:   # the handle alone: a Stream object costs the host several times as much
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -530,7 +530,7 @@ def mla_build_tables(kv_len, new_len, block_table, free_pages, free_count, page_
         block_table.shape[1], free_pages.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(),
         free_pages.numel(), batch, int(page_size), kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(),
         q_indptr.data_ptr(), slots.data_ptr(), positions.data_ptr(), slots.numel(), status.data_ptr(),
-        _stream_handle(stream))
+        _stream_handle(stream, device))
     _check(st, None, "mla_build_tables")
 
 
@@ -564,7 +564,10 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
         positions = positions[None]
     _on_device(device, torch.int32, "positions", positions, contiguous=False)
     _on_device(device, torch.int64, "slots", slots)
-    _on_device(device, torch.bfloat16, "ckv kpe", ckv, kpe, contiguous=False)
+    if q_pe is None:
+        _on_device(device, torch.bfloat16, "ckv kpe", ckv, kpe, contiguous=False)
+    else:
+        _on_device(device, torch.bfloat16, "ckv kpe q_pe", ckv, kpe, q_pe, contiguous=False)
     T = slots.numel()
     n_axes = rope.n_axes
     if positions.dim() != 2 or positions.shape[0] < n_axes:
@@ -577,7 +580,6 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
             raise ValueError("norm_weight must have 512 entries")
     H, q_ptr, q_t, q_h, out_ptr = 0, None, 0, 0, None
     if q_pe is not None:
-        _on_device(device, torch.bfloat16, "q_pe", q_pe, contiguous=False)
         if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != 64 or (q_pe.numel() and q_pe.stride(2) != 1):
             raise ValueError("q_pe must be [tokens, heads, 64] with adjacent dims")
         H = q_pe.shape[1]
@@ -596,7 +598,7 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
         q_t, q_h, out_ptr, ckv.data_ptr(), ckv_stride, kpe.data_ptr(), kpe_stride,
         None if norm_weight is None else norm_weight.data_ptr(), eps, ckv_cache.data_ptr(), kpe_cache.data_ptr(),
         code, kv_scale, ckv_cache.shape[0], ckv_cache.shape[1], T, H, int(bool(check_status)),
-        _stream_handle(stream))
+        _stream_handle(stream, device))
     _check(st, None, "mla_rope_append")
     return q_pe_out
 
@@ -615,7 +617,7 @@ def mla_summarize_pages(slots, ckv_cache, kpe_cache, summaries, kv_scale: float 
     st = load_library().mla_summarize_pages(slots.data_ptr(), slots.numel(), ckv_cache.data_ptr(),
                                             kpe_cache.data_ptr(), code, kv_scale, ckv_cache.shape[0],
                                             ckv_cache.shape[1], summaries.data_ptr(), int(bool(check_status)),
-                                            _stream_handle(stream))
+                                            _stream_handle(stream, device))
     _check(st, None, "mla_summarize_pages")
 
 
@@ -644,7 +646,7 @@ def mla_page_scores(q_nope, q_pe, summaries, kv_indptr, kv_indices, scores, chec
     st = load_library().mla_page_scores(q_nope.data_ptr(), q_pe.data_ptr(), summaries.data_ptr(),
                                         summaries.shape[0], kv_indptr.data_ptr(), kv_indices.data_ptr(),
                                         kv_indices.numel(), rows, heads, scores.data_ptr(), stride,
-                                        int(bool(check_status)), _stream_handle(stream))
+                                        int(bool(check_status)), _stream_handle(stream, device))
     _check(st, None, "mla_page_scores")
 
 
@@ -668,7 +670,7 @@ def mla_select_pages(scores, kv_indptr, kv_indices, top_k: int, keep_first: int,
                                          kv_indices.data_ptr(), kv_indices.numel(), rows, int(top_k),
                                          int(keep_first), int(keep_last), sel_indptr.data_ptr(),
                                          sel_indices.data_ptr(), sel_indices.numel(), int(bool(check_status)),
-                                         _stream_handle(stream))
+                                         _stream_handle(stream, device))
     _check(st, None, "mla_select_pages")
 
 
@@ -744,7 +746,9 @@ class MLASparseDecoder:
 
     With q_len query tokens per request (q_len x heads <= 128, batch x q_len <=
     max_batch) the choice is theirs together, and keep_last must cover the
-    pages that hold them."""
+    pages that hold them.
+
+    Its runs share its buffers, as those of a plan do: one at a time."""
 
     def __init__(self, max_batch: int, num_heads: int, max_pages: int, top_k: int, keep_first: int = 1,
                  keep_last: int = 1, kernel="default"):

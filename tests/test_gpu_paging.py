@@ -218,13 +218,13 @@ def bits(t):
     (7, 3, 2, False, False, 32, False, True), (65, 20, 3, True, True, 64, True, False),
     (300, 16, 1, False, True, 32, True, True), (129, 128, 3, False, False, 16, True, True),
     (40, 0, 1, True, False, 64, True, True), (33, 130, 1, True, False, 64, False, False),
-    (5, 1024, 2, False, True, 32, True, False), (1300, 128, 1, True, False, 64, True, True)])
+    (5, 1024, 2, False, True, 32, True, False), (19, 24, 8, False, False, 64, False, True), (1300, 128, 1, True, False, 64, True, True)])
 def test_append_matches_oracle(T, H, axes, inter, fp8, P, normed, split):
     rng = rng_of(T, H, axes)
     pages, scale, kv_scale = T // P + 4, 1.25, 0.3 if fp8 else 1.0
     axis = [i * axes // 32 for i in range(32)] if inter else [i % axes for i in range(32)]
     pos = rng.integers(0, 1 << 20, (axes, T)).astype(np.int32)
-    pos[:, 0] = [2 ** 31 - 1, 0, -5][:axes]
+    pos[:, 0] = [2 ** 31 - 1, 0, -5, -2 ** 31, 1, 2, 3, 4][:axes]
     slots = rng.permutation(pages * P)[:T].astype(np.int64)
     slots[rng.random(T) < 0.2] = -1
     slots[T - 1] = pages * P - 1 if pages * P - 1 not in slots[:-1] else slots[T - 1]
@@ -675,6 +675,40 @@ def test_calls_on_another_stream():
 def dev_on(stream, a):
     with torch.cuda.stream(stream):
         return dev(a)
+
+
+def test_offsets_past_32_bits():
+    """The last slot of a cache of more than 2^31 values, and the last of more than 2^31 summary values."""
+    pages, P = 66000, 64
+    cc = torch.zeros((pages, P, 512), dtype=torch.float8_e4m3fn, device="cuda")
+    kc = torch.zeros((pages, P, 64), dtype=torch.float8_e4m3fn, device="cuda")
+    assert cc.numel() > 2 ** 31
+    kv = torch.full((1, 576), 2.0, dtype=torch.bfloat16, device="cuda")
+    slot = dev(np.array([pages * P - 1], np.int64))
+    mla.mla_rope_append(mla.rope_spec(FREQ), i32([0]), slot, None, kv[:, :512], kv[:, 512:], None, 0.0, cc, kc,
+                        check_status=True)
+    assert bool((cc[-1, -1].float() == 2).all()) and bool((kc[-1, -1].float() == 2).all())
+    assert int(cc.view(torch.int64).count_nonzero()) == 64      # nothing else was written
+    summaries = torch.empty((pages, 576), dtype=torch.bfloat16, device="cuda")
+    mla.mla_summarize_pages(slot, cc, kc, summaries, check_status=True)
+    assert bool((summaries[-1] == 2 / 64).all())
+    del cc, kc
+    many = 2 ** 31 // 576 + 5
+    summaries = torch.empty((many, 576), dtype=torch.bfloat16, device="cuda")
+    summaries[-1], summaries[0] = 3.0, 1.0
+    for H in (16, 128):
+        q = torch.ones((1, H, 576), dtype=torch.bfloat16, device="cuda")
+        scores = torch.zeros((1, 2), device="cuda")
+        mla.mla_page_scores(q[..., :512].contiguous(), q[..., 512:].contiguous(), summaries, i32([0, 2]),
+                            i32([many - 1, 0]), scores, check_status=True)
+        assert scores.tolist() == [[3 * 576.0, 576.0]]
+    # a page table whose rows lie 2^30 entries apart
+    wide = torch.full((3 * 2 ** 30,), -1, dtype=torch.int32, device="cuda")
+    table = wide.view(3, 2 ** 30)[:, :4]
+    o = [i32([-1] * 4), i32([-1] * 12), i32([-1] * 4), dev(np.full(18, -9)), i32([-1] * 18), i32([-1])]
+    mla.mla_build_tables(i32([0, 0, 0]), i32([1, 0, 17]), table, i32([5, 4, 3, 2, 1, 0]), i32([6]), 16, *o)
+    assert o[5].tolist() == [0] and o[0].tolist() == [0, 1, 1, 3] and o[1].tolist()[:3] == [0, 1, 2]
+    assert table[2].tolist() == [1, 2, -1, -1] and table[0].tolist() == [0, -1, -1, -1]
 
 
 def test_calls_at_once_on_several_threads():
