@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   int* at = reinterpret_cast<int*>(after + 16);          // [rows + 1]: tiles before each row
   int* first_of = at + a.rows + 1;                       // [rows]: where its list begins, and its pages
   int* len_of = first_of + a.rows;
-  __shared__ int warp_sum[kScoreThreads / 32];
+  __shared__ int warp_sum[kScoreThreads / 32], dealt[2];
   __shared__ unsigned size_sum[kSizes][kScoreThreads / 32];
   const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
@@ -153,64 +153,84 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                                                                      : 1);
     fence_barrier_init();
   }
+  __syncwarp();
+  if (kPair) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the barriers are there
   // (what came before touches no memory of the previous kernel's)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // Tensor memory is taken before the next kernel may be scheduled and after
-  // the previous one is done: a CTA that shares the SM with one of theirs can
-  // neither hold what that one waits for nor wait for it.
-  if (warp == 0) {
-    if (kPair) tmem_alloc_pair(smem_u32(tmem_slot), 2 * kMaxHeads);
-    else tmem_alloc(smem_u32(tmem_slot), 2 * kMaxHeads);
-  }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // how many tiles of each size the lists make (32 bits hold a warp's)
-  constexpr int kPer = (kScoreRows + kScoreThreads - 1) / kScoreThreads;   // rows of a thread
-  constexpr int kQuarter = kTilePages * F::kCtas / kSizes;
-  const int units = gridDim.x / F::kCtas;
-  unsigned len[kPer], sum[kSizes] = {};
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = tid * kPer + i;
-    int first = 0;
-    len[i] = r < a.rows ? list_of(a.lists, r, &first) : 0;
-    if (r < a.rows) first_of[r] = first;
-#pragma unroll
-    for (int k = 0; k < kSizes; ++k) sum[k] += (len[i] + (k + 1) * kQuarter - 1) / ((k + 1) * kQuarter);
-  }
-#pragma unroll
-  for (int k = 0; k < kSizes; ++k) {
-    sum[k] = __reduce_add_sync(~0u, sum[k]);
-    if (lane == 0) size_sum[k][warp] = sum[k];
-  }
-  __syncthreads();
-  int quarters = kSizes, total = 0;
-  float least = 0.f;
-  bool sound = true;
-#pragma unroll
-  for (int k = kSizes; k > 0; --k) {
-    const unsigned some = lane < kScoreThreads / 32 ? size_sum[k - 1][lane] : 0;
-    // a warp's rows make no more tiles than kv_indices can hold, or their
-    // lists overlap (kv_indptr goes back)
-    sound &= !__any_sync(~0u, some > kMostTiles);
-    const int n = __reduce_add_sync(~0u, some);
-    const float cost = ceilf(static_cast<float>(n) / units) * (k * kQuarter + kTileCost);
-    if (k == kSizes || cost < least) {
-      quarters = k;
-      least = cost;
-      total = n;
+  const int unit = blockIdx.x / F::kCtas, units = gridDim.x / F::kCtas;
+  int total = 0, tile = kTilePages * F::kCtas;
+  if (warp >= 2 && warp < 6) {
+    // Tensor memory is taken before the next kernel may be scheduled and after
+    // the previous one is done: a CTA that shares the SM with one of theirs
+    // can neither hold what that one waits for nor wait for it.
+    if (warp == 5) {
+      if (kPair) tmem_alloc_pair(smem_u32(tmem_slot), 2 * kMaxHeads);
+      else tmem_alloc(smem_u32(tmem_slot), 2 * kMaxHeads);
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
-  }
-  const int tile = quarters * kQuarter;
-  auto tiles_of = [&](unsigned pages) -> int {   // of a list
-    const unsigned t = (pages + kQuarter - 1) / kQuarter;
-    return quarters == 1 ? t : quarters == 2 ? (t + 1) >> 1 : quarters == 3 ? (t + 2) / 3 : (t + 3) >> 2;
-  };
-  if (!sound) {
-    if (tid == 0) report_error(&g_select_err, kErrBounds);
-    total = 0;
-  }
-  // tiles before each row
-  {
+    // Meanwhile the rows of the first tile start on their way to L2, if the
+    // lists lie end to end and are tiles of full size; where that is a little
+    // off, another CTA reads what comes.
+    const int64_t base0 = a.lists.indptr[0], line = a.lists.indptr[a.rows] - base0;
+    if (base0 >= 0 && line >= units * (tile / 2)) {
+      const int tiles = static_cast<int>((line + tile - 1) / tile), each = tiles / units;
+      const int64_t p = static_cast<int64_t>(unit * each + min(unit, tiles % units)) * tile + rank * kTilePages + tid - 64;
+      if (p < line && base0 + p < a.lists.n_indices) {
+        const int id = a.lists.indices[base0 + p];
+        if (id >= 0 && id < a.num_pages) {
+          const char* row = a.summaries + static_cast<int64_t>(id) * (2 * kD);
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 128 * k));
+        }
+      }
+    }
+  } else {
+    // The other warps: how many tiles of each size the lists make (32 bits
+    // hold a warp's), the size to take, and the tiles before each row.
+    constexpr int kWarps = kScoreThreads / 32 - 4, kPer = kScoreRows / (32 * kWarps);   // kPer: rows of a thread
+    static_assert(kPer * 32 * kWarps == kScoreRows, "every row has a thread");
+    constexpr int kQuarter = kTilePages * F::kCtas / kSizes;
+    const int w = warp < 2 ? warp : warp - 4, r0 = (32 * w + lane) * kPer;
+    unsigned len[kPer], sum[kSizes] = {};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = r0 + i;
+      int first = 0;
+      len[i] = r < a.rows ? list_of(a.lists, r, &first) : 0;
+      if (r < a.rows) {
+        first_of[r] = first;
+        len_of[r] = len[i];
+      }
+#pragma unroll
+      for (int k = 0; k < kSizes; ++k) sum[k] += (len[i] + (k + 1) * kQuarter - 1) / ((k + 1) * kQuarter);
+    }
+#pragma unroll
+    for (int k = 0; k < kSizes; ++k) {
+      sum[k] = __reduce_add_sync(~0u, sum[k]);
+      if (lane == 0) size_sum[k][w] = sum[k];
+    }
+    named_bar_sync(1, 32 * kWarps);
+    int quarters = kSizes, all = 0;
+    float least = 0.f;
+    bool sound = true;
+#pragma unroll
+    for (int k = kSizes; k > 0; --k) {
+      const unsigned some = lane < kWarps ? size_sum[k - 1][lane] : 0;
+      // a warp's rows make no more tiles than kv_indices can hold, or their
+      // lists overlap (kv_indptr goes back)
+      sound &= !__any_sync(~0u, some > kMostTiles);
+      const int n = __reduce_add_sync(~0u, some);
+      const float cost = ceilf(static_cast<float>(n) / units) * (k * kQuarter + kTileCost);
+      if (k == kSizes || cost < least) {
+        quarters = k;
+        least = cost;
+        all = n;
+      }
+    }
+    auto tiles_of = [&](unsigned pages) -> int {   // of a list
+      const unsigned t = (pages + kQuarter - 1) / kQuarter;
+      return quarters == 1 ? t : quarters == 2 ? (t + 1) >> 1 : quarters == 3 ? (t + 2) / 3 : (t + 3) >> 2;
+    };
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) mine += tiles_of(len[i]);
@@ -220,25 +240,29 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int o = __shfl_up_sync(~0u, incl, d);
       if (lane >= d) incl += o;
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int before = incl - mine + __reduce_add_sync(~0u, lane < warp ? warp_sum[lane] : 0);
-    if (tid == 0) at[0] = 0;
+    if (lane == 31) warp_sum[w] = incl;
+    named_bar_sync(1, 32 * kWarps);
+    int before = incl - mine + __reduce_add_sync(~0u, lane < w ? warp_sum[lane] : 0);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       before += tiles_of(len[i]);
-      if (tid * kPer + i < a.rows) at[tid * kPer + i + 1] = before;
+      if (r0 + i < a.rows) at[r0 + i + 1] = before;
     }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (tid * kPer + i < a.rows) len_of[tid * kPer + i] = len[i];
+    if (w == 0 && lane == 0) {
+      at[0] = 0;
+      dealt[0] = sound ? all : 0;
+      dealt[1] = quarters * kQuarter;
+      if (!sound) report_error(&g_select_err, kErrBounds);
+    }
   }
   tc_fence_before();
-  if (kPair) cluster_sync_all(); else __syncthreads();   // (a pair: both CTAs' barriers are there)
+  __syncthreads();
+  if (kPair) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  total = dealt[0];   // tiles, and their size in pages
+  tile = dealt[1];
   // this CTA's (pair's) share of them
-  const int unit = blockIdx.x / F::kCtas;
   const int each = total / units, more = total % units;
   const int begin = unit * each + min(unit, more), end = begin + each + (unit < more);
   int pos = begin, row = 0;
@@ -418,7 +442,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   }
   tc_fence_before();
   if (kPair) cluster_sync_all(); else __syncthreads();   // (a pair: neither reads the other's memory any more)
-  if (warp == 0) {
+  if (warp == 5) {
     tc_fence_after();
     if (kPair) tmem_dealloc_pair(tmem, 2 * kMaxHeads);
     else tmem_dealloc(tmem, 2 * kMaxHeads);
