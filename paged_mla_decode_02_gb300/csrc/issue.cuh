@@ -65,21 +65,19 @@ __device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
       "}\n" ::"r"(bar)
       : "memory");
 }
-// Announce `bytes` on the mbarrier and load the box at {x, y}.
-__device__ __forceinline__ void tma_load_2d_elect(uint32_t dst, const void* tmap, int32_t x, int32_t y, uint32_t bar,
-                                                  uint32_t bytes) {
+// Load the 3-D box at {x, y, z}, completing on the mbarrier.
+__device__ __forceinline__ void tma_load_3d_elect(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
+                                                  uint32_t bar) {
   asm volatile(
       "{\n"
       ".reg .pred q;\n"
       "elect.sync _|q, 0xffffffff;\n"
-      "@q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%4], %5;\n"
-      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];\n"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n"
       "}\n" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(bar), "r"(bytes)
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-
 // The same over a CTA pair (cta_group::2), issued in its even CTA.
 __device__ __forceinline__ void mma_pair_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
@@ -105,17 +103,17 @@ __device__ __forceinline__ void commit_pair_elect(uint32_t bar, int ctas) {
       "h"(static_cast<uint16_t>(ctas))
       : "memory");
 }
-// Load the box at {x, y}, completing on an mbarrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair_elect(uint32_t dst, const void* tmap, int32_t x, int32_t y,
+// Load the 3-D box at {x, y, z}, completing on an mbarrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_3d_pair_elect(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
                                                        uint32_t cluster_bar) {
   asm volatile(
       "{\n"
       ".reg .pred q;\n"
       "elect.sync _|q, 0xffffffff;\n"
-      "@q cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3}], [%4];\n"
+      "@q cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n"
       "}\n" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(cluster_bar)
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
       : "memory");
 }
 

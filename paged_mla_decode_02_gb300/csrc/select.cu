@@ -48,8 +48,8 @@ __device__ __forceinline__ int list_of(const Lists& l, int r, int* first) {
 // in order.  (Few or short lists make smaller tiles, so that all SMs take
 // part: the size, of four, with the least estimated time of the fullest CTA.)
 // - One warp copies a row's queries into shared memory by TMA, in nine panels
-//   of 64 dims that stay for all tiles of the row (and make way one by one for
-//   the next row's).
+//   of 64 dims that stay for all tiles of the row (and make way, four by four,
+//   for the next row's).
 // - Two sets of four warps copy the pages' rows, a 64-dim chunk at a time,
 //   through a ring of panels with cp.async.  (As tile::gather4 copies the TMA
 //   took 90 cycles for four 128-byte rows, half the speed.)
@@ -78,6 +78,7 @@ constexpr int kCopyWarps = 4;           // of each of two sets that take turns
 constexpr int kTilePages = 128;         // the MMA's M
 constexpr int kChunks = kD / 64;        // panels of 64 dims
 constexpr int kPanelBytes = kTilePages * 128;
+constexpr int kQPanels = 4, kQGroups = (kChunks + kQPanels - 1) / kQPanels;   // panels of queries copied at once
 constexpr int kSizes = 4;               // tile sizes to choose from: quarters of the largest
 constexpr unsigned kMostTiles = (1u << 26) + 1024;   // 2^31 pages of kv_indices in tiles of 32, and a part for each row
 constexpr int kTileCost = 48;           // what a tile costs beyond its pages, in pages
@@ -87,7 +88,7 @@ template <bool kPair>
 struct ScoreForm {
   static constexpr int kCtas = kPair ? 2 : 1, kStages = kChunks;   // panels of the ring: a tile's
   // full (pages, queries) and accumulator-free barriers count in the even CTA
-  enum { kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + kChunks, kTFull = kQEmpty + kChunks,
+  enum { kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + kQGroups, kTFull = kQEmpty + kQGroups,
          kTEmpty = kTFull + 2, kFinal = kTEmpty + 2, kBars };
   // heads that a CTA holds (the MMA's N over the CTAs, each a multiple of 16)
   __host__ __device__ static constexpr int heads_held(int heads) {
@@ -297,18 +298,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     while (ok && __any_sync(~0u, next(t))) {
       if (!__any_sync(~0u, t.enters)) continue;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        ok &= spin(F::kQEmpty + c, (visit & 1) ^ 1);
-        const bool pe = c == kChunks - 1;
-        const void* map = pe ? &map_qp : &map_qn;
-        const int x = pe ? 0 : 64 * c, y = t.row * a.heads + rank * held, full = F::kQFull + c;
-        if (kPair) {
-          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(full), 2 * q_panel);
-          __syncwarp();
-          tma_load_2d_pair_elect(q_base + c * q_panel, map, x, y, map_to_rank(bar(full), 0));
-        } else {
-          tma_load_2d_elect(q_base + c * q_panel, map, x, y, bar(full), a.heads * 128);
-        }
+      for (int g = 0; g < kQGroups; ++g) {
+        ok &= spin(F::kQEmpty + g, (visit & 1) ^ 1);
+        const int y = t.row * a.heads + rank * held, full = F::kQFull + g;
+        const int bytes = (g < kQGroups - 1 ? kQPanels : 1) * q_panel * F::kCtas;
+        const void* map = g < kQGroups - 1 ? &map_qn : &map_qp;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
+        __syncwarp();
+        const uint32_t dst = q_base + g * kQPanels * q_panel;
+        const int z = g < kQGroups - 1 ? g * kQPanels : 0;
+        if (kPair) tma_load_3d_pair_elect(dst, map, 0, y, z, map_to_rank(bar(full), 0));
+        else tma_load_3d_elect(dst, map, 0, y, z, bar(full));
       }
       ok = __all_sync(~0u, ok);
       ++visit;
@@ -316,8 +316,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
     if (rank == 0 && lane == 0) {   // every copy issued has landed before the CTA leaves
 #pragma unroll 1
-      for (int c = 0; c < kChunks && visit > 0; ++c) {
-        const uint32_t b = bar(F::kQFull + c), parity = (visit - 1) & 1;
+      for (int g = 0; g < kQGroups && visit > 0; ++g) {
+        const uint32_t b = bar(F::kQFull + g), parity = (visit - 1) & 1;
         if (kPair) mbar_wait_cl_drain(b, parity); else mbar_wait_drain(b, parity);
       }
     }
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       ok &= spin(F::kTEmpty + acc, ((n >> 1) & 1) ^ 1);
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {   // panel c of the ring holds chunk c of every tile
-        if (enters) ok &= spin(F::kQFull + c, visit & 1);
+        if (enters && c % kQPanels == 0) ok &= spin(F::kQFull + c / kQPanels, visit & 1);
         ok &= spin(F::kFull + c, n & 1);
         tc_fence_after();
         const uint64_t da = smem_desc(base + c * kPanelBytes, 16, 1024, kSw128);
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           else mma_ss_elect(tmem + acc * kMaxHeads, da + 2 * kk, dq + 2 * kk, idesc, (c | kk) != 0);
         }
         commit(F::kEmpty + c);
-        if (leaves) commit(F::kQEmpty + c);
+        if (leaves && (c % kQPanels == kQPanels - 1 || c == kChunks - 1)) commit(F::kQEmpty + c / kQPanels);
       }
       commit(F::kTFull + acc);
       ok = __all_sync(~0u, ok);
@@ -449,15 +449,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   }
 }
 
-// Row-major [rows, cols] bf16, box box_rows x 64 elements, 128-byte swizzle.
-bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows) {
+// Row-major [rows, 64 panels] bf16 as (dim of a panel, row, panel): a box of
+// some rows and panels lands panel by panel, each in rows of 128 bytes with the
+// 128-byte swizzle.
+bool encode_panels(CUtensorMap* m, const void* base, int64_t rows, int panels, int box_rows, int box_panels) {
   EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(panels)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(panels) * 128, 128};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_panels)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -708,7 +710,8 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // one CTA to a run of pages with few heads, else a pair
   const bool pair = num_heads > kFewHeads;
-  const int ctas = pair ? 2 : 1, box = pair ? ScoreForm<true>::heads_held(num_heads) : num_heads;
+  const int ctas = pair ? 2 : 1;
+  const int held = pair ? ScoreForm<true>::heads_held(num_heads) : ScoreForm<false>::heads_held(num_heads);
   static_assert(ScoreForm<false>::smem(kFewHeads, kScoreRows) <= 227 * 1024 - 128 &&
                 ScoreForm<true>::smem(kMaxHeads, kScoreRows) <= 227 * 1024 - 128, "shared memory of a CTA");
   auto kernel = pair ? scores_kernel<true> : scores_kernel<false>;
@@ -724,8 +727,8 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
     a.scores = scores + r0 * score_stride;
     const int64_t first = static_cast<int64_t>(r0) * num_heads, q_rows = static_cast<int64_t>(a.rows) * num_heads;
     CUtensorMap mn, mp;
-    if (!encode_rows(&mn, static_cast<const char*>(q_nope) + first * kDCkv * 2, q_rows, kDCkv, box) ||
-        !encode_rows(&mp, static_cast<const char*>(q_pe) + first * kDKpe * 2, q_rows, kDKpe, box))
+    if (!encode_panels(&mn, static_cast<const char*>(q_nope) + first * kDCkv * 2, q_rows, kDCkv / 64, held, kQPanels) ||
+        !encode_panels(&mp, static_cast<const char*>(q_pe) + first * kDKpe * 2, q_rows, 1, held, 1))
       return MLA_ERR_CUDA;
     const int smem = pair ? ScoreForm<true>::smem(num_heads, a.rows) : ScoreForm<false>::smem(num_heads, a.rows);
     // no more CTAs than the lists can have tiles of the smallest size
