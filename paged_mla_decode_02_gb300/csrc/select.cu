@@ -328,9 +328,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     // copies 16-byte column i % 8 of rows i / 8 + 16 j.
     const int set = (warp - 6) / kCopyWarps, i = (tid - 6 * 32) % (32 * kCopyWarps), col = i & 7, row0 = i >> 3;
     const uint32_t dst = base + row0 * 128 + ((col ^ (row0 & 7)) << 4);
-    auto row_of = [&](const Tile& x, int p) {   // page p of the tile (a wrong id reads page 0; scored -inf below)
-      const int id = a.lists.indices[first_of[x.row] + x.page0 + (p < x.pages ? p : x.pages ? x.pages - 1 : 0)];
-      return a.summaries + static_cast<int64_t>(id < 0 || id >= a.num_pages ? 0 : id) * (2 * kD);
+    // the ids of a tile's pages that this thread copies (a wrong one reads page
+    // 0; scored -inf below)
+    int ids[8];
+    auto read_ids = [&](const Tile& x) {
+      const int32_t* list = a.lists.indices + first_of[x.row] + x.page0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ids[j] = list[max(0, min(row0 + 16 * j, x.pages - 1))];
     };
     int turn = set, slot = set % kStages, phase = 1;        // the set's next chunk: its number, slot and phase
     int landing = set % kStages, pending = 0, first = 0;    // first: number of the tile's first chunk
@@ -342,11 +346,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (landing >= kStages) landing -= kStages;
       --pending;
     };
-    while (ok && next(t)) {
+    bool more = next(t);
+    if (more) read_ids(t);
+    while (ok && more) {
       const char* src[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) src[j] = row_of(t, row0 + 16 * j) + 16 * col + 128 * (turn - first);
+      for (int j = 0; j < 8; ++j) {
+        const int64_t id = ids[j] < 0 || ids[j] >= a.num_pages ? 0 : ids[j];
+        src[j] = a.summaries + id * (2 * kD) + 16 * col + 128 * (turn - first);
+      }
       const int rows16 = (t.pages + 15) >> 4;
+      if ((more = next(t))) read_ids(t);   // the next tile's are on their way meanwhile
 #pragma unroll 1
       for (; turn < first + kChunks; turn += 2) {
         if (!(ok = wait(F::kEmpty + slot, phase))) break;
