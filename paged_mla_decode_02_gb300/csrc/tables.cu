@@ -204,10 +204,11 @@ __global__ void __launch_bounds__(kThreads, 1) tables_kernel(const TablesArgs a)
   };
   bool bad = false;
 
-  // page lists: each warp a run of whole 32-entry rows of the flat list
+  // page lists: each warp a run of whole 32-entry rows of the flat list (a list
+  // may end so near 2^31 entries that a step past its end does not fit an int)
   {
     constexpr int kWarps = kAll / 32;
-    const long long run = ((total.pages + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const long long run = ((total.pages + kWarps - 1ll) / kWarps + 31) / 32 * 32;
     const long long lo = gwarp * run;
     const int e1 = static_cast<int>(lo + run < total.pages ? lo + run : total.pages);
     int e = static_cast<int>(lo < total.pages ? lo : total.pages);
@@ -216,8 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1) tables_kernel(const TablesArgs a)
         const int base = page_at[b], end = page_at[b + 1] < e1 ? page_at[b + 1] : e1;
         const int old = page_at[b + 1] - base - (fresh_at[b + 1] - fresh_at[b]);
         int32_t* row = a.block_table + b * a.table_stride;
-        int i = e + lane;
-        for (; i - lane + 128 <= min(end, base + old); i += 128) {   // four reads in flight
+        unsigned i = static_cast<unsigned>(e) + lane;
+        const unsigned known = min(end, base + old);
+        for (; i - lane + 128 <= known; i += 128) {   // four reads in flight
           int page[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) page[k] = row[i - base + 32 * k];
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) tables_kernel(const TablesArgs a)
             a.kv_indices[i + 32 * k] = page[k];
           }
         }
-        for (; i < end; i += 32) {
+        for (; i < static_cast<unsigned>(end); i += 32) {
           const int col = i - base;
           int page;
           if (col < old) {

@@ -160,6 +160,27 @@ def test_tables_report_bad_page_ids():
     assert got["status"][0] == mla.ERR_DEVICE_BOUNDS and np.all(got["slots"][12:] == -1)
 
 
+def test_tables_of_lists_near_the_largest():
+    """16 requests of 2^27 - 1 pages: a page list that ends 16 entries below 2^31,
+    the last page of it met by a new token."""
+    B, P, most = 16, 16, 2 ** 27 - 1
+    n = B * most
+    table = torch.arange(n, dtype=torch.int32, device="cuda").bitwise_and_(7).view(B, most)
+    kv_len = np.full(B, most * P, np.int32)
+    kv_len[-1] -= 1
+    new = np.zeros(B, np.int32)
+    new[-1] = 1
+    indices = torch.full((n + 64,), -3, dtype=torch.int32, device="cuda")
+    free, count, status = i32(np.zeros(8)), i32([0]), i32([-3])
+    indptr, q, lens = i32(np.full(B + 1, -3)), i32(np.full(B + 1, -3)), i32(kv_len)
+    slots, positions = torch.full((1,), -3, dtype=torch.int64, device="cuda"), i32([-3])
+    mla.mla_build_tables(lens, i32(new), table, free, count, P, indptr, indices, q, slots, positions, status)
+    assert status.item() == 0 and torch.equal(indptr.long().cpu(), torch.arange(B + 1) * most)
+    assert torch.equal(indices[:n].view(B, most), table) and bool((indices[n:] == -3).all())
+    assert lens.tolist() == [most * P] * B and positions.item() == most * P - 1
+    assert slots.item() == table[-1, -1].item() * P + P - 1
+
+
 def test_tables_replayed_steps():
     """Decode steps in place from one captured graph, against the oracle step by step."""
     rng = rng_of(9)
