@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kQThreads, 4) append_kernel(const __grid_const
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x >= a.kv_blocks) {
     // ---------------- queries ----------------
-    __shared__ float2 turns[kMostTokens][kPairs];
+    __shared__ __align__(16) float2 turns[kMostTokens][kPairs];   // read two at a time
     __shared__ bool real[kMostTokens];
     const int64_t t0 = (blockIdx.x - a.kv_blocks) * a.tokens_per_block;
     const int n = static_cast<int>(a.tokens - t0 < a.tokens_per_block ? a.tokens - t0 : a.tokens_per_block);
