@@ -808,6 +808,7 @@ class MLASparseDecoder:
         self.sel_indptr = self._sel_indptr[:batch + 1]   # device offsets of the selected pages, after a run
         # the arguments of run()'s calls that stay as they are
         lists = (self._kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(), batch)
+        self._heads = self.decoder.num_heads * max(q_len, 1)
         self._choice = (self._scores.data_ptr(), self.max_pages)
         self._score_args = lists
         self._select_args = self._choice + lists + (self.top_k, self.keep_first, self.keep_last,
@@ -830,8 +831,10 @@ class MLASparseDecoder:
             raise ValueError("q_nope must be [batch, ..., heads, 512] and q_pe [batch, ..., heads, 64]")
         if len(rows) != 2 or rows[1] != 576:
             raise ValueError("summaries must be [num_pages, 576]")
-        lib, stream = load_library(), _stream_handle(stream)
         heads = q[1] if len(q) == 3 else q[1] * q[2]
+        if heads != self._heads:   # the decode reads as many rows as were planned
+            raise ValueError(f"q_nope must have {self._heads} query rows (tokens x heads) per request, got {heads}")
+        lib, stream = load_library(), _stream_handle(stream)
         st = lib.mla_page_scores(q_nope.data_ptr(), q_pe.data_ptr(), summaries.data_ptr(), rows[0], *self._score_args,
                                  heads, *self._choice, 0, stream)
         if st == OK:

@@ -661,6 +661,23 @@ def test_sparse_decoder_checks():
         dec.close()
 
 
+def test_sparse_decoder_refuses_another_head_count():
+    """The decode would read the planned heads of every request, past the queries."""
+    dec = mla.MLASparseDecoder(2, 16, 4, 3, 1, 1)
+    try:
+        cache = torch.zeros((8, 16, 576), dtype=torch.bfloat16, device="cuda")
+        cache = cache[..., :512].contiguous(), cache[..., 512:].contiguous()
+        s = torch.zeros((8, 576), dtype=torch.bfloat16, device="cuda")
+        for q_len, shapes in ((0, [(1, 8), (1, 32), (1, 2, 16)]), (2, [(1, 16), (1, 1, 16), (1, 2, 8)])):
+            dec.plan([0, 2], i32(range(2)), [20], 16, 0.1, q_len=q_len)
+            for lead in shapes:
+                q = torch.zeros(lead + (576,), dtype=torch.bfloat16, device="cuda")
+                with pytest.raises(ValueError):
+                    dec.run(q[..., :512].contiguous(), q[..., 512:].contiguous(), *cache, s)
+    finally:
+        dec.close()
+
+
 def test_calls_on_another_stream():
     """Every operator queued on a stream that is not the current one, while the current one is held up."""
     side = torch.cuda.Stream()
