@@ -663,7 +663,7 @@ def test_sparse_decoder_checks():
 
 def test_sparse_decoder_refuses_another_head_count():
     """The decode would read the planned heads of every request, past the queries."""
-    dec = mla.MLASparseDecoder(2, 16, 4, 3, 1, 1)
+    dec = mla.MLASparseDecoder(2, 16, 4, 3, 1, 2)
     try:
         cache = torch.zeros((8, 16, 576), dtype=torch.bfloat16, device="cuda")
         cache = cache[..., :512].contiguous(), cache[..., 512:].contiguous()
