@@ -182,25 +182,27 @@ mla_status_t mla_summarize_pages(const int64_t* slots, int64_t tokens, const voi
  *              are rows of one: num_heads = tokens x heads.
  *   summaries  [num_pages, 576] bf16
  *   kv_indptr  [rows + 1] int32 and kv_indices [n_indices] int32, DEVICE
- *   scores     [rows, score_stride] fp32; entries past a row's list are left
- *              as they were
+ *   scores     fp32, max_pages entries of a row, rows score_stride apart;
+ *              entries past a row's list are left as they were
  * num_heads 1 .. 128; q_nope, q_pe and summaries 16-byte aligned.  A page id
  * outside [0, num_pages) scores -inf and is reported; a row whose list leaves
- * kv_indices or is longer than score_stride (or 2^30 pages) is reported and
+ * kv_indices or is longer than max_pages (or 2^30 pages) is reported and
  * skipped.
- * rows <= 4096 (else MLA_ERR_CAPACITY).
+ * 0 <= max_pages <= score_stride (else MLA_ERR_INVALID_ARG); rows <= 4096 (else
+ * MLA_ERR_CAPACITY).
  */
 mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, const void* summaries,
                              int num_pages, const int32_t* kv_indptr, const int32_t* kv_indices,
                              int64_t n_indices, int rows, int num_heads, float* scores,
-                             int64_t score_stride, int check_status, void* stream);
+                             int64_t score_stride, int64_t max_pages, int check_status,
+                             void* stream);
 
 /*
  * The page lists of a sparse decode: of the n pages of row r, the first
  * keep_first, the last keep_last and the highest scoring of the others, in
  * all min(top_k, n), in their order.  Equal scores go to the lower position;
  * NaN counts as -inf; the scores of the kept ends are not looked at.
- *   scores, score_stride, kv_indptr, kv_indices, n_indices  as above
+ *   scores, score_stride, max_pages, kv_indptr, kv_indices, n_indices  as above
  *   sel_indptr   [rows + 1] int32: offsets of each row's pages
  *   sel_indices  [sel_cap] int32: page ids, sel_cap >= rows * top_k; what lies
  *                past sel_indptr[rows] is left as it was
@@ -209,10 +211,10 @@ mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, const void* s
  * kv_len that mla_decode_plan takes with sel_indptr and sel_indices.
  * top_k >= 1, keep_first >= 0, keep_last >= 1 and keep_first + keep_last <=
  * top_k (else MLA_ERR_INVALID_ARG).  A row whose list leaves kv_indices or is
- * longer than score_stride is reported and counts as empty.  rows <= 4096,
+ * longer than max_pages is reported and counts as empty.  rows <= 4096,
  * rows * top_k <= 2^31 - 1 and sel_cap as above (else MLA_ERR_CAPACITY).
  */
-mla_status_t mla_select_pages(const float* scores, int64_t score_stride,
+mla_status_t mla_select_pages(const float* scores, int64_t score_stride, int64_t max_pages,
                               const int32_t* kv_indptr, const int32_t* kv_indices,
                               int64_t n_indices, int rows, int top_k, int keep_first,
                               int keep_last, int32_t* sel_indptr, int32_t* sel_indices,

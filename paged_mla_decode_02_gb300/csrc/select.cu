@@ -701,18 +701,19 @@ using namespace mla;
 extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, const void* summaries, int num_pages,
                                         const int32_t* kv_indptr, const int32_t* kv_indices, int64_t n_indices,
                                         int rows, int num_heads, float* scores, int64_t score_stride,
-                                        int check_status, void* stream) {
-  if (rows < 0 || num_heads < 1 || num_heads > kMaxHeads || num_pages < 1 || n_indices < 0 || score_stride < 0)
+                                        int64_t max_pages, int check_status, void* stream) {
+  if (rows < 0 || num_heads < 1 || num_heads > kMaxHeads || num_pages < 1 || n_indices < 0 || max_pages < 0 ||
+      score_stride < max_pages)
     return MLA_ERR_INVALID_ARG;
   if (rows > kMaxRows) return MLA_ERR_CAPACITY;
   if (rows > 0 && (!q_nope || !q_pe || !summaries || !kv_indptr || (n_indices > 0 && !kv_indices) ||
-                   (score_stride > 0 && !scores)))
+                   (max_pages > 0 && !scores)))
     return MLA_ERR_INVALID_ARG;
   if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(summaries)) return MLA_ERR_INVALID_ARG;
   ScoreArgs a{};
   a.summaries = static_cast<const char*>(summaries);
   a.num_pages = num_pages;
-  a.lists = {kv_indptr, kv_indices, n_indices, score_stride < kMaxList ? score_stride : kMaxList};
+  a.lists = {kv_indptr, kv_indices, n_indices, max_pages < kMaxList ? max_pages : kMaxList};
   a.rows = rows;
   a.heads = num_heads;
   a.scores = scores;
@@ -749,23 +750,23 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
   return finish_call(e, &g_select_err, check_status, s);
 }
 
-extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stride, const int32_t* kv_indptr,
-                                         const int32_t* kv_indices, int64_t n_indices, int rows, int top_k,
-                                         int keep_first, int keep_last, int32_t* sel_indptr, int32_t* sel_indices,
-                                         int64_t sel_cap, int check_status, void* stream) {
-  if (rows < 0 || n_indices < 0 || score_stride < 0 || sel_cap < 0) return MLA_ERR_INVALID_ARG;
+extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stride, int64_t max_pages,
+                                         const int32_t* kv_indptr, const int32_t* kv_indices, int64_t n_indices,
+                                         int rows, int top_k, int keep_first, int keep_last, int32_t* sel_indptr,
+                                         int32_t* sel_indices, int64_t sel_cap, int check_status, void* stream) {
+  if (rows < 0 || n_indices < 0 || max_pages < 0 || score_stride < max_pages || sel_cap < 0) return MLA_ERR_INVALID_ARG;
   if (top_k < 1 || keep_first < 0 || keep_last < 1 || static_cast<int64_t>(keep_first) + keep_last > top_k)
     return MLA_ERR_INVALID_ARG;
   if (rows > kMaxRows || static_cast<int64_t>(rows) * top_k > INT32_MAX ||
       static_cast<int64_t>(rows) * top_k > sel_cap)
     return MLA_ERR_CAPACITY;
   if (!sel_indptr || (rows > 0 && (!kv_indptr || !sel_indices || (n_indices > 0 && !kv_indices) ||
-                                   (score_stride > 0 && !scores))))
+                                   (max_pages > 0 && !scores))))
     return MLA_ERR_INVALID_ARG;
   SelectArgs a{};
   a.scores = scores;
   a.stride = score_stride;
-  a.lists = {kv_indptr, kv_indices, n_indices, score_stride < kMaxList ? score_stride : kMaxList};
+  a.lists = {kv_indptr, kv_indices, n_indices, max_pages < kMaxList ? max_pages : kMaxList};
   a.rows = rows;
   a.top_k = top_k;
   a.keep_first = keep_first;
@@ -773,11 +774,11 @@ extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stri
   a.sel_indptr = sel_indptr;
   a.sel_indices = sel_indices;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // (a list is no longer than a row of scores; a run of 32 pages to a warp)
+  // (a list is no longer than max_pages; a run of 32 pages to a warp)
   const int few = 256, many = 1024;
-  const bool wide = score_stride > kNarrow, staged = score_stride <= kStagedPages;
+  const bool wide = max_pages > kNarrow, staged = max_pages <= kStagedPages;
   const int threads = wide ? many : few;
-  const size_t smem = staged ? (score_stride + threads - 1) / threads * threads * sizeof(uint32_t) : 0;
+  const size_t smem = staged ? (max_pages + threads - 1) / threads * threads * sizeof(uint32_t) : 0;
   cudaError_t e = cudaSuccess;
   auto kernel = !wide ? select_kernel<few, true> : staged ? select_kernel<many, true> : select_kernel<many, false>;
   // (the same limit in every call: calls may run at once on several threads)

@@ -135,10 +135,11 @@ def bind_library(path: str) -> ctypes.CDLL:
     lib.mla_summarize_pages.restype = c_int
     lib.mla_summarize_pages.argtypes = [_VP, c_i64, _VP, _VP, c_int, c_float, c_int, c_int, _VP, c_int, _VP]
     lib.mla_page_scores.restype = c_int
-    lib.mla_page_scores.argtypes = [_VP, _VP, _VP, c_int, _VP, _VP, c_i64, c_int, c_int, _VP, c_i64, c_int, _VP]
+    lib.mla_page_scores.argtypes = [_VP, _VP, _VP, c_int, _VP, _VP, c_i64, c_int, c_int, _VP, c_i64, c_i64, c_int,
+                                    _VP]
     lib.mla_select_pages.restype = c_int
-    lib.mla_select_pages.argtypes = [_VP, c_i64, _VP, _VP, c_i64, c_int, c_int, c_int, c_int, _VP, _VP, c_i64,
-                                     c_int, _VP]
+    lib.mla_select_pages.argtypes = [_VP, c_i64, c_i64, _VP, _VP, c_i64, c_int, c_int, c_int, c_int, _VP, _VP,
+                                     c_i64, c_int, _VP]
     return lib
 
 
@@ -645,7 +646,7 @@ def mla_page_scores(q_nope, q_pe, summaries, kv_indptr, kv_indices, scores, chec
     heads = lead[1] if len(lead) == 2 else lead[1] * lead[2]
     st = load_library().mla_page_scores(q_nope.data_ptr(), q_pe.data_ptr(), summaries.data_ptr(),
                                         summaries.shape[0], kv_indptr.data_ptr(), kv_indices.data_ptr(),
-                                        kv_indices.numel(), rows, heads, scores.data_ptr(), stride,
+                                        kv_indices.numel(), rows, heads, scores.data_ptr(), stride, scores.shape[1],
                                         int(bool(check_status)), _stream_handle(stream, device))
     _check(st, None, "mla_page_scores")
 
@@ -666,7 +667,7 @@ def mla_select_pages(scores, kv_indptr, kv_indices, top_k: int, keep_first: int,
         raise ValueError("scores must not overlap")
     if sel_indptr.numel() != rows + 1:
         raise ValueError("sel_indptr must have rows + 1 entries")
-    st = load_library().mla_select_pages(scores.data_ptr(), stride, kv_indptr.data_ptr(),
+    st = load_library().mla_select_pages(scores.data_ptr(), stride, scores.shape[1], kv_indptr.data_ptr(),
                                          kv_indices.data_ptr(), kv_indices.numel(), rows, int(top_k),
                                          int(keep_first), int(keep_last), sel_indptr.data_ptr(),
                                          sel_indices.data_ptr(), sel_indices.numel(), int(bool(check_status)),
@@ -809,7 +810,7 @@ class MLASparseDecoder:
         # the arguments of run()'s calls that stay as they are
         lists = (self._kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(), batch)
         self._heads = self.decoder.num_heads * max(q_len, 1)
-        self._choice = (self._scores.data_ptr(), self.max_pages)
+        self._choice = (self._scores.data_ptr(), self.max_pages, self.max_pages)
         self._score_args = lists
         self._select_args = self._choice + lists + (self.top_k, self.keep_first, self.keep_last,
                                                     self._sel_indptr.data_ptr(), self.sel_indices.data_ptr(),
@@ -848,7 +849,7 @@ class MLASparseDecoder:
         import torch
         torch.cuda.synchronize()
         # a call of no rows queues nothing and reports what the kernels recorded
-        _check(load_library().mla_page_scores(None, None, None, 1, None, None, 0, 0, 1, None, 0, 1,
+        _check(load_library().mla_page_scores(None, None, None, 1, None, None, 0, 0, 1, None, 0, 0, 1,
                                               _stream_handle(None)), None, "MLASparseDecoder")
         return self.decoder.check_status()
 

@@ -481,6 +481,30 @@ def test_scores_report_bad_lists():
         mla.mla_page_scores(qn, qp, s, i32([0, 1]), indices, good)
 
 
+def test_scores_of_a_list_past_the_columns():
+    """Rows of scores further apart than their columns: a list longer than the columns is
+    reported by the scores and the selection, and the entries between the rows stay."""
+    s = torch.ones((6, 576), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((3, 4, 576), dtype=torch.bfloat16, device="cuda")
+    qn, qp, indices = q[..., :512].contiguous(), q[..., 512:].contiguous(), i32([0, 1, 2, 3, 4, 5])
+    wide = torch.full((3, 8), 9.0, device="cuda")
+    for indptr, written in (([0, 1, 5, 6], (1, 0, 1)), ([0, 1, 2, 6], (1, 1, 0))):
+        wide.fill_(9.0)
+        with pytest.raises(mla.MLAError) as ei:
+            mla.mla_page_scores(qn, qp, s, i32(indptr), indices, wide[:, :3], check_status=True)
+        assert ei.value.status == mla.ERR_DEVICE_BOUNDS
+        expect = torch.full((3, 8), 9.0)
+        for r, n in enumerate(written):
+            expect[r, :n] = 576.0
+        assert torch.equal(wide.cpu(), expect)
+        si, sp = i32([-3] * 4), i32([-3] * 6)
+        with pytest.raises(mla.MLAError) as ei:
+            mla.mla_select_pages(wide[:, :3], i32(indptr), indices, 2, 0, 1, si, sp, check_status=True)
+        assert ei.value.status == mla.ERR_DEVICE_BOUNDS
+        assert np.diff(si.cpu()).tolist() == list(written)
+        assert sp.tolist() == [indptr[r] for r in range(3) if written[r]] + [-3] * 4
+
+
 def test_scores_several_tokens_share_a_choice():
     """[R, tokens, heads, .] queries: the best over tokens and heads."""
     rng = rng_of(13)

@@ -173,7 +173,7 @@ def test_summarize_refuses(lib, bad, status):
 
 
 def _scores(lib, **bad):
-    kw = dict(qn=PTR, qp=PTR, s=PTR, pages=9, indptr=PTR, indices=PTR, n=9, rows=2, H=16, out=PTR, stride=9)
+    kw = dict(qn=PTR, qp=PTR, s=PTR, pages=9, indptr=PTR, indices=PTR, n=9, rows=2, H=16, out=PTR, stride=9, most=9)
     kw.update(bad)
     return lib.mla_page_scores(*kw.values(), 0, None)
 
@@ -184,13 +184,14 @@ def _scores(lib, **bad):
     (dict(out=None), mla.ERR_INVALID_ARG), (dict(qn=PTR + 8), mla.ERR_INVALID_ARG),
     (dict(H=0), mla.ERR_INVALID_ARG), (dict(H=129), mla.ERR_INVALID_ARG), (dict(pages=0), mla.ERR_INVALID_ARG),
     (dict(rows=-1), mla.ERR_INVALID_ARG), (dict(n=-1), mla.ERR_INVALID_ARG), (dict(rows=4097), mla.ERR_CAPACITY),
+    (dict(most=10), mla.ERR_INVALID_ARG), (dict(most=-1), mla.ERR_INVALID_ARG),
 ])
 def test_scores_refuse(lib, bad, status):
     assert _scores(lib, **bad) == status
 
 
 def _select(lib, **bad):
-    kw = dict(s=PTR, stride=9, indptr=PTR, indices=PTR, n=9, rows=2, k=4, kf=1, kl=1, si=PTR, sp=PTR, cap=8)
+    kw = dict(s=PTR, stride=9, most=9, indptr=PTR, indices=PTR, n=9, rows=2, k=4, kf=1, kl=1, si=PTR, sp=PTR, cap=8)
     kw.update(bad)
     return lib.mla_select_pages(*kw.values(), 0, None)
 
@@ -203,6 +204,7 @@ def _select(lib, **bad):
     (dict(kf=2 ** 31 - 1, kl=2 ** 31 - 1, k=2 ** 31 - 1, cap=1 << 40), mla.ERR_INVALID_ARG),
     (dict(cap=7), mla.ERR_CAPACITY), (dict(rows=4097, cap=1 << 20), mla.ERR_CAPACITY),
     (dict(k=2 ** 31 - 1, cap=1 << 40), mla.ERR_CAPACITY),
+    (dict(most=10), mla.ERR_INVALID_ARG), (dict(most=-1), mla.ERR_INVALID_ARG),
 ])
 def test_selection_refuses(lib, bad, status):
     assert _select(lib, **bad) == status
