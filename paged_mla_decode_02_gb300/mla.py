@@ -468,6 +468,21 @@ def _on_device(device: int, dtype, names: str, *tensors, contiguous: bool = True
             raise ValueError(f"{name} must be contiguous")
 
 
+def _torch_stream(stream):
+    import torch
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for what a call fills, of the stream it fills it on: a block that
+    another stream gave back may still be read there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _row_stride(name: str, t, rows: int, cols=None) -> int:
     """The row stride of a [rows, cols] tensor whose rows are runs of adjacent
     entries (strides of dimensions of one entry or none say nothing)."""
@@ -586,7 +601,7 @@ def mla_rope_append(rope: RopeSpec, positions, slots, q_pe, ckv, kpe, norm_weigh
         H = q_pe.shape[1]
         q_t, q_h = q_pe.stride(0) if T > 1 else 0, q_pe.stride(1) if H > 1 else 0
         if q_pe_out is None:
-            q_pe_out = torch.empty((T, H, 64), dtype=torch.bfloat16, device=q_pe.device)
+            q_pe_out = _empty((T, H, 64), torch.bfloat16, q_pe.device, stream)
         else:
             _on_device(device, torch.bfloat16, "q_pe_out", q_pe_out)
             if q_pe_out.shape != q_pe.shape:
@@ -767,6 +782,7 @@ class MLASparseDecoder:
         self._kv_indptr = torch.zeros(self.max_batch + 1, dtype=torch.int32, device=dev)
         self._scores = torch.empty((self.max_batch, self.max_pages), dtype=torch.float32, device=dev)
         self._kv_indices, self.sel_indptr, self.batch = None, None, 0
+        torch.cuda.current_stream().synchronize()   # the zeros are in place for a run on any stream
 
     def plan(self, kv_indptr, kv_indices, kv_len, page_size: int, sm_scale: float, stream=None,
              q_len: int = 0) -> None:
@@ -799,11 +815,7 @@ class MLASparseDecoder:
         # rows past the batch get empty lists: a graph of a larger batch replays this plan
         whole = np.full(self.max_batch + 1, indptr[-1], np.int32)
         whole[:batch + 1] = indptr
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        elif not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else _torch_stream(stream)):
             self._kv_indptr.copy_(torch.from_numpy(whole))
         self._kv_indices, self.batch = kv_indices, batch   # keep the borrowed page list alive
         self.sel_indptr = self._sel_indptr[:batch + 1]   # device offsets of the selected pages, after a run
@@ -835,6 +847,11 @@ class MLASparseDecoder:
         heads = q[1] if len(q) == 3 else q[1] * q[2]
         if heads != self._heads:   # the decode reads as many rows as were planned
             raise ValueError(f"q_nope must have {self._heads} query rows (tokens x heads) per request, got {heads}")
+        if stream is not None:   # (the decode would take them from the current stream)
+            if out is None:
+                out = _empty(tuple(q), out_dtype or torch.bfloat16, q_nope.device, stream)
+            if lse is None:
+                lse = _empty(tuple(q[:-1]), torch.float32, q_nope.device, stream)
         lib, stream = load_library(), _stream_handle(stream)
         st = lib.mla_page_scores(q_nope.data_ptr(), q_pe.data_ptr(), summaries.data_ptr(), rows[0], *self._score_args,
                                  heads, *self._choice, 0, stream)

@@ -739,6 +739,46 @@ def dev_on(stream, a):
         return dev(a)
 
 
+def test_outputs_made_on_another_stream():
+    """An output that a call makes for another stream is not memory that the current
+    stream gave back and has yet to read."""
+    side = torch.cuda.Stream()
+    T, H, B = 1024, 128, 128    # outputs of 16 MB, blocks of their own
+    q_pe = torch.zeros((T, H, 64), dtype=torch.bfloat16, device="cuda")
+    ckv, kpe = (torch.zeros((T, n), dtype=torch.bfloat16, device="cuda") for n in (512, 64))
+    cache = [torch.zeros((8, 16, n), dtype=torch.bfloat16, device="cuda") for n in (512, 64)]
+    pos, slots = i32(np.zeros(T)), torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    slots[:32] = torch.arange(32, device="cuda")
+    qn, qp = (torch.zeros((B, H, n), dtype=torch.bfloat16, device="cuda") for n in (512, 64))
+    s = torch.zeros((8, 576), dtype=torch.bfloat16, device="cuda")
+    dec = mla.MLASparseDecoder(B, H, 2, 2)
+    dec.plan(range(B + 1), i32(np.arange(B) % 8), [16] * B, 16, 0.1)
+    torch.cuda.synchronize()
+
+    def behind(shape, call):
+        call()                               # (loads its kernels)
+        before = torch.ones(shape, dtype=torch.bfloat16, device="cuda")
+        copy = torch.empty_like(before)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(1 << 27)           # the current stream is busy for some tens of milliseconds
+        copy.copy_(before)                   # and reads its tensor after that
+        del before
+        made = call()                        # meanwhile another stream has an output of the same size
+        torch.cuda.synchronize()
+        assert bool((copy == 1).all())
+        return made
+
+    try:
+        spec = mla.rope_spec(FREQ)
+        turned = behind((T, H, 64), lambda: mla.mla_rope_append(spec, pos, slots, q_pe, ckv, kpe, None, 0.0, *cache,
+                                                                 stream=side))
+        assert bool((turned[:32] == 0).all())
+        out, lse = behind((B, H, 512), lambda: dec.run(qn, qp, *cache, s, stream=side))
+        assert bool((out == 0).all())
+    finally:
+        dec.close()
+
+
 def test_offsets_past_32_bits():
     """The last slot of a cache of more than 2^31 values, and the last of more than 2^31 summary values."""
     pages, P = 66000, 64
