@@ -263,7 +263,10 @@ __global__ void __launch_bounds__(kQThreads, 4) append_kernel(const __grid_const
 // Page summaries
 // ---------------------------------------------------------------------------
 constexpr int kSumThreads = 32 * (kD / 64);   // a warp for each 64 dims of a row
-constexpr int kSumBlocksPerSm = 3;            // all resident: one wave, no CTA waits for another's end
+// CTAs of an SM, all resident: one wave, no CTA waits for another's end (65500
+// tokens in bf16: 14.3 us with four, 16.5 with three; 131000 in e4m3, whose
+// threads sum more dims: 15.2 with three, 15.8 with four)
+__host__ __device__ constexpr int sum_blocks(bool fp8) { return fp8 ? 3 : 4; }
 
 struct SummarizeArgs {
   const int64_t* slots;
@@ -277,7 +280,15 @@ struct SummarizeArgs {
   int per_block;             // tokens a CTA looks at
 };
 
-// Sixteen bytes of a cached row as fp32: 8 bf16 or 16 e4m3 values.
+// sum + v in fp32, v the bits of an fp16 or bf16 value: one instruction, where
+// a conversion and an addition are two (131000 tokens, e4m3: 15.7 us with those).
+template <bool kHalf>
+__device__ __forceinline__ void add_wide(float& sum, unsigned short v) {
+  if (kHalf) asm("add.rn.f32.f16 %0, %1, %0;" : "+f"(sum) : "h"(v));
+  else asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(sum) : "h"(v));
+}
+
+// Sixteen bytes of a cached row added in fp32: 8 bf16 or 16 e4m3 values.
 template <bool kFp8, int N>
 __device__ __forceinline__ void add_values(float (&sum)[N], const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -285,15 +296,14 @@ __device__ __forceinline__ void add_values(float (&sum)[N], const uint4& v) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      sum[2 * i] += f.x;
-      sum[2 * i + 1] += f.y;
+      add_wide<true>(sum[2 * i], h.x);
+      add_wide<true>(sum[2 * i + 1], h.y);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sum[2 * i] += __uint_as_float(w[i] << 16);
-      sum[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+      add_wide<false>(sum[2 * i], w[i] & 0xffffu);
+      add_wide<false>(sum[2 * i + 1], w[i] >> 16);
     }
   }
 }
@@ -303,14 +313,17 @@ __device__ __forceinline__ void add_values(float (&sum)[N], const uint4& v) {
 // (bf16) or 8 (e4m3) rows to a load.  The rows' partial sums meet in the warp
 // by halves: at each step a lane passes on half of its dims and adds what it
 // gets to the other half, down to two.  The warps of a CTA read the same rows
-// at about the same time, and each has the next reads under way while it adds
-// the last.  Bound by HBM for long prompts (131000 tokens, e4m3, 32-token
-// pages: 81 MB in 15.7 us, 5.2 TB/s).
-template <bool kFp8>
-__global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) summarize_kernel(const SummarizeArgs a) {
+// at about the same time, and each has the next four loads under way while it
+// adds the last; two pages share them where one has rows for two only (kPair:
+// e4m3, 16 tokens).  Bound by HBM for long prompts (131000 tokens, e4m3,
+// 32-token pages: 81 MB in 15.2 us, 5.3 TB/s; 16-token pages 15.8, a page at a
+// time 20.7).
+template <bool kFp8, bool kPair>
+__global__ void __launch_bounds__(kSumThreads, sum_blocks(kFp8)) summarize_kernel(const SummarizeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kDims = kFp8 ? 16 : 8, kLanes = 64 / kDims, kRows = 32 / kLanes, kLoads = 4;
+  constexpr int kOfPage = kPair ? kLoads / 2 : kLoads;   // loads of a page at a time
   __shared__ int pages[kSumThreads], n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = 1 << a.page_shift, row0 = lane / kLanes, col = (lane % kLanes) * kDims;
@@ -322,36 +335,24 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) summarize_kernel
   if (slot >= a.cache_slots) report_error(&g_append_err, kErrBounds);
   else if (slot >= 0 && (slot & (P - 1)) == P - 1) pages[atomicAdd(&n, 1)] = static_cast<int>(slot >> a.page_shift);
   __syncthreads();
-  // their rows, kRows * kLoads at a time
+  // their rows, kLoads loads of kRows at a time
   const bool pe = warp == kSumThreads / 32 - 1;
   const int width = (pe ? kDKpe : kDCkv) * (kFp8 ? 1 : 2);   // bytes of a row
   const char* rows = static_cast<const char*>(pe ? a.kpe : a.ckv) + ((pe ? 0 : 64 * warp) + col) * (kFp8 ? 1 : 2);
-  const int batches = P > kRows * kLoads ? P / (kRows * kLoads) : 1;
+  const int batches = P / (kRows * kOfPage);   // of a page
   uint4 next[kLoads];
-  auto read = [&](int page, int batch) {
-    const char* src = rows + ((static_cast<int64_t>(page) << a.page_shift) + row0) * width;
+  auto read = [&](int i, int batch) {
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const int r = (batch * kLoads + k) * kRows;
-      if (r < P) next[k] = *reinterpret_cast<const uint4*>(src + r * width);
+    for (int k0 = 0; k0 < kLoads; k0 += kOfPage) {
+      if (kPair && i + k0 / kOfPage >= n) break;
+      const char* src = rows + ((static_cast<int64_t>(pages[i + k0 / kOfPage]) << a.page_shift) + row0) * width;
+#pragma unroll
+      for (int k = 0; k < kOfPage; ++k)
+        next[k0 + k] = *reinterpret_cast<const uint4*>(src + (batch * kOfPage + k) * kRows * width);
     }
   };
   float sum[kDims] = {};
-  if (n > 0) read(pages[0], 0);
-  for (int i = 0, batch = 0; i < n;) {
-    uint4 v[kLoads];
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) v[k] = next[k];
-    const int page = pages[i], done = batch;
-    if (++batch == batches) {
-      batch = 0;
-      ++i;
-    }
-    if (i < n) read(pages[i], batch);
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k)
-      if ((done * kLoads + k) * kRows < P) add_values<kFp8>(sum, v[k]);
-    if (batch) continue;
+  auto finish = [&](int page) {   // the sums of its rows are done
     int at = col;   // the first of this lane's dims
 #pragma unroll
     for (int half = kDims / 2, d = kLanes; half > 1; half >>= 1, d <<= 1) {
@@ -367,6 +368,29 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) summarize_kernel
         pack_bf16x2(sum[0] * a.scale, sum[1] * a.scale);
 #pragma unroll
     for (int j = 0; j < kDims; ++j) sum[j] = 0.f;
+  };
+  if (n > 0) read(0, 0);
+  for (int i = 0, batch = 0; i < n;) {
+    uint4 v[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) v[k] = next[k];
+    const int now = i;
+    if (kPair) {
+      i += 2;
+    } else if (++batch == batches) {
+      batch = 0;
+      ++i;
+    }
+    if (i < n) read(i, batch);
+#pragma unroll
+    for (int k = 0; k < kOfPage; ++k) add_values<kFp8>(sum, v[k]);
+    if (!kPair && batch) continue;
+    finish(pages[now]);
+    if (kPair && now + 1 < n) {
+#pragma unroll
+      for (int k = kOfPage; k < kLoads; ++k) add_values<kFp8>(sum, v[k]);
+      finish(pages[now + 1]);
+    }
   }
 }
 
@@ -473,12 +497,16 @@ extern "C" mla_status_t mla_summarize_pages(const int64_t* slots, int64_t tokens
   int sms = 0;
   cudaError_t e = cudaSuccess;
   if (tokens > 0 && (e = current_sms(&sms)) == cudaSuccess) {
-    // one wave of CTAs with equal runs of tokens (131000 tokens, e4m3: 15.7 us;
-    // four CTAs an SM 17.5, two waves of three 17.5)
-    const int64_t blocks = static_cast<int64_t>(sms) * kSumBlocksPerSm, run = (tokens + blocks - 1) / blocks;
+    // one wave of CTAs with equal runs of tokens (fewer CTAs for a short run are no
+    // better: 8192 tokens of a prompt 2.9 us against 3.4 with one an SM, but 4096
+    // single ones 5.2 against 4.4, and 88 against 48 where each completes a page)
+    const bool fp8 = kv_dtype == MLA_DTYPE_FP8_E4M3;
+    const int64_t blocks = static_cast<int64_t>(sms) * sum_blocks(fp8), run = (tokens + blocks - 1) / blocks;
     a.per_block = static_cast<int>(run < kSumThreads ? run : kSumThreads);
-    e = launch_dependent(kv_dtype == MLA_DTYPE_FP8_E4M3 ? summarize_kernel<true> : summarize_kernel<false>,
-                         static_cast<int>((tokens + a.per_block - 1) / a.per_block), kSumThreads, 0, 1, s, a);
+    auto kernel = !fp8              ? summarize_kernel<false, false>
+                  : page_size == 16 ? summarize_kernel<true, true>
+                                    : summarize_kernel<true, false>;
+    e = launch_dependent(kernel, static_cast<int>((tokens + a.per_block - 1) / a.per_block), kSumThreads, 0, 1, s, a);
   }
   return finish_call(e, &g_append_err, check_status, s);
 }

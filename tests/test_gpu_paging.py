@@ -392,6 +392,25 @@ def test_summaries_match_oracle(P, fp8):
         assert np.all(np.abs(got[p] - ref) <= rounded_bound(ref, False) + size * (P + 2) * 2.0 ** -23), p
 
 
+@pytest.mark.parametrize("P, fp8", [(16, True), (16, False), (32, True), (64, False)])
+def test_summaries_of_a_long_step(P, fp8):
+    """Runs of tokens that complete several pages each, an odd number of them too."""
+    rng = rng_of(7, P, fp8)
+    pages, kv_scale = 40000 // P, 0.25 if fp8 else 1.0
+    cc, kc = cache_of(rng, pages, P, fp8)
+    out = torch.full((pages, 576), 5.0, dtype=torch.bfloat16, device="cuda")
+    slots = (rng.permutation(pages)[:, None] * P + np.arange(P)).astype(np.int64).reshape(-1)
+    slots[rng.random(slots.size) < 0.1] = -1                 # padding: some pages are not completed
+    mla.mla_summarize_pages(dev(slots), cc, kc, out, kv_scale=kv_scale, check_status=True)
+    full = np.zeros(pages, bool)
+    full[slots[slots % P == P - 1] // P] = True
+    rows = np.concatenate([f64(cc.float()), f64(kc.float())], 2) * kv_scale
+    ref, size, got = rows.mean(1), np.abs(rows).mean(1), f64(out)
+    assert np.all(got[~full] == 5.0) and 0 < full.sum() < pages
+    # as above: P additions in fp32 and a product, and the rounding to bf16
+    assert np.all(np.abs(got - ref)[full] <= (rounded_bound(ref, False) + size * (P + 2) * 2.0 ** -23)[full])
+
+
 def test_summaries_report_a_slot_past_the_cache():
     cc, kc = cache_of(rng_of(5), 2, 16, False)
     out = torch.full((2, 576), 5.0, dtype=torch.bfloat16, device="cuda")
