@@ -140,8 +140,8 @@ __device__ __forceinline__ void store1(void* cache, int64_t at, float x) {
 // few tokens each.  A token's 32 angles are shared by all of its heads: a CTA
 // makes them once, into shared memory, while its first reads are under way,
 // and then is bound by reading and writing the rows (a thread turns a quarter
-// of a row, 32 bytes each way): 8190 tokens x 128 heads, 283 MB in 47.8 us,
-// 5.8 TB/s.
+// of a row, 32 bytes each way): 8190 tokens x 128 heads, 283 MB in 48.0 us,
+// 5.9 TB/s.
 template <bool kInterleaved, bool kFp8>
 __global__ void __launch_bounds__(kQThreads, 4) append_kernel(const __grid_constant__ AppendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -461,7 +461,7 @@ extern "C" mla_status_t mla_rope_append(const mla_rope_t* rope, const int32_t* p
   a.tokens = tokens;
   a.heads = num_heads > 0 ? num_heads : 1;
   // Query rows of a CTA: four quarters to a thread keep 128 KB an SM in flight
-  // (8190 tokens x 128 heads: 47.8 us, with two 54.6), but a short step is over
+  // (8190 tokens x 128 heads: 48.0 us, with two 54.6), but a short step is over
   // sooner on more SMs (64 x 128: 2.5 us with two, 3.5 with four).
   const int rows = tokens * num_heads >= kManyRows ? kRowsPerBlock : kRowsPerBlock / 2;
   a.tokens_per_block = num_heads == 0 || num_heads >= rows ? 1 : rows / num_heads < kMostTokens ? rows / num_heads : kMostTokens;

@@ -61,9 +61,9 @@ __device__ __forceinline__ int list_of(const Lists& l, int r, int* first) {
 // by a CTA pair (kPair, cta_group::2): tiles have up to 256 pages, halved
 // between the two CTAs, as are the heads of the queries that each holds, and
 // the even CTA issues MMAs of M = 256 that read both.
-// Measured: 64 rows x 1024 pages x 128 heads, 85 MB, 18.0 us (4.7 TB/s, of
+// Measured: 64 rows x 1024 pages x 128 heads, 85 MB, 17.8 us (4.8 TB/s, of
 // which about 5 us until the first tile has arrived; then the rate of HBM);
-// 4 rows x 100 pages x 16 heads 5.6 us.
+// 4 rows x 100 pages x 16 heads 5.7 us.
 struct ScoreArgs {
   const char* summaries;
   int num_pages;
