@@ -756,9 +756,10 @@ class MLASparseDecoder:
     selected pages, all queued on the stream without synchronisation.
 
     Holds lists of up to ``max_pages`` pages for each of ``max_batch`` requests.
-    A captured run replays after re-plans of at most the captured batch; like a
-    decode plan's graph it keeps the addresses it was captured with, that of
-    the page list included.
+    A captured run replays after re-plans of at most the captured batch and of
+    the captured q_len; like a decode plan's graph it keeps the addresses it was
+    captured with, that of the page list included.  The list may be passed
+    shorter or longer there at every plan (``indices[:n]`` of one buffer).
 
     With q_len query tokens per request (q_len x heads <= 128, batch x q_len <=
     max_batch) the choice is theirs together, and keep_last must cover the
@@ -819,8 +820,12 @@ class MLASparseDecoder:
             self._kv_indptr.copy_(torch.from_numpy(whole))
         self._kv_indices, self.batch = kv_indices, batch   # keep the borrowed page list alive
         self.sel_indptr = self._sel_indptr[:batch + 1]   # device offsets of the selected pages, after a run
-        # the arguments of run()'s calls that stay as they are
-        lists = (self._kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(), batch)
+        # the arguments of run()'s calls that stay as they are.  A captured run keeps
+        # them while later plans lengthen the list at its place, so its bound is not
+        # the list's length (the plan checked that) but the memory behind its first
+        # entry, or what the decoder holds.
+        behind = kv_indices.untyped_storage().nbytes() // kv_indices.element_size() - kv_indices.storage_offset()
+        lists = (self._kv_indptr.data_ptr(), kv_indices.data_ptr(), min(behind, self.max_batch * self.max_pages), batch)
         self._heads = self.decoder.num_heads * max(q_len, 1)
         self._choice = (self._scores.data_ptr(), self.max_pages, self.max_pages)
         self._score_args = lists
