@@ -22,10 +22,14 @@
  * long as none writes what another reads or writes.
  *
  * check_status != 0 waits for the stream and returns the first device error
- * that this file's kernels recorded since the last such call
- * (MLA_ERR_DEVICE_BOUNDS: an index outside its array, whose access was
- * skipped; MLA_ERR_DEVICE_TIMEOUT: a bounded wait ran out), then clears it.
- * It cannot be captured.
+ * recorded on this device since the last such call (MLA_ERR_DEVICE_BOUNDS: an
+ * index outside its array, whose access was skipped; MLA_ERR_DEVICE_TIMEOUT: a
+ * bounded wait ran out), and clears it.  All calls of this file that take
+ * check_status share one word, whichever of them recorded the error and on
+ * whichever stream: a step may check once, through its last call, and callers
+ * that are to tell their errors apart check after each of their calls.  A call
+ * of no tokens or rows checks without a kernel of its own.  It cannot be
+ * captured.
  */
 #ifndef MLA_PAGING_H
 #define MLA_PAGING_H

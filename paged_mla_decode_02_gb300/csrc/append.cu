@@ -23,8 +23,6 @@
 namespace mla {
 namespace {
 
-__device__ int32_t g_append_err;   // first device error of this file's kernels
-
 constexpr int kPairs = kDKpe / 2;
 constexpr int kMaxAxes = 8;
 constexpr int kQThreads = 256;
@@ -56,6 +54,7 @@ struct AppendArgs {
   void* ckv_cache;
   void* kpe_cache;
   float inv_scale;           // 1 / kv_scale (1 for a bf16 cache)
+  int32_t* err;
   int64_t cache_slots;       // num_pages * page_size
   int64_t tokens;
   int heads;
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(kQThreads, 4) append_kernel(const __grid_const
   const float2 cs = cos_sin(a, lane, t);
   if (slot < 0) return;
   if (slot >= a.cache_slots) {
-    if (lane == 0) report_error(&g_append_err, kErrBounds);
+    if (lane == 0) report_error(a.err, kErrBounds);
     return;
   }
   float sq = 0.f;
@@ -277,6 +276,7 @@ struct SummarizeArgs {
   int64_t cache_slots;
   int page_shift;
   __nv_bfloat16* summaries;
+  int32_t* err;
   int per_block;             // tokens a CTA looks at
 };
 
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kSumThreads, sum_blocks(kFp8)) summarize_kerne
   const int64_t t = static_cast<int64_t>(blockIdx.x) * a.per_block + threadIdx.x;
   const int64_t slot = static_cast<int>(threadIdx.x) < a.per_block && t < a.tokens ? a.slots[t] : -1;
   __syncthreads();
-  if (slot >= a.cache_slots) report_error(&g_append_err, kErrBounds);
+  if (slot >= a.cache_slots) report_error(a.err, kErrBounds);
   else if (slot >= 0 && (slot & (P - 1)) == P - 1) pages[atomicAdd(&n, 1)] = static_cast<int>(slot >> a.page_shift);
   __syncthreads();
   // their rows, kLoads loads of kRows at a time
@@ -467,14 +467,14 @@ extern "C" mla_status_t mla_rope_append(const mla_rope_t* rope, const int32_t* p
   a.tokens_per_block = num_heads == 0 || num_heads >= rows ? 1 : rows / num_heads < kMostTokens ? rows / num_heads : kMostTokens;
   a.kv_blocks = (tokens + kKvWarps - 1) / kKvWarps;
   cudaError_t e = cudaSuccess;
-  if (tokens > 0) {
+  if (tokens > 0 && (e = paging_error_word(&a.err)) == cudaSuccess) {
     const int64_t q_blocks = num_heads > 0 ? (tokens + a.tokens_per_block - 1) / a.tokens_per_block : 0;
     const int grid = static_cast<int>(a.kv_blocks + q_blocks);
     auto kernel = rope->interleaved ? (fp8 ? append_kernel<true, true> : append_kernel<true, false>)
                                     : (fp8 ? append_kernel<false, true> : append_kernel<false, false>);
     e = launch_dependent(kernel, grid, kQThreads, 0, 1, s, a);
   }
-  return finish_call(e, &g_append_err, check_status, s);
+  return finish_call(e, check_status, s);
 }
 
 extern "C" mla_status_t mla_summarize_pages(const int64_t* slots, int64_t tokens, const void* ckv_cache,
@@ -496,7 +496,7 @@ extern "C" mla_status_t mla_summarize_pages(const int64_t* slots, int64_t tokens
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = 0;
   cudaError_t e = cudaSuccess;
-  if (tokens > 0 && (e = current_sms(&sms)) == cudaSuccess) {
+  if (tokens > 0 && (e = current_sms(&sms)) == cudaSuccess && (e = paging_error_word(&a.err)) == cudaSuccess) {
     // one wave of CTAs with equal runs of tokens (fewer CTAs for a short run are no
     // better: 8192 tokens of a prompt 2.9 us against 3.4 with one an SM, but 4096
     // single ones 5.2 against 4.4, and 88 against 48 where each completes a page)
@@ -508,5 +508,5 @@ extern "C" mla_status_t mla_summarize_pages(const int64_t* slots, int64_t tokens
                                     : summarize_kernel<true, false>;
     e = launch_dependent(kernel, static_cast<int>((tokens + a.per_block - 1) / a.per_block), kSumThreads, 0, 1, s, a);
   }
-  return finish_call(e, &g_append_err, check_status, s);
+  return finish_call(e, check_status, s);
 }

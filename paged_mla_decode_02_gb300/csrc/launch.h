@@ -1,4 +1,4 @@
-// Launches and device error words of the operators around the decode.
+// Launches and the device error word of the operators around the decode.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -38,26 +38,13 @@ inline cudaError_t current_sms(int* sms) {
   return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
 }
 
-// Status of a call whose kernels record their first error in the __device__
-// word `symbol`: with check_status, waits for the stream, reads the word and
-// clears it.
-inline mla_status_t finish_call(cudaError_t e, const void* symbol, int check_status, cudaStream_t s) {
-  int32_t err = 0;
-  if (e == cudaSuccess && check_status) {
-    e = cudaMemcpyFromSymbolAsync(&err, symbol, sizeof(err), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess && err != 0) {
-      const int32_t zero = 0;
-      e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-      if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-  }
-  if (e != cudaSuccess) {
-    cudaGetLastError();   // clear a non-sticky error so later calls start clean
-    return MLA_ERR_CUDA;
-  }
-  return static_cast<mla_status_t>(err);
-}
+// The current device's error word, in which the kernels of mla_paging.h record
+// the first error.
+cudaError_t paging_error_word(int32_t** word);
+
+// Status of a call that queued its kernels with result `e`; with check_status,
+// waits for the stream and takes what the error word holds.
+mla_status_t finish_call(cudaError_t e, int check_status, cudaStream_t s);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 

@@ -19,7 +19,6 @@ namespace {
 
 constexpr int kMaxRows = 4096;
 constexpr int64_t kMaxList = 1 << 30;   // pages of a list
-__device__ int32_t g_select_err;   // first device error of this file's kernels
 
 // Row r's page list: its first entry and length, or nothing (reported) when
 // it leaves kv_indices or is longer than `longest`.
@@ -28,12 +27,13 @@ struct Lists {
   const int32_t* indices;
   int64_t n_indices;
   int64_t longest;
+  int32_t* err;
 };
 __device__ __forceinline__ int list_of(const Lists& l, int r, int* first) {
   const int b = l.indptr[r], e = l.indptr[r + 1];
   *first = b;
   if (b >= 0 && e >= b && e <= l.n_indices && e - b <= l.longest) return e - b;
-  report_error(&g_select_err, kErrBounds);
+  report_error(l.err, kErrBounds);
   return 0;
 }
 
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       at[0] = 0;
       dealt[0] = sound ? all : 0;
       dealt[1] = quarters * kQuarter;
-      if (!sound) report_error(&g_select_err, kErrBounds);
+      if (!sound) report_error(a.lists.err, kErrBounds);
     }
   }
   tc_fence_before();
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       ok = __all_sync(~0u, ok);
       ++visit;
     }
-    if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
+    if (!ok && lane == 0) report_error(a.lists.err, kErrTimeout);
     if (rank == 0 && lane == 0) {   // every copy issued has landed before the CTA leaves
 #pragma unroll 1
       for (int g = 0; g < kQGroups && visit > 0; ++g) {
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     cp_async_wait<0>();
     while (ok && pending > 0) land();
-    if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
+    if (!ok && lane == 0) report_error(a.lists.err, kErrTimeout);
   } else if (warp == 1) {
     // ---------------- MMAs (a pair: in its even CTA) ----------------
     const uint32_t idesc = idesc_bf16_f32(kTilePages * F::kCtas, held * F::kCtas, false, false);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       commit(F::kTFull + acc);
       ok = __all_sync(~0u, ok);
     }
-    if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
+    if (!ok && lane == 0) report_error(a.lists.err, kErrTimeout);
     if (rank == 0) {
       commit(F::kFinal, 1);   // every MMA issued completes before TMEM is freed
       if (lane == 0) {
@@ -442,13 +442,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (lane == 0) arrive_even(F::kTEmpty + acc);
       if (p < t.pages) {
         if (id < 0 || id >= a.num_pages) {
-          report_error(&g_select_err, kErrBounds);
+          report_error(a.lists.err, kErrBounds);
           best = -INFINITY;
         }
         a.scores[t.row * a.stride + t.page0 + p] = best;
       }
     }
-    if (!ok && lane == 0) report_error(&g_select_err, kErrTimeout);
+    if (!ok && lane == 0) report_error(a.lists.err, kErrTimeout);
   }
   tc_fence_before();
   if (kPair) cluster_sync_all(); else __syncthreads();   // (a pair: neither reads the other's memory any more)
@@ -713,7 +713,7 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
   ScoreArgs a{};
   a.summaries = static_cast<const char*>(summaries);
   a.num_pages = num_pages;
-  a.lists = {kv_indptr, kv_indices, n_indices, max_pages < kMaxList ? max_pages : kMaxList};
+  a.lists = {kv_indptr, kv_indices, n_indices, max_pages < kMaxList ? max_pages : kMaxList, nullptr};
   a.rows = rows;
   a.heads = num_heads;
   a.scores = scores;
@@ -728,6 +728,7 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
   auto kernel = pair ? scores_kernel<true> : scores_kernel<false>;
   int sms = 0;
   cudaError_t e = rows > 0 ? current_sms(&sms) : cudaSuccess;
+  if (rows > 0 && e == cudaSuccess) e = paging_error_word(&a.lists.err);
   // (the same limit in every call: calls may run at once on several threads)
   if (rows > 0 && e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -747,7 +748,7 @@ extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, co
     const int grid = ctas * static_cast<int>(tiles < most ? tiles : most);
     e = launch_dependent(kernel, grid, kScoreThreads, smem, ctas, s, mn, mp, a);
   }
-  return finish_call(e, &g_select_err, check_status, s);
+  return finish_call(e, check_status, s);
 }
 
 extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stride, int64_t max_pages,
@@ -766,7 +767,7 @@ extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stri
   SelectArgs a{};
   a.scores = scores;
   a.stride = score_stride;
-  a.lists = {kv_indptr, kv_indices, n_indices, max_pages < kMaxList ? max_pages : kMaxList};
+  a.lists = {kv_indptr, kv_indices, n_indices, max_pages < kMaxList ? max_pages : kMaxList, nullptr};
   a.rows = rows;
   a.top_k = top_k;
   a.keep_first = keep_first;
@@ -782,11 +783,12 @@ extern "C" mla_status_t mla_select_pages(const float* scores, int64_t score_stri
   cudaError_t e = cudaSuccess;
   auto kernel = !wide ? select_kernel<few, true> : staged ? select_kernel<many, true> : select_kernel<many, false>;
   // (the same limit in every call: calls may run at once on several threads)
-  if (smem > 32 * 1024)
+  if (rows > 0) e = paging_error_word(&a.lists.err);
+  if (e == cudaSuccess && smem > 32 * 1024)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kStagedPages * static_cast<int>(sizeof(uint32_t)));
   if (e == cudaSuccess)
     e = rows == 0 ? cudaMemsetAsync(sel_indptr, 0, sizeof(int32_t), s)
                   : launch_dependent(kernel, rows, threads, smem, 1, s, a);
-  return finish_call(e, &g_select_err, check_status, s);
+  return finish_call(e, check_status, s);
 }

@@ -327,5 +327,5 @@ extern "C" mla_status_t mla_build_tables(const int32_t* kv_len, const int32_t* n
                              static_cast<int>(sizeof(int)) * (5 * kMaxBatch + 4));
   if (e == cudaSuccess)
     e = launch_dependent(tables_kernel, kCtas, kThreads, smem, kCtas, static_cast<cudaStream_t>(stream), a);
-  return finish_call(e, nullptr, 0, nullptr);
+  return finish_call(e, 0, nullptr);
 }
