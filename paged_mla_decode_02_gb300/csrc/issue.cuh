@@ -42,6 +42,14 @@ __device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, volatil
   return true;
 }
 
+// A word of a CTA of the cluster's shared memory (address from map_to_rank).
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void pause_ns(uint64_t ns) {
+  for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < ns;) __nanosleep(1000);
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16.
 __device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
@@ -63,6 +71,18 @@ __device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
       "elect.sync _|q, 0xffffffff;\n"
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
       "}\n" ::"r"(bar)
+      : "memory");
+}
+// The same, if the elected lane says so.
+__device__ __forceinline__ void mma_commit_elect_if(uint32_t bar, bool yes) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "setp.ne.and.b32 p, %1, 0, q;\n"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      "}\n" ::"r"(bar),
+      "r"(static_cast<uint32_t>(yes))
       : "memory");
 }
 // Load the 3-D box at {x, y, z}, completing on the mbarrier.
@@ -101,6 +121,18 @@ __device__ __forceinline__ void commit_pair_elect(uint32_t bar, int ctas) {
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n"
       "}\n" ::"r"(bar),
       "h"(static_cast<uint16_t>(ctas))
+      : "memory");
+}
+// The same, if the elected lane says so.
+__device__ __forceinline__ void commit_pair_elect_if(uint32_t bar, int ctas, bool yes) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "setp.ne.and.b32 p, %2, 0, q;\n"
+      "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n"
+      "}\n" ::"r"(bar),
+      "h"(static_cast<uint16_t>(ctas)), "r"(static_cast<uint32_t>(yes))
       : "memory");
 }
 // Load the 3-D box at {x, y, z}, completing on an mbarrier of either CTA of the pair.

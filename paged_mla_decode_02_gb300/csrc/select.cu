@@ -104,6 +104,15 @@ struct Tile {
   bool enters, leaves;     // the first, the last tile of the row in this share
 };
 
+#ifdef MLA_STALL_TEST
+// Test build only: when nonzero, one CTA (the first, or the second if negative)
+// leaves out the signal of its n-th chunk of pages (n = 1 ..), or, from
+// kStallQueries up, its copy of group n - kStallQueries of its first row's
+// queries: the waits for them run out.
+__device__ int g_scores_stall;
+constexpr int kStallQueries = 1000;
+#endif
+
 // 16 bytes into shared memory, the 256 around them into L2: the next chunk of
 // the row follows.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -141,6 +150,20 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     return kPair ? mbar_wait_cl_warp(bar(i), parity, abort_flag) : mbar_wait_warp(bar(i), parity, abort_flag);
   };
   auto spin = [&](int i, int parity) { return mbar_spin<kPair>(bar(i), parity, abort_flag); };
+  // A role whose wait ran out issues nothing more that another CTA or a later
+  // wait would have to see land; it reports that, and tells the pair's other CTA.
+  auto give_up = [&]() {
+    if (lane == 0) {
+      report_error(a.lists.err, kErrTimeout);
+      *abort_flag = 1;
+      if (kPair) st_cluster_u32(map_to_rank(smem_u32(const_cast<const int*>(abort_flag)), rank ^ 1), 1);
+    }
+  };
+#ifdef MLA_STALL_TEST
+  const int stall = static_cast<int>(blockIdx.x) == (g_scores_stall < 0) ? abs(g_scores_stall) : 0;
+#else
+  constexpr int stall = 0, kStallQueries = 0;
+#endif
   auto arrive_even = [&](int i) {   // at the even CTA's barrier
     if (kPair) mbar_arrive_remote(map_to_rank(bar(i), 0)); else mbar_arrive(bar(i));
   };
@@ -299,7 +322,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (!__any_sync(~0u, t.enters)) continue;
 #pragma unroll
       for (int g = 0; g < kQGroups; ++g) {
-        ok &= spin(F::kQEmpty + g, (visit & 1) ^ 1);
+        // (armed again while its last copy was still expected, a barrier would count wrongly)
+        ok = ok && __all_sync(~0u, spin(F::kQEmpty + g, (visit & 1) ^ 1));
+        if (!ok) continue;
         const int y = t.row * a.heads + rank * held, full = F::kQFull + g;
         const int bytes = (g < kQGroups - 1 ? kQPanels : 1) * q_panel * F::kCtas;
         const void* map = g < kQGroups - 1 ? &map_qn : &map_qp;
@@ -307,14 +332,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         __syncwarp();
         const uint32_t dst = q_base + g * kQPanels * q_panel;
         const int z = g < kQGroups - 1 ? g * kQPanels : 0;
+        if (stall && visit == 0 && stall == kStallQueries + g) continue;
         if (kPair) tma_load_3d_pair_elect(dst, map, 0, y, z, map_to_rank(bar(full), 0));
         else tma_load_3d_elect(dst, map, 0, y, z, bar(full));
       }
-      ok = __all_sync(~0u, ok);
       ++visit;
     }
-    if (!ok && lane == 0) report_error(a.lists.err, kErrTimeout);
-    if (rank == 0 && lane == 0) {   // every copy issued has landed before the CTA leaves
+    if (!ok) give_up();
+    if (ok && rank == 0 && lane == 0) {   // every copy issued has landed before the CTA leaves
 #pragma unroll 1
       for (int g = 0; g < kQGroups && visit > 0; ++g) {
         const uint32_t b = bar(F::kQFull + g), parity = (visit - 1) & 1;
@@ -338,10 +363,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     };
     int turn = set, slot = set % kStages, phase = 1;        // the set's next chunk: its number, slot and phase
     int landing = set % kStages, pending = 0, first = 0;    // first: number of the tile's first chunk
+    int landed = set - 1;                                   // chunks landed, of both sets
     auto land = [&]() {   // the set's oldest chunk in flight is in place
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_even(F::kFull + landing);
+      landed += 2;
+      if (lane == 0 && !(stall && stall == landed)) arrive_even(F::kFull + landing);
       landing += 2;
       if (landing >= kStages) landing -= kStages;
       --pending;
@@ -380,7 +407,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     cp_async_wait<0>();
     while (ok && pending > 0) land();
-    if (!ok && lane == 0) report_error(a.lists.err, kErrTimeout);
+    if (!ok) give_up();
   } else if (warp == 1) {
     // ---------------- MMAs (a pair: in its even CTA) ----------------
     const uint32_t idesc = idesc_bf16_f32(kTilePages * F::kCtas, held * F::kCtas, false, false);
@@ -403,12 +430,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           else mma_ss_elect(tmem + acc * kMaxHeads, da + 2 * kk, dq + 2 * kk, idesc, (c | kk) != 0);
         }
         commit(F::kEmpty + c);
-        if (leaves && (c % kQPanels == kQPanels - 1 || c == kChunks - 1)) commit(F::kQEmpty + c / kQPanels);
+        if (leaves && (c % kQPanels == kQPanels - 1 || c == kChunks - 1)) {
+          // (not where the issuing lane's wait ran out: their copy may still be expected)
+          const uint32_t empty = bar(F::kQEmpty + c / kQPanels);
+          if (kPair) commit_pair_elect_if(empty, 3, ok); else mma_commit_elect_if(empty, ok);
+        }
       }
       commit(F::kTFull + acc);
       ok = __all_sync(~0u, ok);
     }
-    if (!ok && lane == 0) report_error(a.lists.err, kErrTimeout);
+    if (!ok) give_up();
     if (rank == 0) {
       commit(F::kFinal, 1);   // every MMA issued completes before TMEM is freed
       if (lane == 0) {
@@ -448,7 +479,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         a.scores[t.row * a.stride + t.page0 + p] = best;
       }
     }
-    if (!ok && lane == 0) report_error(a.lists.err, kErrTimeout);
+    if (!ok) give_up();
   }
   tc_fence_before();
   if (kPair) cluster_sync_all(); else __syncthreads();   // (a pair: neither reads the other's memory any more)
@@ -456,6 +487,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     tc_fence_after();
     if (kPair) tmem_dealloc_pair(tmem, 2 * kMaxHeads);
     else tmem_dealloc(tmem, 2 * kMaxHeads);
+  } else if (warp == 0 && *abort_flag) {
+    // Where a wait ran out, here or in the pair's other CTA, copies of queries
+    // may be on their way whose barrier nobody waited for: no more are issued
+    // now, and the shared memory is held until they must have landed.
+    pause_ns(kDrainLimitNs);
   }
 }
 
@@ -697,6 +733,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
 }  // namespace mla
 
 using namespace mla;
+
+#ifdef MLA_STALL_TEST
+// Test build only: the signal or copy that a CTA of scores_kernel leaves out (0: none).
+extern "C" int mla_test_set_scores_stall(int n) {
+  return static_cast<int>(cudaMemcpyToSymbol(g_scores_stall, &n, sizeof(n)));
+}
+#endif
 
 extern "C" mla_status_t mla_page_scores(const void* q_nope, const void* q_pe, const void* summaries, int num_pages,
                                         const int32_t* kv_indptr, const int32_t* kv_indices, int64_t n_indices,
