@@ -781,6 +781,9 @@ class MLASparseDecoder:
         self.sel_indices = torch.zeros(self.max_batch * self.top_k, dtype=torch.int32, device=dev)
         self._sel_indptr = torch.zeros(self.max_batch + 1, dtype=torch.int32, device=dev)
         self._kv_indptr = torch.zeros(self.max_batch + 1, dtype=torch.int32, device=dev)
+        # the offsets on their way there: written again once the last upload has read them
+        self._staged_indptr = torch.zeros(self.max_batch + 1, dtype=torch.int32, pin_memory=True)
+        self._uploaded = torch.cuda.Event()
         self._scores = torch.empty((self.max_batch, self.max_pages), dtype=torch.float32, device=dev)
         self._kv_indices, self.sel_indptr, self.batch = None, None, 0
         torch.cuda.current_stream().synchronize()   # the zeros are in place for a run on any stream
@@ -788,7 +791,8 @@ class MLASparseDecoder:
     def plan(self, kv_indptr, kv_indices, kv_len, page_size: int, sm_scale: float, stream=None,
              q_len: int = 0) -> None:
         """Arguments as for ``MLADecoder.plan``: the whole page lists, of which
-        run() reads the selected pages."""
+        run() reads the selected pages.  Like that plan it queues its uploads on
+        the stream and waits for those of the plan before it alone."""
         import torch
         indptr, lens = _i32_host(kv_indptr), _i32_host(kv_len)
         if lens.ndim != 1 or indptr.shape != (lens.shape[0] + 1,):
@@ -814,10 +818,13 @@ class MLASparseDecoder:
         sel_len = (lens - (pages - kept) * page_size).astype(np.int32)
         self.decoder.plan(sel_indptr, self.sel_indices, sel_len, page_size, sm_scale, stream=stream, q_len=q_len)
         # rows past the batch get empty lists: a graph of a larger batch replays this plan
-        whole = np.full(self.max_batch + 1, indptr[-1], np.int32)
+        self._uploaded.synchronize()
+        whole = self._staged_indptr.numpy()
         whole[:batch + 1] = indptr
+        whole[batch + 1:] = indptr[-1]
         with torch.cuda.stream(torch.cuda.current_stream() if stream is None else _torch_stream(stream)):
-            self._kv_indptr.copy_(torch.from_numpy(whole))
+            self._kv_indptr.copy_(self._staged_indptr, non_blocking=True)
+            self._uploaded.record()
         self._kv_indices, self.batch = kv_indices, batch   # keep the borrowed page list alive
         self.sel_indptr = self._sel_indptr[:batch + 1]   # device offsets of the selected pages, after a run
         # the arguments of run()'s calls that stay as they are.  A captured run keeps

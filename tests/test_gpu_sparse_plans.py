@@ -79,3 +79,35 @@ def test_replay_reads_a_longer_list_than_was_captured(offset):
             assert torch.equal(w.out, out) and torch.equal(w.lse, lse), lens
     finally:
         dec.close()
+
+
+def test_plan_does_not_wait_for_the_stream():
+    """A plan returns while earlier work of its stream is still running, and the runs queued around it each see
+    their own plan."""
+    w = World(2)
+    side = torch.cuda.Stream()
+    dec = mla.MLASparseDecoder(2, H, W, 6, 1, 1)
+    first, second = [300, 40], [17, 380]
+    try:
+        dec.plan(indptr_of(first), w.ids, first, P, 0.07, stream=side)
+        with torch.cuda.stream(side):
+            w.run(dec)                                   # (loads the kernels)
+        torch.cuda.synchronize()
+        made = []
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1 << 29)                   # some tenths of a second
+            busy = torch.cuda.Event()
+            busy.record()
+            dec.plan(indptr_of(second), w.ids, second, P, 0.07, stream=side)
+            assert not busy.query()
+            made.append([t.clone() for t in w.run(dec)])
+            # (this one may wait for the upload of the plan before it)
+            dec.plan(indptr_of(first), w.ids, first, P, 0.07, stream=side)
+            made.append([t.clone() for t in w.run(dec)])
+        torch.cuda.synchronize()
+        dec.check_status()
+        for lens, (out, lse) in zip((second, first), made):
+            ref, ref_lse = w.expect(lens, w.ids)
+            assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    finally:
+        dec.close()
