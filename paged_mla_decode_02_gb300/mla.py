@@ -755,7 +755,8 @@ class MLASparseDecoder:
     step or layer: mla_page_scores, mla_select_pages, then the decode over the
     selected pages, all queued on the stream without synchronisation.
 
-    Holds lists of up to ``max_pages`` pages for each of ``max_batch`` requests.
+    Holds lists of up to ``max_pages`` pages for each of ``max_batch`` requests
+    (of which a plan takes at most 4096, and batch x top_k <= 2^31 - 1).
     A captured run replays after re-plans of at most the captured batch and of
     the captured q_len; like a decode plan's graph it keeps the addresses it was
     captured with, that of the page list included.  The list may be passed
@@ -805,6 +806,8 @@ class MLASparseDecoder:
             raise ValueError("kv_indptr must count ceil(kv_len / page_size) pages for each request")
         if batch > self.max_batch or np.any(pages > self.max_pages):
             raise MLAError(ERR_CAPACITY, "the batch exceeds the decoder's max_batch or max_pages")
+        if batch > 4096 or batch * self.top_k > 2 ** 31 - 1:   # what the scores and the selection take
+            raise MLAError(ERR_CAPACITY, "more than 4096 requests, or batch x top_k past 2^31 - 1")
         _on_device(torch.cuda.current_device(), torch.int32, "kv_indices", kv_indices)
         if kv_indices.numel() < indptr[-1]:
             raise ValueError("kv_indices is shorter than kv_indptr says")

@@ -111,3 +111,28 @@ def test_plan_does_not_wait_for_the_stream():
             assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
     finally:
         dec.close()
+
+
+def test_plan_refuses_what_its_runs_would():
+    """More requests, or more kept pages, than the scores and the selection take: refused by the plan, which leaves
+    the one before it in place."""
+    w = World(3)
+    dec = mla.MLASparseDecoder(4097, 1, 1, 1, 0, 1)      # (the kept pages of 4097 requests, or of several query tokens each)
+    try:
+        dec.plan([0, 1], w.ids, [16], P, 0.07)
+        with pytest.raises(mla.MLAError) as ei:
+            dec.plan(np.zeros(4098, np.int32), w.ids, [0] * 4097, P, 0.07)
+        assert ei.value.status == mla.ERR_CAPACITY
+        q = torch.zeros((1, 1, 576), dtype=torch.bfloat16, device="cuda")
+        out, _ = dec.run(q[..., :512].contiguous(), q[..., 512:].contiguous(), w.cc, w.kc, w.summaries,
+                         out_dtype=torch.float32)
+        dec.check_status()
+        # equal logits: the mean of the page's 16 rows, bf16 probabilities
+        ref = w.cc[w.ids[0].long()].double().mean(0)
+        assert float((out[0, 0].double() - ref).abs().max()) <= 1e-2
+        dec.top_k = 2 ** 30                              # as if it held so many (16 GB)
+        with pytest.raises(mla.MLAError) as ei:
+            dec.plan([0, 0, 0], w.ids, [0, 0], P, 0.07)
+        assert ei.value.status == mla.ERR_CAPACITY
+    finally:
+        dec.close()
