@@ -120,8 +120,10 @@ typedef struct {
  *   q_pe_out[t, h]           = bf16(scale * rotate(q_pe[t, h]))
  *   ckv_cache[slots[t]]      = round(ckv[t] * norm_weight / sqrt(mean(ckv[t]^2) + eps) / kv_scale)
  *   kpe_cache[slots[t]]      = round(scale * rotate(kpe[t]) / kv_scale)
- * computed in fp32 (angles reduced exactly to one turn first) and rounded
- * once to the cache's type; an e4m3 cache saturates at +-448 and keeps NaN.
+ * computed in fp32 and rounded once to the cache's type; an e4m3 cache
+ * saturates at +-448 and keeps NaN.  Angles are first reduced to one turn, to
+ * within 2^-31 turns at any position for frequencies up to 2^40 in magnitude
+ * (larger ones lose up to a bit for each doubling).
  * (The squares are summed in fp32: latent values past about 1e17 overflow it.)
  * A token with slots[t] < 0 is padding: nothing of it is written.  A slot
  * past the cache is reported (MLA_ERR_DEVICE_BOUNDS) and nothing of its token

@@ -6,7 +6,27 @@ written from the definitions in include/mla_paging.h.
 """
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
+
+
+def _pi() -> Fraction:
+    """Pi to more than 150 digits, by Machin's formula."""
+    unit = 10 ** 170
+
+    def arctan_of_inverse(n):
+        term, k, total = unit // n, 1, 0
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    return Fraction(4 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239)), unit)
+
+
+PI = _pi()
 
 
 def build_tables(kv_len, new_len, block_table, free_pages, free_count, page_size, indices_cap, max_tokens):
@@ -67,7 +87,8 @@ def rotate(x, positions, inv_freq, axis_of_pair, interleaved, scale=1.0):
     out = np.array(x, np.float64)
     for i in range(32):
         # whole turns are taken off the exact product before cos and sin
-        angle = float(int(positions[axis_of_pair[i]])) * float(inv_freq[i])
+        turns = int(positions[axis_of_pair[i]]) * Fraction(float(inv_freq[i])) / (2 * PI)
+        angle = float((turns - round(turns)) * 2 * PI)
         c, s = scale * np.cos(angle), scale * np.sin(angle)
         a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + 32)
         out[..., a] = x[..., a] * c - x[..., b] * s

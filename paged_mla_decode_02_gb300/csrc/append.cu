@@ -5,10 +5,12 @@
 // Rotation: pair i of a row turns by pos * f_i radians.  Far positions need
 // that product modulo one turn to more bits than fp32 has, so the host turns
 // f_i into a 64-bit fixed-point fraction of a turn, F_i = f_i / 2 pi * 2^64,
-// and the kernel multiplies pos * F_i in wrapping 64-bit integers: the whole
-// turns fall off the top exactly, and the product is off by at most |pos|
-// units of 2^-64 turns.  Its upper 32 bits, signed, are the angle in
-// [-1/2, 1/2) turns that sincospi takes.
+// good to two units for |f_i| up to 2^40 (fraction_of_turn), and the kernel
+// multiplies pos * F_i in wrapping 64-bit integers: the whole turns fall off the
+// top exactly, and the product is off by at most 2 |pos| units of 2^-64 turns,
+// 2^-32 turns at the largest.  Its upper 32 bits, signed, are the angle in
+// [-1/2, 1/2) turns that sincospi takes: off by less than 2^-31 turns with what
+// lies below them, where fp32 itself, which holds 24 bits of it, is off by 2^-26.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -394,6 +396,22 @@ __global__ void __launch_bounds__(kSumThreads, sum_blocks(kFp8)) summarize_kerne
   }
 }
 
+// frequency / 2 pi, a fraction of a turn in units of 2^-64.  1 / 2 pi is taken
+// as the double next to it and the double next to what that leaves (together
+// within 2^-110), the first product with the rounding that fma recovers, and
+// each of the three terms is rounded once, after its whole turns are off.
+uint64_t fraction_of_turn(double frequency) {
+  constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;
+  const double turns = frequency * kHigh;
+  const double terms[3] = {turns, std::fma(frequency, kHigh, -turns), frequency * kLow};
+  uint64_t sum = 0;
+  for (const double t : terms) {
+    const double units = std::nearbyint((t - std::nearbyint(t)) * 0x1p64);   // at most 2^63 either way
+    sum += units < 0 ? uint64_t{0} - static_cast<uint64_t>(-units) : static_cast<uint64_t>(units);
+  }
+  return sum;
+}
+
 bool cache_args(const void* ckv_cache, const void* kpe_cache, int kv_dtype, float kv_scale, int num_pages,
                 int page_size, mla_status_t* st) {
   *st = MLA_ERR_INVALID_ARG;
@@ -426,10 +444,7 @@ extern "C" mla_status_t mla_rope_append(const mla_rope_t* rope, const int32_t* p
   for (int i = 0; i < kPairs; ++i) {
     if (rope->axis_of_pair[i] < 0 || rope->axis_of_pair[i] >= rope->n_axes || !std::isfinite(rope->inv_freq[i]))
       return MLA_ERR_INVALID_ARG;
-    const double turns = rope->inv_freq[i] * 0.15915494309189533577;   // 1 / 2 pi
-    double part = turns - std::floor(turns);                          // whole turns per position fall away
-    if (part >= 1.0) part = 0.0;                                      // a tiny negative frequency rounds up to one
-    a.rope.turn[i] = static_cast<uint64_t>(std::ldexp(part, 64));
+    a.rope.turn[i] = fraction_of_turn(rope->inv_freq[i]);
     a.rope.axis[i] = static_cast<uint8_t>(rope->axis_of_pair[i]);
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
