@@ -124,7 +124,6 @@ typedef struct {
  * saturates at +-448 and keeps NaN.  Angles are first reduced to one turn, to
  * within 2^-31 turns at any position for frequencies up to 2^40 in magnitude
  * (larger ones lose up to a bit for each doubling).
- * (The squares are summed in fp32: latent values past about 1e17 overflow it.)
  * A token with slots[t] < 0 is padding: nothing of it is written.  A slot
  * past the cache is reported (MLA_ERR_DEVICE_BOUNDS) and nothing of its token
  * is written either.  No two tokens may have the same slot.

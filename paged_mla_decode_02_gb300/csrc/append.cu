@@ -228,14 +228,30 @@ __global__ void __launch_bounds__(kQThreads, 4) append_kernel(const __grid_const
     if (lane == 0) report_error(a.err, kErrBounds);
     return;
   }
-  float sq = 0.f;
+  float r = 1.f;
+  if (a.weight) {
+    auto mean_square = [&]() {
+      float sq = 0.f;
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sq += x[j][k] * x[j][k];
+        for (int k = 0; k < 8; ++k) sq += x[j][k] * x[j][k];
 #pragma unroll
-  for (int d = 16; d; d >>= 1) sq += __shfl_xor_sync(~0u, sq, d);
-  const float r = a.weight ? rsqrtf(sq * (1.f / kDCkv) + a.eps) : 1.f;
+      for (int d = 16; d; d >>= 1) sq += __shfl_xor_sync(~0u, sq, d);
+      return sq * (1.f / kDCkv);
+    };
+    float eps = a.eps, of = mean_square() + eps;
+    if (of < 0x1p-100f || of == INFINITY) {   // squares that fp32 does not hold: of the row times a power of two
+      const float up = of < 1.f ? 0x1p100f : 0x1p-100f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[j][k] *= up;
+      eps = eps * up * up;
+      of = mean_square() + eps;
+    }
+    r = rsqrtf(of);
+  }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (a.weight) {
