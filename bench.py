@@ -588,7 +588,9 @@ def run_sparse(args) -> None:
     """One serving step over long caches: page tables from the lengths, rope
     append of the new tokens, summaries of the pages they complete, then the
     sparse decode (page scores, selection, decode over the selected pages) of
-    64 requests x 32768 tokens, 128 heads, 64 of 512 pages read."""
+    64 requests x 32768 tokens, 128 heads, 64 of 512 pages read.  The step is
+    planned before it is timed, as a step's layers share one plan; what a plan
+    takes on the host is printed beside it (plan_us)."""
     import torch
     from paged_mla_decode_02_gb300 import build as B
     from paged_mla_decode_02_gb300 import mla
@@ -659,6 +661,13 @@ def run_sparse(args) -> None:
     dec.check_status()
     us = statistics.mean(a.elapsed_time(b) for a, b in ev) * 1000.0
 
+    plan = []
+    for _ in range(20):
+        t0 = time.perf_counter()
+        dec.plan(host_indptr, indices, np.full(Bq, SPARSE_TOKENS + new, np.int32), P, sm_scale, stream=stream)
+        plan.append((time.perf_counter() - t0) * 1e6)
+        stream.synchronize()
+
     # end to end: the step's queries and latent rows from pinned host memory in, output and lse back
     ins = [(t, t.cpu().pin_memory()) for t in (kv_new, q_nope, q_rope)]
     out_h, lse_h = (torch.empty(t.shape, dtype=t.dtype).pin_memory() for t in (out, lse))
@@ -702,6 +711,7 @@ def run_sparse(args) -> None:
             "e2e": {"value": statistics.mean(e2e), "unit": UNIT,
                     "h2d_bytes_per_step": int(sum(h.numel() * h.element_size() for _, h in ins)),
                     "d2h_bytes_per_step": int(out.numel() * 2 + lse.numel() * 4)},
+            "plan_us": statistics.median(plan),
             "gpu_launches": (5 + RUN_LAUNCHES[dec.decoder.info()["kernel"]]) * args.steps, "cuda_graph": True}
     print(json.dumps(line), flush=True)
     dec.close()
