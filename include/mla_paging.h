@@ -21,6 +21,14 @@
  * call throws, exits or traps.  Calls on different streams may overlap as
  * long as none writes what another reads or writes.
  *
+ * The lengths that a step makes on the device are not read back: a decode is
+ * planned from HOST offsets and lengths (mla_decode_plan), so the caller keeps
+ * the lengths of its requests as well, and adds to them what it asks
+ * mla_build_tables for.  A step that mla_build_tables refuses shows in its
+ * status word alone.  Nothing of its tokens is written then (their slots are
+ * -1), and a decode planned for the lengths it asked for reads page lists that
+ * were not made: read the status before such a step's results are used.
+ *
  * check_status != 0 waits for the stream and returns the first device error
  * recorded on this device since the last such call (MLA_ERR_DEVICE_BOUNDS: an
  * index outside its array, whose access was skipped; MLA_ERR_DEVICE_TIMEOUT: a

@@ -44,8 +44,8 @@ __device__ __forceinline__ int list_of(const Lists& l, int r, int* first) {
 // A row's scores are the row maxima of S = summaries[pages] . q^T, a product
 // of M = pages, N = heads, K = 576 that reads 1152 bytes per page: bound by
 // HBM, and next by what passes from L2 to the SMs.  The rows' lists are cut
-// into tiles of up to 128 pages, and each CTA takes an even share of the tiles
-// in order.  (Few or short lists make smaller tiles, so that all SMs take
+// into tiles of up to 128 pages, and the CTAs take whole tiles in order, some one
+// more than others.  (Few or short lists make smaller tiles, so that all SMs take
 // part: the size, of four, with the least estimated time of the fullest CTA.)
 // - One warp copies a row's queries into shared memory by TMA, in nine panels
 //   of 64 dims that stay for all tiles of the row (and make way, four by four,
@@ -61,9 +61,11 @@ __device__ __forceinline__ int list_of(const Lists& l, int r, int* first) {
 // by a CTA pair (kPair, cta_group::2): tiles have up to 256 pages, halved
 // between the two CTAs, as are the heads of the queries that each holds, and
 // the even CTA issues MMAs of M = 256 that read both.
-// Measured: 64 rows x 1024 pages x 128 heads, 85 MB, 17.8 us (4.8 TB/s, of
-// which about 5 us until the first tile has arrived; then the rate of HBM);
-// 4 rows x 100 pages x 16 heads 5.7 us.
+// Measured: 64 rows x 1024 pages x 128 heads, 85 MB, 17.7 us (4.8 TB/s, of
+// which about 5 us until the first tile has arrived; then the rate of HBM, at
+// which 28 of the 76 pairs take four tiles and the others three: 19 % above the
+// mean); with 16 heads, 77 MB, 16.4 us (152 CTAs, four tiles of 128 for 56 of
+// them); 4 rows x 100 pages x 16 heads 5.7 us.
 struct ScoreArgs {
   const char* summaries;
   int num_pages;

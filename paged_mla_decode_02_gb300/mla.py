@@ -519,7 +519,9 @@ def mla_build_tables(kv_len, new_len, block_table, free_pages, free_count, page_
     new_len [B]; block_table [B, max_pages] (rows may be strided); free_pages
     [num_pages]; outputs kv_indptr, q_indptr [B + 1], kv_indices, slots
     (int64), positions, status [1].  Without kv_len_out / free_count_out the
-    lengths and the count are updated in place."""
+    lengths and the count are updated in place.  Decodes are planned from host
+    lengths: the caller keeps those as well, and reads ``status`` to learn of a
+    step that was refused."""
     import torch
     if kv_len_out is None:
         kv_len_out = kv_len
