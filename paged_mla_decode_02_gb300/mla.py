@@ -322,10 +322,10 @@ def mla_merge_states(o_a, lse_a, o_b, lse_b, out, lse_out, stream=None) -> None:
 
 
 def _check_layouts(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, page_size=None) -> None:
-    """The shapes mla_decode.h documents, checked before the library reads
-    through the raw pointers: the cache [pages, page_size, 512] and [pages,
-    page_size, 64] of one dtype, q [..., 512] / [..., 64], out [..., 512] and
-    lse [...] over the same leading dims."""
+    """The shapes and types mla_decode.h documents, checked before the library
+    reads and writes through the raw pointers: the cache [pages, page_size, 512]
+    and [pages, page_size, 64] of one dtype, q [..., 512] / [..., 64] of one
+    dtype, out [..., 512] and fp32 lse [...] over the same leading dims."""
     cache, q = ckv_cache.shape, q_nope.shape
     if len(cache) != 3 or cache[2] != 512:
         raise ValueError(f"ckv_cache must be [num_pages, page_size, 512], got {tuple(cache)}")
@@ -341,6 +341,10 @@ def _check_layouts(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, page_size=None)
         raise ValueError("q_nope must be [..., 512] and q_pe [..., 64] over the same leading dims")
     if out.shape != q or lse.shape != lead:
         raise ValueError("out must be [..., 512] and lse [...] over q_nope's leading dims")
+    if q_pe.dtype != q_nope.dtype:
+        raise ValueError(f"q_pe must have q_nope's dtype, got {q_pe.dtype}")
+    if _dtype_code(lse, "lse") != DTYPE_FP32:
+        raise ValueError(f"lse must be float32, got {lse.dtype}")
 
 
 def mla_decode_run(plan, q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale: float = 1.0,
