@@ -885,7 +885,7 @@ class MLASparseDecoder:
     def check_status(self) -> int:
         """Synchronise and raise on a device error of the decode, or of any call of
         mla_paging.h on this device since the last check: those calls and all
-        decoders share one word, which the first to ask reads and clears."""
+        sparse decoders share one word, which the first to ask reads and clears."""
         import torch
         torch.cuda.synchronize()
         # a call of no rows queues nothing and reports what the kernels recorded
