@@ -55,16 +55,38 @@ typedef enum {
 typedef enum {
   MLA_DTYPE_BF16 = 0,
   MLA_DTYPE_FP8_E4M3 = 1,     /* OCP E4M3 ("e4m3fn"), value = code * kv_scale */
-  MLA_DTYPE_FP32 = 2
+  MLA_DTYPE_FP32 = 2,
+  MLA_DTYPE_FP16 = 3,         /* rows given to or taken from a cache (mla_paging.h) */
+  MLA_DTYPE_Q4 = 4            /* a 4-bit cache; its rows are described below */
 } mla_dtype_t;
+
+/*
+ * A 4-bit cache is one array, uint8 [num_pages, page_size, MLA_Q4_ROW_BYTES]:
+ * a row holds a token's 576 values (the 512 of ckv, then the 64 of kpe) in 18
+ * groups of 32 dims that follow each other.  A value is
+ *   +- m * 2^(E - k),   m one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (index 0 .. 7),
+ * with an exponent E of the row and a shift k of the group.
+ *   bytes 0 .. 287    72 little-endian words of 8 dims: the index of dim i's
+ *                     magnitude in bits 4i .. 4i + 2; the sign of dim i in bit
+ *                     8i + 7 (i < 4) or 8 (i - 4) + 3 (i >= 4)
+ *   bytes 288 .. 296  the shifts, 4 bits each, lower half first; 0 .. 14
+ *   byte 297          E + 127, E in -32 .. 63; 255: the row held a NaN, and
+ *                     all its values are NaN
+ *   bytes 298 .. 303  zero
+ * mla_quantize_append writes such rows.  Rows that were written otherwise must
+ * keep to these ranges: with other exponents or shifts the results are
+ * undefined numbers (never an access out of place).
+ */
+#define MLA_Q4_ROW_BYTES 304
 
 typedef enum {
   MLA_KERNEL_DEFAULT = 0,     /* MLA_KERNEL_PAIR (an fp8 cache with 16-token pages runs on
                                  the tcgen05 kernel over the same plan, which rejects it) */
   MLA_KERNEL_TCGEN05 = 1,     /* one-CTA tcgen05 / TMEM kernel (bf16 and fp8 caches) */
   MLA_KERNEL_MMA_SYNC = 2,    /* warp-level mma.sync kernel (legacy tensor path, for comparison) */
-  MLA_KERNEL_PAIR = 3         /* tcgen05 kernel whose MMAs span a CTA pair (cta_group::2); bf16
+  MLA_KERNEL_PAIR = 3,        /* tcgen05 kernel whose MMAs span a CTA pair (cta_group::2); bf16
                                  caches, and fp8 caches with page_size >= 32 (e4m3 MMAs) */
+  MLA_KERNEL_Q4 = 4           /* 4-bit caches: a plan of this kernel is run by mla_decode_run_q4 */
 } mla_kernel_t;
 
 /* Plan statistics, filled by mla_plan_info. */
@@ -204,6 +226,21 @@ mla_status_t mla_decode_run(mla_plan_t plan, const void* q_nope, const void* q_p
                             int q_dtype, const void* ckv_cache, const void* kpe_cache,
                             int kv_dtype, float kv_scale, int num_pages, void* out,
                             int out_dtype, float* lse, void* stream);
+
+/*
+ * Run the planned batch over a 4-bit cache.  The plan was created with
+ * MLA_KERNEL_Q4 (else MLA_ERR_UNSUPPORTED, as mla_decode_run is for such a
+ * plan).  Arguments as for mla_decode_run, but for the cache:
+ *   cache     [num_pages, page_size, MLA_Q4_ROW_BYTES] uint8, 16-byte aligned
+ * Rows behind a request's last token may hold anything.  Everything that
+ * mla_decode_run says of page sizes, launches, graphs, errors and bad page ids
+ * holds here too; a row that held a NaN makes its request's results NaN.  With
+ * q_len * num_heads <= 128 the q_len query tokens of mla_decode_plan_multi
+ * share one pass over their request's rows.
+ */
+mla_status_t mla_decode_run_q4(mla_plan_t plan, const void* q_nope, const void* q_pe, int q_dtype,
+                               const void* cache, int num_pages, void* out, int out_dtype,
+                               float* lse, void* stream);
 
 /*
  * One whole decode step from HOST buffers: copies q_nope / q_pe from host to

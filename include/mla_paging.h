@@ -12,6 +12,8 @@
  *   mla_page_scores      a page's best score over the heads of a query
  *   mla_select_pages     the pages of the best scores, as a page list that
  *                        mla_decode_plan takes
+ *   mla_quantize_append  rows written into a 4-bit cache
+ *   mla_read_cache       rows read back out of a paged cache of any type
  *
  * Conventions, as in mla_decode.h: device pointers of the current device
  * owned by the caller; every call queues its work on `stream`, allocates
@@ -232,6 +234,62 @@ mla_status_t mla_select_pages(const float* scores, int64_t score_stride, int64_t
                               int64_t n_indices, int rows, int top_k, int keep_first,
                               int keep_last, int32_t* sel_indptr, int32_t* sel_indices,
                               int64_t sel_cap, int check_status, void* stream);
+
+/*
+ * Rows into a 4-bit cache (its layout: mla_decode.h, MLA_Q4_ROW_BYTES).
+ * For each token t with slots[t] >= 0, of its 576 values (ckv[t], then kpe[t])
+ * in 18 groups of 32, in exact arithmetic:
+ *   e_g  = the least e with max |x| <= 6 * 2^e over group g (none for a group
+ *          of zeros)
+ *   E    = max e_g, brought into -32 .. 63
+ *   k_g  = E - e_g, brought into 0 .. 14; 14 for a group of zeros
+ *   code = x / 2^(E - k_g) rounded to the nearest magnitude, ties to the even
+ *          index, what lies past 6 to 6; with x's sign
+ * A row with a NaN is marked as such, its codes and shifts are 0.
+ * A token with slots[t] < 0 is padding: nothing of it is written.  A slot
+ * past the cache is reported (MLA_ERR_DEVICE_BOUNDS) and its row not written.
+ * No two tokens may have the same slot.
+ *   ckv, kpe     of row_dtype (BF16, FP16 or FP32), element (t, d) at t *
+ *                stride + d; both and their rows 16-byte aligned
+ *   slots        [tokens] int64
+ *   cache        [num_pages, page_size, MLA_Q4_ROW_BYTES] uint8, 16-byte aligned
+ * page_size 16, 32 or 64; tokens <= 2^24 (else MLA_ERR_CAPACITY).
+ * Rows to be turned or normed first go through mla_rope_append into a bf16
+ * cache of the step's tokens (slots 0, 1, ..), whose rows this call then takes.
+ */
+mla_status_t mla_quantize_append(const void* ckv, int64_t ckv_stride, const void* kpe,
+                                 int64_t kpe_stride, int row_dtype, const int64_t* slots,
+                                 void* cache, int num_pages, int page_size, int64_t tokens,
+                                 int check_status, void* stream);
+
+/*
+ * Rows read back out of a paged cache, as a prefill over cached context takes
+ * them: request b's tokens starts[b], starts[b] + 1, .. become the rows
+ * row_indptr[b] .. row_indptr[b + 1] - 1 of the outputs, each value times
+ * kv_scale (FP8_E4M3), rounded once to out_dtype.
+ *   cache, kpe_cache  kv_dtype BF16 or FP8_E4M3: the two parts, as for
+ *                mla_decode_run; Q4: cache is the 4-bit cache, kpe_cache NULL
+ *   kv_scale     as in mla_decode_run (FP8_E4M3 only)
+ *   kv_indptr    [batch + 1] int32 and kv_indices [n_indices] int32, DEVICE:
+ *                the page lists
+ *   starts       [batch] int32, DEVICE: the first token of each, >= 0
+ *   row_indptr   [batch + 1] int32, DEVICE, from 0 on and never decreasing
+ *   ckv_out      element (r, d) at r * ckv_stride + d, d < 512; kpe_out alike,
+ *                d < 64; of out_dtype (BF16, FP16, FP32), rows 16-byte aligned
+ *   max_rows     rows of the outputs; those from row_indptr[batch] on are left
+ *                as they were
+ * A row whose token lies outside its request's pages, or whose page id lies
+ * outside [0, num_pages), is reported (MLA_ERR_DEVICE_BOUNDS) and left as it
+ * was; so are rows that row_indptr places past max_rows.  Tokens behind a
+ * request's last one are read as the cache holds them.
+ * batch 0 .. 4096 and max_rows <= 2^31 - 1 (else MLA_ERR_CAPACITY).
+ */
+mla_status_t mla_read_cache(const void* cache, const void* kpe_cache, int kv_dtype, float kv_scale,
+                            int num_pages, int page_size, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, int64_t n_indices, const int32_t* starts,
+                            const int32_t* row_indptr, int batch, void* ckv_out,
+                            int64_t ckv_stride, void* kpe_out, int64_t kpe_stride, int out_dtype,
+                            int64_t max_rows, int check_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -84,6 +84,7 @@ int workers_for(int kernel, int num_sms, int num_heads) {
     const int w = 2 * num_sms / head_groups;
     return w < 1 ? 1 : w;
   }
+  if (kernel == MLA_KERNEL_Q4) return num_sms;   // a CTA per worker (and group of query rows)
   return num_sms / 2 < 1 ? 1 : num_sms / 2;   // one 2-CTA cluster per worker
 }
 
@@ -230,7 +231,7 @@ mla_status_t mla_plan_create(int max_batch, int num_heads, int kernel, mla_plan_
   *out = nullptr;
   if (max_batch < 1 || num_heads < 1 || num_heads > kMaxHeads) return MLA_ERR_INVALID_ARG;
   if (kernel != MLA_KERNEL_DEFAULT && kernel != MLA_KERNEL_TCGEN05 &&
-      kernel != MLA_KERNEL_MMA_SYNC && kernel != MLA_KERNEL_PAIR)
+      kernel != MLA_KERNEL_MMA_SYNC && kernel != MLA_KERNEL_PAIR && kernel != MLA_KERNEL_Q4)
     return MLA_ERR_INVALID_ARG;
   mla_plan_t p = new (std::nothrow) mla_plan_s();
   if (!p) return MLA_ERR_CUDA;
@@ -281,11 +282,11 @@ mla_status_t mla_plan_create(int max_batch, int num_heads, int kernel, mla_plan_
   p->off_wptr = align16(p->off_units + sizeof(WorkUnit) * p->units_cap);
   p->off_merge = align16(p->off_wptr + sizeof(int32_t) * (p->n_workers + 1));
   p->blob_bytes = align16(p->off_merge + sizeof(MergeEntry) * p->merge_cap);
-  // Partial shares: a row per (share, head).  A CTA-pair plan may pack up
+  // Partial shares: a row per (share, head).  A CTA-pair or 4-bit plan may pack up
   // to 128 rows per request (several query tokens), whose split units take
   // at most n_workers x 128 + max_batch x num_heads rows in all.
   p->part_rows_cap = static_cast<size_t>(p->slots_cap) * num_heads;
-  if (p->kernel == MLA_KERNEL_PAIR)
+  if (p->kernel == MLA_KERNEL_PAIR || p->kernel == MLA_KERNEL_Q4)
     p->part_rows_cap = static_cast<size_t>(p->n_workers) * kMaxHeads + static_cast<size_t>(max_batch) * num_heads;
   const size_t o_bytes = sizeof(float) * p->part_rows_cap * kDCkv;
   const size_t l_bytes = sizeof(float) * p->part_rows_cap * kLsePartCopies;
@@ -430,12 +431,13 @@ mla_status_t mla_decode_plan_multi(mla_plan_t plan, const int32_t* kv_indptr_hos
       return fail(plan, MLA_ERR_INVALID_ARG,
                   "every request must hold its q_len query tokens in the cache (kv_len >= q_len)");
   // Query j of request b sees the first kv_len - q_len + 1 + j tokens.  On
-  // the CTA-pair kernel, when q_len x heads <= 128, the q_len query tokens of
+  // the CTA-pair and the 4-bit kernel, when q_len x heads <= 128, the q_len query tokens of
   // a request share its MMA rows (row j * heads + h of the [batch, q_len *
   // heads] view of the query and output arrays, each row masked to its own
   // prefix), so its pages are read once (the plan's share buffers hold any
   // such partition; should one not fit, the form below is used).
-  if (plan->kernel == MLA_KERNEL_PAIR && q_len > 1 && q_len * num_heads <= kMaxHeads) {
+  if ((plan->kernel == MLA_KERNEL_PAIR || plan->kernel == MLA_KERNEL_Q4) && q_len > 1 &&
+      q_len * num_heads <= kMaxHeads) {
     st = plan_requests(plan, kv_indptr_host, kv_len_host, batch, kv_indices_dev, q_len * num_heads,
                        page_size, sm_scale, stream, q_len, num_heads);
     if (st != MLA_ERR_CAPACITY) return st;
@@ -454,12 +456,61 @@ mla_status_t mla_decode_plan_multi(mla_plan_t plan, const int32_t* kv_indptr_hos
                        page_size, sm_scale, stream);
 }
 
+namespace {
+
+// The decode kernels' arguments for a run of the plan.
+DecodeArgs decode_args(mla_plan_t plan, const void* q_nope, const void* q_pe, const void* ckv, const void* kpe,
+                       float kv_scale, int num_pages, void* out, float* lse) {
+  const char* blob = static_cast<const char*>(plan->d_blob);
+  DecodeArgs a{};
+  a.q_nope = q_nope;
+  a.q_pe = q_pe;
+  a.ckv = ckv;
+  a.kpe = kpe;
+  a.kv_indices = plan->kv_indices;
+  a.units = reinterpret_cast<const WorkUnit*>(blob + plan->off_units);
+  a.worker_ptr = reinterpret_cast<const int32_t*>(blob + plan->off_wptr);
+  a.params = reinterpret_cast<const PlanDev*>(blob);
+  a.out = out;
+  a.lse = lse;
+  a.o_part = plan->d_o_part;
+  a.lse_part = plan->d_lse_part;
+  a.merge = reinterpret_cast<const MergeEntry*>(blob + plan->off_merge);
+  a.counters = plan->d_counters;
+  a.err = plan->d_err;
+  a.num_pages = num_pages;
+  a.num_heads = plan->params.num_heads;   // rows per request (q_len x heads when packed)
+  a.kv_scale = kv_scale;                  // the dequantisation scale of fp8 codes only
+  a.units_cap = plan->units_cap;
+  a.n_workers = plan->n_workers;
+  return a;
+}
+
+// Combines the split requests of a run and fills the empty ones.
+mla_status_t merge_shares(mla_plan_t plan, const DecodeArgs& a, bool out_f32, cudaStream_t s) {
+  MergeArgs m{};
+  m.merge = a.merge;
+  m.params = a.params;
+  m.o_part = plan->d_o_part;
+  m.lse_part = plan->d_lse_part;
+  m.out = a.out;
+  m.lse = a.lse;
+  m.num_heads = plan->params.num_heads;
+  m.merge_cap = plan->merge_cap;
+  const cudaError_t e = launch_merge(m, out_f32, s);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(plan, e, "merge kernel launch");
+}
+
+}  // namespace
+
 mla_status_t mla_decode_run(mla_plan_t plan, const void* q_nope, const void* q_pe, int q_dtype,
                             const void* ckv_cache, const void* kpe_cache, int kv_dtype,
                             float kv_scale, int num_pages, void* out, int out_dtype, float* lse,
                             void* stream) {
   if (!plan) return MLA_ERR_INVALID_ARG;
   if (!plan->planned) return fail(plan, MLA_ERR_NOT_PLANNED, "mla_decode_run before mla_decode_plan");
+  if (plan->kernel == MLA_KERNEL_Q4)
+    return fail(plan, MLA_ERR_UNSUPPORTED, "a plan made for MLA_KERNEL_Q4 is run by mla_decode_run_q4");
   if (q_dtype != MLA_DTYPE_BF16)
     return fail(plan, MLA_ERR_UNSUPPORTED, "q_dtype must be MLA_DTYPE_BF16");
   if (kv_dtype != MLA_DTYPE_BF16 && kv_dtype != MLA_DTYPE_FP8_E4M3)
@@ -479,29 +530,7 @@ mla_status_t mla_decode_run(mla_plan_t plan, const void* q_nope, const void* q_p
   const bool out_f32 = out_dtype == MLA_DTYPE_FP32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-  const char* blob = static_cast<const char*>(plan->d_blob);
-  DecodeArgs a{};
-  a.q_nope = q_nope;
-  a.q_pe = q_pe;
-  a.ckv = ckv_cache;
-  a.kpe = kpe_cache;
-  a.kv_indices = plan->kv_indices;
-  a.units = reinterpret_cast<const WorkUnit*>(blob + plan->off_units);
-  a.worker_ptr = reinterpret_cast<const int32_t*>(blob + plan->off_wptr);
-  a.params = reinterpret_cast<const PlanDev*>(blob);
-  a.out = out;
-  a.lse = lse;
-  a.o_part = plan->d_o_part;
-  a.lse_part = plan->d_lse_part;
-  a.merge = reinterpret_cast<const MergeEntry*>(blob + plan->off_merge);
-  a.counters = plan->d_counters;
-  a.err = plan->d_err;
-  a.num_pages = num_pages;
-  a.num_heads = plan->params.num_heads;   // rows per request (q_len x heads when packed)
-  a.kv_scale = fp8 ? kv_scale : 1.f;   // the dequantisation scale of fp8 codes only
-  a.units_cap = plan->units_cap;
-  a.n_workers = plan->n_workers;
-
+  const DecodeArgs a = decode_args(plan, q_nope, q_pe, ckv_cache, kpe_cache, fp8 ? kv_scale : 1.f, num_pages, out, lse);
   cudaError_t e;
   if (plan->prof_start && (e = cudaEventRecord(plan->prof_start, s)) != cudaSuccess)
     return cuda_fail(plan, e, "cudaEventRecord");
@@ -538,18 +567,35 @@ mla_status_t mla_decode_run(mla_plan_t plan, const void* q_nope, const void* q_p
   // The one-CTA tcgen05 kernel combines split requests and fills empty ones
   // itself; after the others a merge kernel does it.
   if (kern == MLA_KERNEL_TCGEN05) return MLA_OK;
-  MergeArgs m{};
-  m.merge = reinterpret_cast<const MergeEntry*>(blob + plan->off_merge);
-  m.params = a.params;
-  m.o_part = plan->d_o_part;
-  m.lse_part = plan->d_lse_part;
-  m.out = out;
-  m.lse = lse;
-  m.num_heads = plan->params.num_heads;
-  m.merge_cap = plan->merge_cap;
-  e = launch_merge(m, out_f32, s);
-  if (e != cudaSuccess) return cuda_fail(plan, e, "merge kernel launch");
-  return MLA_OK;
+  return merge_shares(plan, a, out_f32, s);
+}
+
+mla_status_t mla_decode_run_q4(mla_plan_t plan, const void* q_nope, const void* q_pe, int q_dtype,
+                               const void* cache, int num_pages, void* out, int out_dtype, float* lse,
+                               void* stream) {
+  if (!plan) return MLA_ERR_INVALID_ARG;
+  if (!plan->planned) return fail(plan, MLA_ERR_NOT_PLANNED, "mla_decode_run_q4 before mla_decode_plan");
+  if (plan->kernel != MLA_KERNEL_Q4)
+    return fail(plan, MLA_ERR_UNSUPPORTED, "mla_decode_run_q4 takes a plan made for MLA_KERNEL_Q4");
+  if (q_dtype != MLA_DTYPE_BF16)
+    return fail(plan, MLA_ERR_UNSUPPORTED, "q_dtype must be MLA_DTYPE_BF16");
+  if (out_dtype != MLA_DTYPE_BF16 && out_dtype != MLA_DTYPE_FP32)
+    return fail(plan, MLA_ERR_UNSUPPORTED, "out_dtype must be BF16 or FP32");
+  if (!q_nope || !q_pe || !cache || !out || !lse) return fail(plan, MLA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (num_pages < 1) return fail(plan, MLA_ERR_INVALID_ARG, "num_pages must be >= 1");
+  if ((reinterpret_cast<uintptr_t>(cache) | reinterpret_cast<uintptr_t>(q_nope) |
+       reinterpret_cast<uintptr_t>(q_pe) | reinterpret_cast<uintptr_t>(out)) & 15)
+    return fail(plan, MLA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  const bool out_f32 = out_dtype == MLA_DTYPE_FP32;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const DecodeArgs a = decode_args(plan, q_nope, q_pe, cache, nullptr, 1.f, num_pages, out, lse);
+  cudaError_t e;
+  if (plan->prof_start && (e = cudaEventRecord(plan->prof_start, s)) != cudaSuccess)
+    return cuda_fail(plan, e, "cudaEventRecord");
+  if ((e = launch_decode_q4(a, out_f32, s)) != cudaSuccess) return cuda_fail(plan, e, "decode kernel launch");
+  if (plan->prof_stop && (e = cudaEventRecord(plan->prof_stop, s)) != cudaSuccess)
+    return cuda_fail(plan, e, "cudaEventRecord");
+  return merge_shares(plan, a, out_f32, s);
 }
 
 mla_status_t mla_decode_run_host(mla_plan_t plan, const void* q_nope_host, const void* q_pe_host,

@@ -105,6 +105,10 @@ bool encode_pair_maps(PairMaps* maps, const void* q_nope, const void* q_pe, cons
                       bool kv_fp8);
 cudaError_t decode_pair_max_workers(int* workers);
 
+// Decode over a 4-bit cache (a.ckv: its rows; kpe and kv_scale unused): units
+// and partials as for the CTA-pair kernel.
+cudaError_t launch_decode_q4(const DecodeArgs& a, bool out_f32, cudaStream_t s);
+
 // LSE merge of split partials (and zero-fill of empty requests); the mma.sync
 // and CTA-pair paths -- the one-CTA tcgen05 kernel merges in its own epilogue.
 cudaError_t launch_merge(const MergeArgs& a, bool out_f32, cudaStream_t s);

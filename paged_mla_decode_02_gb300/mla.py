@@ -25,18 +25,20 @@ LIB_PATH = os.path.join(PKG, "lib", "libmla_decode.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_CUDA, ERR_DEVICE_TIMEOUT, \
     ERR_DEVICE_BOUNDS, ERR_NOT_PLANNED = range(8)
 # mla_dtype_t
-DTYPE_BF16, DTYPE_FP8_E4M3, DTYPE_FP32 = 0, 1, 2
+DTYPE_BF16, DTYPE_FP8_E4M3, DTYPE_FP32, DTYPE_FP16, DTYPE_Q4 = 0, 1, 2, 3, 4
 # mla_kernel_t
-KERNEL_DEFAULT, KERNEL_TCGEN05, KERNEL_MMA_SYNC, KERNEL_PAIR = 0, 1, 2, 3
+KERNEL_DEFAULT, KERNEL_TCGEN05, KERNEL_MMA_SYNC, KERNEL_PAIR, KERNEL_Q4 = 0, 1, 2, 3, 4
 KERNELS = {"default": KERNEL_DEFAULT, "tcgen05": KERNEL_TCGEN05, "mma_sync": KERNEL_MMA_SYNC,
-           "pair": KERNEL_PAIR}
+           "pair": KERNEL_PAIR, "q4": KERNEL_Q4}
+Q4_ROW_BYTES = 304           # of a token in a 4-bit cache, uint8 [num_pages, page_size, Q4_ROW_BYTES]
 
 EXPORTED = ("mla_plan_create", "mla_decode_plan", "mla_decode_run", "mla_decode_run_host",
             "mla_plan_check_status", "mla_plan_info", "mla_plan_destroy", "mla_status_string",
             "mla_plan_last_error", "mla_plan_partition_host", "mla_plan_set_profile_events",
             "mla_decode_noalloc", "mla_decode_plan_multi", "mla_merge_states",
             "mla_absorb_q", "mla_project_out", "mla_build_tables", "mla_rope_append",
-            "mla_summarize_pages", "mla_page_scores", "mla_select_pages")
+            "mla_summarize_pages", "mla_page_scores", "mla_select_pages", "mla_quantize_append",
+            "mla_read_cache", "mla_decode_run_q4")
 
 
 class MLAError(RuntimeError):
@@ -140,6 +142,13 @@ def bind_library(path: str) -> ctypes.CDLL:
     lib.mla_select_pages.restype = c_int
     lib.mla_select_pages.argtypes = [_VP, c_i64, c_i64, _VP, _VP, c_i64, c_int, c_int, c_int, c_int, _VP, _VP,
                                      c_i64, c_int, _VP]
+    lib.mla_decode_run_q4.restype = c_int
+    lib.mla_decode_run_q4.argtypes = [_VP, _VP, _VP, c_int, _VP, c_int, _VP, c_int, _VP, _VP]
+    lib.mla_quantize_append.restype = c_int
+    lib.mla_quantize_append.argtypes = [_VP, c_i64, _VP, c_i64, c_int, _VP, _VP, c_int, c_int, c_i64, c_int, _VP]
+    lib.mla_read_cache.restype = c_int
+    lib.mla_read_cache.argtypes = [_VP, _VP, c_int, c_float, c_int, c_int, _VP, _VP, c_i64, _VP, _VP, c_int, _VP,
+                                   c_i64, _VP, c_i64, c_int, c_i64, c_int, _VP]
     return lib
 
 
@@ -326,7 +335,7 @@ def _check_layouts(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, page_size=None)
     reads and writes through the raw pointers: the cache [pages, page_size, 512]
     and [pages, page_size, 64] of one dtype, q [..., 512] / [..., 64] of one
     dtype, out [..., 512] and fp32 lse [...] over the same leading dims."""
-    cache, q = ckv_cache.shape, q_nope.shape
+    cache = ckv_cache.shape
     if len(cache) != 3 or cache[2] != 512:
         raise ValueError(f"ckv_cache must be [num_pages, page_size, 512], got {tuple(cache)}")
     if kpe_cache.shape != (cache[0], cache[1], 64):
@@ -336,6 +345,12 @@ def _check_layouts(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, page_size=None)
         raise ValueError("ckv_cache and kpe_cache must have the same dtype")
     if page_size is not None and cache[1] != page_size:
         raise ValueError(f"the cache holds pages of {cache[1]} tokens, the plan {page_size}")
+    _check_queries(q_nope, q_pe, out, lse)
+
+
+def _check_queries(q_nope, q_pe, out, lse) -> None:
+    """The queries and outputs of _check_layouts."""
+    q = q_nope.shape
     lead = tuple(q[:-1])
     if q[-1] != 512 or q_pe.shape != lead + (64,):
         raise ValueError("q_nope must be [..., 512] and q_pe [..., 64] over the same leading dims")
@@ -359,6 +374,26 @@ def mla_decode_run(plan, q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale:
                             lse.data_ptr(), _stream_handle(stream))
     if st != OK:
         _check(st, plan, "mla_decode_run")
+
+
+def mla_decode_run_q4(plan, q_nope, q_pe, cache, out, lse, stream=None, page_size=None) -> None:
+    """Run the planned batch over a 4-bit cache, uint8 [num_pages, page_size,
+    304] (see mla_decode.h); the plan's kernel is "q4"."""
+    import torch
+    lib = load_library()
+    _on_cuda("q_nope q_pe cache out lse", q_nope, q_pe, cache, out, lse)
+    shape, q = cache.shape, q_nope.shape
+    if cache.dtype != torch.uint8 or len(shape) != 3 or shape[2] != Q4_ROW_BYTES:
+        raise ValueError(f"cache must be uint8 [num_pages, page_size, {Q4_ROW_BYTES}], got {cache.dtype} "
+                         f"{tuple(shape)}")
+    if page_size is not None and shape[1] != page_size:
+        raise ValueError(f"the cache holds pages of {shape[1]} tokens, the plan {page_size}")
+    _check_queries(q_nope, q_pe, out, lse)
+    st = lib.mla_decode_run_q4(plan, q_nope.data_ptr(), q_pe.data_ptr(), _dtype_code(q_nope, "q_nope"),
+                               cache.data_ptr(), shape[0], out.data_ptr(), _dtype_code(out, "out"), lse.data_ptr(),
+                               _stream_handle(stream))
+    if st != OK:
+        _check(st, plan, "mla_decode_run_q4")
 
 
 def mla_decode_noalloc(kv_indptr, kv_indices, kv_len, page_size: int, sm_scale: float, q_nope,
@@ -696,6 +731,72 @@ def mla_select_pages(scores, kv_indptr, kv_indices, top_k: int, keep_first: int,
     _check(st, None, "mla_select_pages")
 
 
+def _row_code(name: str, t) -> int:
+    """The dtype code of plain rows given to or taken from a cache."""
+    import torch
+    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _check_q4_cache(device: int, cache) -> None:
+    import torch
+    _on_device(device, torch.uint8, "cache", cache)
+    if cache.dim() != 3 or cache.shape[2] != Q4_ROW_BYTES:
+        raise ValueError(f"cache must be [num_pages, page_size, {Q4_ROW_BYTES}], got {tuple(cache.shape)}")
+
+
+def mla_quantize_append(ckv, kpe, slots, cache, check_status: bool = False, stream=None) -> None:
+    """Rows into a 4-bit cache, uint8 [num_pages, page_size, 304], at ``slots``
+    (see mla_paging.h): ckv [T, 512] and kpe [T, 64] of one type (bf16, fp16 or
+    fp32; rows may be strided), slots int64 [T], negative for padding."""
+    import torch
+    device = torch.cuda.current_device()
+    _check_q4_cache(device, cache)
+    code = _row_code("ckv", ckv)
+    _on_device(device, ckv.dtype, "ckv kpe", ckv, kpe, contiguous=False)
+    _on_device(device, torch.int64, "slots", slots)
+    T = slots.numel()
+    ckv_stride, kpe_stride = _row_stride("ckv", ckv, T, 512), _row_stride("kpe", kpe, T, 64)
+    st = load_library().mla_quantize_append(ckv.data_ptr(), ckv_stride, kpe.data_ptr(), kpe_stride, code,
+                                            slots.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1], T,
+                                            int(bool(check_status)), _stream_handle(stream, device))
+    _check(st, None, "mla_quantize_append")
+
+
+def mla_read_cache(cache, kpe_cache, kv_indptr, kv_indices, starts, row_indptr, ckv_out, kpe_out,
+                   kv_scale: float = 1.0, check_status: bool = False, stream=None) -> None:
+    """Tokens starts[b], starts[b] + 1, .. of each request out of a paged cache
+    into the rows row_indptr[b] .. row_indptr[b + 1] - 1 of ckv_out [N, 512]
+    and kpe_out [N, 64] (bf16, fp16 or fp32; rows may be strided; see
+    mla_paging.h).  ``cache``: a 4-bit cache, with kpe_cache None, or the ckv
+    part of a bf16 or e4m3 one.  kv_indptr, row_indptr int32 [B + 1], starts
+    int32 [B] and kv_indices int32 on the device."""
+    import torch
+    device = torch.cuda.current_device()
+    if kpe_cache is None:
+        _check_q4_cache(device, cache)
+        kind, kpe_ptr = DTYPE_Q4, None
+    else:
+        kind, kpe_ptr = _check_cache(device, cache, kpe_cache), kpe_cache.data_ptr()
+    _on_device(device, torch.int32, "kv_indptr kv_indices starts row_indptr", kv_indptr, kv_indices, starts,
+               row_indptr)
+    batch = starts.numel()
+    if kv_indptr.numel() != batch + 1 or row_indptr.numel() != batch + 1:
+        raise ValueError("kv_indptr and row_indptr must have one entry more than starts")
+    code = _row_code("ckv_out", ckv_out)
+    _on_device(device, ckv_out.dtype, "ckv_out kpe_out", ckv_out, kpe_out, contiguous=False)
+    N = ckv_out.shape[0]
+    ckv_stride, kpe_stride = _row_stride("ckv_out", ckv_out, N, 512), _row_stride("kpe_out", kpe_out, N, 64)
+    st = load_library().mla_read_cache(cache.data_ptr(), kpe_ptr, kind, kv_scale, cache.shape[0], cache.shape[1],
+                                       kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(),
+                                       starts.data_ptr(), row_indptr.data_ptr(), batch, ckv_out.data_ptr(),
+                                       ckv_stride, kpe_out.data_ptr(), kpe_stride, code, N, int(bool(check_status)),
+                                       _stream_handle(stream, device))
+    _check(st, None, "mla_read_cache")
+
+
 # ---------------------------------------------------------------------------
 # Convenience wrappers
 # ---------------------------------------------------------------------------
@@ -734,6 +835,17 @@ class MLADecoder:
             lse = torch.empty(lead, dtype=torch.float32, device=q_nope.device)
         mla_decode_run(self.handle, q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale, stream,
                        page_size=self.page_size)
+        return out, lse
+
+    def run_q4(self, q_nope, q_pe, cache, out=None, lse=None, out_dtype=None, stream=None):
+        """run() over a 4-bit cache, for a decoder made with kernel="q4"."""
+        import torch
+        lead = tuple(q_nope.shape[:-1])
+        if out is None:
+            out = _empty(lead + (512,), out_dtype or torch.bfloat16, q_nope.device, stream)
+        if lse is None:
+            lse = _empty(lead, torch.float32, q_nope.device, stream)
+        mla_decode_run_q4(self.handle, q_nope, q_pe, cache, out, lse, stream, page_size=self.page_size)
         return out, lse
 
     def info(self) -> dict:
