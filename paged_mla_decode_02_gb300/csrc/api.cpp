@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -331,10 +332,12 @@ mla_status_t plan_requests(mla_plan_t plan, const int32_t* page_base, const int3
                            const int32_t* kv_indices_dev, int num_heads, int page_size,
                            float sm_scale, void* stream, int q_len = 1, int heads_per_token = 0) {
   Partition part;
+  int n_workers = plan->n_workers;
+  if (plan->kernel == MLA_KERNEL_Q4) n_workers = std::max(1, n_workers / decode_q4_groups(num_heads));
   if (plan->kernel == MLA_KERNEL_PAIR)
-    partition_batch_pair(page_base, len, n_req, plan->n_workers, num_heads, &part);
+    partition_batch_pair(page_base, len, n_req, n_workers, num_heads, &part);
   else
-    partition_batch(page_base, len, n_req, plan->n_workers, plan->tile_tokens, &part);
+    partition_batch(page_base, len, n_req, n_workers, plan->tile_tokens, &part);
   if (static_cast<int>(part.units.size()) > plan->units_cap || part.n_slots > plan->slots_cap ||
       static_cast<size_t>(part.n_slots) * num_heads > plan->part_rows_cap ||
       static_cast<int>(part.merge.size()) > plan->merge_cap)
@@ -348,7 +351,7 @@ mla_status_t plan_requests(mla_plan_t plan, const int32_t* page_base, const int3
   PlanDev prm{};
   prm.n_units = static_cast<int32_t>(part.units.size());
   prm.n_merge = static_cast<int32_t>(part.merge.size());
-  prm.n_workers = plan->n_workers;
+  prm.n_workers = n_workers;
   prm.batch = n_req;
   prm.num_heads = num_heads;
   prm.page_size = page_size;

@@ -1,16 +1,53 @@
 // Paged MLA decode over a 4-bit cache.
 //
-// For request b, head h, over the rows k_t of the request's tokens:
+// For request b, query row h, over the rows k_t of the request's tokens:
 //   S = sm_scale * (q_nope . k_t[0:512] + q_pe . k_t[512:576]),
 //   out = softmax(S) . k[0:512],  lse = ln sum exp(S).
 //
-// Simple form: a CTA takes eight query rows of a work unit, a warp each, and
-// walks the unit's tokens 32 at a time.  The rows are expanded to fp32 in shared
-// memory; lane t makes the score of token t, then holds 16 of the output dims.
+// A row's values are e2m1 numbers times 2^(E - k), k <= 14 the shift of a group
+// of 32 dims.  Over 2^(E - 6) each is an e4m3 number exactly (6 * 2^6 = 384 at
+// most, 0.5 * 2^-8 = 2^-9 at least), so a tile of rows becomes a tile of e4m3
+// codes by table lookup, and both products are tcgen05 MMAs of kind::f8f6f4 with
+// the rows as A, read from shared memory in either direction:
+//   S^T [128 tokens x rows]    = K [128 tokens x 576] . Q^T       (K-major)
+//   O^T [512 dims x rows]     += V^T [512 dims x 128 tokens] . P^T (MN-major)
+// One expanded tile serves both, and a CTA needs M = 128 of tokens and of dims
+// only, so N is as small as the number of query rows: 16, 32 or 64 to a CTA (two
+// CTAs share a request of 65 to 128 rows).
+//
+// The other operand of each product is split into terms of 8 bits:
+// - the query row, under a power of two that brings its largest magnitude into
+//   [2^7, 2^8), into hi = e4m3(x) and lo = e4m3(x - hi), which together are the
+//   bf16 query exactly (but for elements below 2^-2 after the scaling, off by
+//   2^-11 at most).  Both are rows of the same B: S^T has a column for each, and
+//   their sum is the score.
+// - P.  With the row's unit 2^(E_t - 6) moved into it, p = 2^(s_t + E_t - ref)
+//   can span many powers of two that add up over a long context, so the terms'
+//   range matters as much as their bits.  Up to 32 query rows, three e5m2 terms
+//   side by side in B (the columns of O^T are added in the epilogue): nine bits,
+//   from 2^15 down to 2^-17.  64 rows (O^T's three terms would not fit into
+//   tensor memory): hi = e5m2(p), lo = e4m3(p - hi), two MMAs into the same
+//   columns: eight bits for the larger p, from 2^12 down to 2^-17.
+//
+// The softmax's state is kept per query row: a reference that moves (and O with
+// it) when a score passes it by more than kSlack, and two sums in fp32 per
+// thread: of the exact p for the lse, and for the output of the p that its terms
+// stand for.  A weight is p / 2^E_t, one more factor a token.  A p too small for
+// all its bits enters both sums as it is: the row of a small E_t may weigh much
+// and hold little, so that its p is rounded coarsely, or away.
+//
+// 16 worker warps expand tile g + 1 and make P of tile g; a further warp issues
+// the MMAs: scores of g + 1, then P . V of g.  The raw rows of g + 2 are on their
+// way into registers meanwhile.  Waits are bounded (2 s): a warp that gives up
+// says so, and goes on without waiting, so that the named barriers and commits
+// of the others still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is
+// recorded.
 #include <cuda_bf16.h>
-#include <cuda_runtime.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "device_utils.cuh"
+#include "issue.cuh"
 #include "kernels.h"
 #include "launch.h"
 #include "q4.cuh"
@@ -18,109 +55,670 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = kThreads / 32;     // query rows of a CTA
-constexpr int kTok = 32;                 // tokens at a time
-constexpr int kPitch = kD + 1;           // words between rows: lanes of a column in different banks
+using namespace tc;
+
+#ifdef MLA_STALL_TEST
+// Test build only: when nonzero, CTA 0's first worker warp leaves out its
+// g_q4_stall-th signal of an expanded tile (1-based).
+__device__ int g_q4_stall;
+#endif
+
+constexpr int kT = kTileTc;                   // 128 tokens to a tile
+constexpr int kWorkerWarps = 16;
+constexpr int kWorkers = 32 * kWorkerWarps;
+constexpr int kThreads = kWorkers + 32;
+constexpr int kTokWarp = kT / kWorkerWarps;   // rows that a warp expands
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr size_t kSmem = (kTok * kPitch + kRows * kD) * sizeof(float);
+static_assert(kTokWarp == 8, "rows of a warp lie in one page of 16 or more");
 
-template <bool kOutF32>
-__global__ void __launch_bounds__(kThreads) decode_q4_kernel(const DecodeArgs a) {
+template <int kRows>
+struct Shape {
+  static constexpr int kNS = 2 * kRows;                    // columns of S^T
+  static constexpr bool kSide = kRows < 64;                // P's terms side by side
+  static constexpr int kPN = kSide ? 3 * kRows : kRows;    // N of P . V
+  static constexpr int kPRow = kRows == 32 ? 128 : 64;     // bytes of a token's row of P
+  static constexpr int kPPanel = kT * kPRow;
+  static constexpr SmemSwizzle kPSwizzle = kRows == 32 ? kSw128 : kSw64;
+  static constexpr int kWarpRows = kRows / 4;              // query rows of a warp's softmax
+  // p reaches 2^kTop: the reference is set to leave kSlack of that, and moves when it is used up
+  static constexpr float kTop = kSide ? 15.f : 12.f, kSlack = 1.5f;
+  // p from here on has all its bits (the last term's least unit is 2^-16, 2^-9)
+  static constexpr float kFull = kSide ? 0x1p-8f : 0x1p-2f;
+  // tensor memory columns
+  static constexpr int kOBlock = kRows == 16 ? 64 : kPN;   // of 128 dims
+  static constexpr int kColS = 4 * kOBlock;
+  static_assert(kColS + 2 * kNS <= 512, "tensor memory");
+  // shared memory
+  static constexpr int kOffQ = 0;
+  static constexpr int kQPanel = kNS * 128;                // 128 dims of every term
+  static constexpr int kOffQPe = 4 * kQPanel;
+  static constexpr int kOffP = kOffQPe + kNS * 64;
+  static constexpr int kOffK = kOffP + (kSide ? 1 : 2) * kPPanel;
+  static constexpr int kPanel = kT * 128;                  // 128 tokens x 128 dims
+  static constexpr int kOffKPe = kOffK + 2 * 4 * kPanel;
+  static constexpr int kOffExp = kOffKPe + kT * 64;        // [2][128] exponent bytes
+  static constexpr int kOffScale = kOffExp + 2 * kT;       // [64] 1 / query scale
+  static constexpr int kOffRef = kOffScale + 64 * 4;       // [64] reference, less kTop - kSlack
+  static constexpr int kOffTable = kOffRef + 64 * 4;       // [16] e4m3 codes of the magnitudes, by shift
+  static constexpr int kOffRed = kOffTable + 16 * 8;       // [16 warps][16] floats
+  static constexpr int kOffBar = kOffRed + kWorkerWarps * 16 * 4;
+  static_assert(kOffP % 1024 == 0 && kOffK % 1024 == 0 && kOffKPe % 1024 == 0, "swizzle atoms");
+};
+
+enum Bar {
+  kKFull0,                   // [2] tile expanded (a signal of every worker warp)
+  kSFull0 = kKFull0 + 2,     // [2] scores made
+  kPReady0 = kSFull0 + 2,    // [4] P of 32 tokens written (4 warps)
+  kPvDone0 = kPReady0 + 4,   // [4] P . V over 32 tokens made: their rows of K and P may be written again
+  kQReady = kPvDone0 + 4,    // the unit's query in place
+  kFinal,
+  kNumBars
+};
+template <int kRows>
+constexpr int smem_bytes() {
+  return Shape<kRows>::kOffBar + 8 * kNumBars + 16 + 1024;   // flags, and slack to align
+}
+static_assert(smem_bytes<64>() <= 232448, "shared memory budget");
+
+// A and B of kind::f8f6f4: format 0 e4m3, 1 e5m2; D f32.
+constexpr uint32_t idesc_f8(int N, int b_format, bool mn) {
+  return (1u << 4) | (static_cast<uint32_t>(b_format) << 10) | (static_cast<uint32_t>(mn) << 15) |
+         (static_cast<uint32_t>(mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p, q;\n"
+      "elect.sync _|q, 0xffffffff;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A warp's 32 lanes x N consecutive columns of tensor memory.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// A barrier of `threads` threads that also tells whether any of them says so.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool yes) {
+  uint32_t any;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbar.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(yes))
+      : "memory");
+  return any != 0;
+}
+
+// Two numbers in fp16 -> two 8-bit codes (the first in the low byte; nearest
+// even, saturating) and back.
+template <__nv_fp8_interpretation_t kType>
+__device__ __forceinline__ uint32_t to_fp8x2(__half2 x) {
+  return __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, kType);
+}
+template <__nv_fp8_interpretation_t kType>
+__device__ __forceinline__ __half2 from_fp8x2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), kType);
+  return *reinterpret_cast<const __half2*>(&h);
+}
+// Two floats -> hi + lo in e4m3 (x - hi is exact).
+__device__ __forceinline__ void split_query(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+  const float2 h = __half22float2(from_fp8x2<__NV_E4M3>(hi));
+  lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 - h.x, x1 - h.y), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Four codes to four e4m3 numbers: the magnitudes' indices select bytes of the
+// table, the signs (in place already) go on top.
+__device__ __forceinline__ uint32_t expand4(uint2 table, uint32_t select, uint32_t signs) {
+  return __byte_perm(table.x, table.y, select) | (signs & 0x80808080u);
+}
+__device__ __forceinline__ uint4 expand16(uint2 table, uint2 w) {
+  const uint32_t a = w.x & 0x77777777u, b = w.y & 0x77777777u;
+  return make_uint4(expand4(table, a, w.x), expand4(table, a >> 16, w.x << 4), expand4(table, b, w.y),
+                    expand4(table, b >> 16, w.y << 4));
+}
+
+// Where the walk over a worker's tiles stands.
+struct Cursor {
+  int ui, tile, tiles;      // unit, tile of the unit
+  int tok_begin, tok_end, page_base;
+  __device__ __forceinline__ void read(const WorkUnit* units) {
+    const WorkUnit u = units[ui];
+    tok_begin = u.tok_begin;
+    tok_end = u.tok_end;
+    page_base = u.page_base;
+    tile = 0;
+    tiles = (tok_end - tok_begin + kT - 1) / kT;
+  }
+  __device__ __forceinline__ int tok0() const { return tok_begin + tile * kT; }
+  // To the next tile; false past the last one.
+  __device__ __forceinline__ bool next(const WorkUnit* units, int end) {
+    if (++tile < tiles) return true;
+    if (++ui >= end) return false;
+    read(units);
+    return true;
+  }
+};
+
+template <int kRows, bool kOutF32>
+__global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ float sm[];
-  float* keys = sm;
-  float* query = sm + kTok * kPitch;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  using S = Shape<kRows>;
+  constexpr int kJ = S::kWarpRows;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t base = smem_u32(sm);
+  auto bar = [&](int i) { return base + S::kOffBar + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kOffBar + 8 * kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const PlanDev prm = *a.params;
-  const int H = a.num_heads, P = prm.page_size;
-  const int groups = (H + kRows - 1) / kRows;
-  const int worker = blockIdx.x / groups, h = (blockIdx.x % groups) * kRows + warp;
+  const int H = a.num_heads;
+  const int groups = (H + 63) / 64;                 // CTAs to a worker (1 below kRows = 64)
+  const int worker = blockIdx.x / groups, row0 = 64 * (blockIdx.x % groups);
   const int u0 = worker < prm.n_workers ? a.worker_ptr[worker] : 0;
   const int u1 = worker < prm.n_workers ? a.worker_ptr[worker + 1] : 0;
-  const int hide = prm.q_len > 1 && h < H ? prm.q_len - 1 - h / prm.heads_per_token : 0;
-  const float c = prm.sm_scale * kLog2e;
-  for (int ui = u0; ui < u1; ++ui) {
-    const WorkUnit u = a.units[ui];
-    __syncthreads();
-    if (h < H) {
-      const size_t row = static_cast<size_t>(u.req) * H + h;
-      for (int d = lane; d < kD; d += 32)
-        query[warp * kD + d] = __bfloat162float(d < kDCkv ? static_cast<const __nv_bfloat16*>(a.q_nope)[row * kDCkv + d]
-                                                          : static_cast<const __nv_bfloat16*>(a.q_pe)[row * kDKpe + d - kDCkv]);
+  const int page_shift = 31 - __clz(prm.page_size);
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(bar(i), i < kSFull0 || i == kQReady ? kWorkerWarps : i >= kPReady0 && i < kPvDone0 ? 4 : 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x < 16) {
+    // e4m3 codes of magnitude * 2^(6 - shift); a shift of 15 (which no row has) as 14
+    uint32_t t[2] = {0, 0};
+    const int shift = min(static_cast<int>(threadIdx.x), kQ4MaxShift);
+    for (int m = 1; m < 8; ++m) {
+      // magnitude m = (2 + m % 2) 2^(m / 2) / 4 from index 2 on, m / 2 below
+      const float v = (m < 2 ? 0.5f * m : (2 + (m & 1)) * pow2((m >> 1) - 2)) * pow2(6 - shift);
+      t[m >> 2] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3)) << (8 * (m & 3));
     }
-    float o[kDCkv / 32] = {};
-    float top = -INFINITY, sum = 0.f;
-    const int end = min(u.tok_end, u.kv_len - hide);
-    for (int t0 = u.tok_begin; t0 < u.tok_end; t0 += kTok) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kTok * kQ4Words; i += kThreads) {
-        const int t = i / kQ4Words, w = i % kQ4Words;
-        float x[8] = {};
-        float unit = 0.f;
-        if (t0 + t < u.tok_end) {
-          const int page = a.kv_indices[u.page_base + (t0 + t) / P];
-          if (page < 0 || page >= a.num_pages) {
-            report_error(a.err, kErrBounds);
+    reinterpret_cast<uint2*>(sm + S::kOffTable)[threadIdx.x] = make_uint2(t[0], t[1]);
+  }
+  if (warp == kWorkerWarps) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  bool ok = true;
+  auto wait = [&](int i, int phase) { ok &= mbar_spin<false>(bar(i), phase & 1, abort_flag); };
+
+  if (warp == kWorkerWarps) {
+    // ================= the issuing warp =================
+    const uint64_t k_desc = smem_desc(base + S::kOffK, 16, 1024, kSw128);
+    const uint64_t kpe_desc = smem_desc(base + S::kOffKPe, 16, 512, kSw64);
+    const uint64_t q_desc = smem_desc(base + S::kOffQ, 16, 1024, kSw128);
+    const uint64_t qpe_desc = smem_desc(base + S::kOffQPe, 16, 512, kSw64);
+    const uint64_t p_desc = smem_desc(base + S::kOffP, 16, 8 * S::kPRow, S::kPSwizzle);
+    constexpr uint32_t id_s = idesc_f8(S::kNS, 0, false), id_hi = idesc_f8(S::kPN, 1, true), id_lo = idesc_f8(S::kPN, 0, true);
+    auto scores = [&](int g) {
+      wait(kKFull0 + (g & 1), g >> 1);
+      tc_fence_after();
+      const uint32_t d = tmem + S::kColS + (g & 1) * S::kNS;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint64_t ka = k_desc + static_cast<uint64_t>((((g & 1) * 4 + p) * S::kPanel) >> 4);
+        const uint64_t qb = q_desc + static_cast<uint64_t>((p * S::kQPanel) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_f8_elect(d, ka + 2 * kk, qb + 2 * kk, id_s, (p | kk) != 0);
+      }
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) mma_f8_elect(d, kpe_desc + 2 * kk, qpe_desc + 2 * kk, id_s, 1);
+      mma_commit_elect(bar(kSFull0 + (g & 1)));
+    };
+    auto values = [&](int g, bool first) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {   // 32 tokens
+        wait(kPReady0 + j, g);
+        tc_fence_after();
+        const uint64_t pb = p_desc + static_cast<uint64_t>((j * 32 * S::kPRow) >> 4);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint64_t va = k_desc + static_cast<uint64_t>((((g & 1) * 4 + p) * S::kPanel + j * 32 * 128) >> 4);
+          mma_f8_elect(tmem + p * S::kOBlock, va, pb, id_hi, !first || j > 0);
+          if (!S::kSide) mma_f8_elect(tmem + p * S::kOBlock, va, pb + static_cast<uint64_t>(S::kPPanel >> 4), id_lo, 1);
+        }
+        mma_commit_elect(bar(kPvDone0 + j));
+      }
+    };
+    // S of tile g + 1 before P . V of tile g, but where g + 1 begins a unit, whose
+    // query is written after g's scores are read
+    int g = 0;
+    for (int ui = u0; ui < u1; ++ui) {
+      const WorkUnit u = a.units[ui];
+      const int n = (u.tok_end - u.tok_begin + kT - 1) / kT;
+      wait(kQReady, ui - u0);
+      scores(g);
+      for (int i = 0; i < n; ++i, ++g) {
+        if (i + 1 < n) scores(g + 1);
+        values(g, i == 0);
+      }
+    }
+    mma_commit_elect(bar(kFinal));
+    if (!ok && lane == 0) report_error(a.err, kErrTimeout);
+    mbar_wait_drain(bar(kFinal), 0);   // every MMA issued is done before tensor memory is freed
+    __syncwarp();
+  } else if (u0 < u1) {
+    // ================= workers =================
+    const int q = warp & 3, cg = warp >> 2;             // tokens 32 q .. of a tile (lane quadrant), query rows kJ cg ..
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const int tok = 32 * q + lane;
+    const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
+    float* scale = reinterpret_cast<float*>(sm + S::kOffScale);
+    float* refs = reinterpret_cast<float*>(sm + S::kOffRef);
+    float* red = reinterpret_cast<float*>(sm + S::kOffRed);
+    const uint2* table = reinterpret_cast<const uint2*>(sm + S::kOffTable);
+
+    // ---- the query of a unit ----
+    auto put_query = [&](int req) {
+#pragma unroll 1
+      for (int k = 0; k < kRows / kWorkerWarps; ++k) {
+        const int r = warp * (kRows / kWorkerWarps) + k;
+        uint32_t w[9] = {};   // dims 16 lane .. + 15 of q_nope, 2 lane and + 1 of q_pe
+        if (row0 + r < H) {
+          const size_t row = static_cast<size_t>(req) * H + row0 + r;
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_nope) + row * kDCkv + 16 * lane);
+          const uint4 v0 = src[0], v1 = src[1];
+          w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w, w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
+          w[8] = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q_pe) + row * kDKpe)[lane];
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 9; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        const uint32_t top = __reduce_max_sync(~0u, max(m >> 16, m & 0xffffu));   // bits of the largest magnitude
+        const int e = top == 0 ? 0 : min(max(7 - (static_cast<int>(top >> 7) - 127), -100), 100);
+        const float up = pow2(e);
+        uint32_t hi[9], lo[9];
+#pragma unroll
+        for (int i = 0; i < 9; ++i)
+          split_query(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up, hi[i], lo[i]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t* c = t ? lo : hi;
+          const int row = t * kRows + r;
+          *reinterpret_cast<uint4*>(sm + S::kOffQ + (lane >> 3) * S::kQPanel + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+              make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+          *reinterpret_cast<uint16_t*>(sm + S::kOffQPe + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7)) =
+              static_cast<uint16_t>(c[8]);
+        }
+        // an infinite or NaN query has NaN scores
+        if (lane == 0) scale[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff) : pow2(-e);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kQReady));
+    };
+
+    // ---- raw rows: a tile's 8 rows of this warp, 16 codes of ckv a lane and row, and
+    // of kpe 16 codes a lane (row lane / 4) ----
+    uint2 raw[kTokWarp], raw_pe;
+    uint32_t shifts, meta_pe;   // of row lane / 4: the shifts of groups 4 (lane % 4) ..; of kpe, and the exponent
+    Cursor ld;
+    ld.ui = u0;
+    ld.read(a.units);
+    bool ld_more = true;
+    int page = 0;
+    auto next_page = [&]() {
+      const int t = ld.tok0() + kTokWarp * warp;
+      page = ld_more && t < ld.tok_end ? a.kv_indices[ld.page_base + (t >> page_shift)] : 0;
+    };
+    next_page();
+    auto load_rows = [&]() {
+      const int t = ld.tok0() + kTokWarp * warp;
+      int n = ld_more ? min(kTokWarp, ld.tok_end - t) : 0;
+      if (n > 0 && (page < 0 || page >= a.num_pages)) {   // its rows count as zeros
+        if (lane == 0) report_error(a.err, kErrBounds);
+        n = 0;
+      }
+      const uint8_t* src = cache + ((static_cast<size_t>(n > 0 ? page : 0) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
+#pragma unroll
+      for (int r = 0; r < kTokWarp; ++r) {
+        raw[r] = make_uint2(0, 0);
+        if (r < n) raw[r] = __ldg(reinterpret_cast<const uint2*>(src + r * kQ4Row) + lane);
+      }
+      raw_pe = make_uint2(0, 0);
+      shifts = 0;
+      meta_pe = 127 << 8;
+      if ((lane >> 2) < n) {
+        const uint8_t* row = src + (lane >> 2) * kQ4Row;
+        raw_pe = __ldg(reinterpret_cast<const uint2*>(row + kDCkv / 2) + (lane & 3));
+        shifts = __ldg(reinterpret_cast<const uint16_t*>(row + kQ4Meta) + (lane & 3));
+        meta_pe = __ldg(reinterpret_cast<const uint16_t*>(row + kQ4Meta + 8));
+      }
+      if (ld_more) ld_more = ld.next(a.units, u1);
+      next_page();
+    };
+    auto expand = [&](int g) {
+      unsigned char* dst = sm + S::kOffK + (g & 1) * 4 * S::kPanel + (lane >> 3) * S::kPanel + kTokWarp * warp * 128;
+#pragma unroll
+      for (int r = 0; r < kTokWarp; ++r) {
+        const uint32_t mine = __shfl_sync(~0u, shifts, 4 * r + (lane >> 3));   // groups lane / 8 * 4 ..
+        const uint2 t = table[(mine >> (4 * ((lane >> 1) & 3))) & 15];
+        *reinterpret_cast<uint4*>(dst + r * 128 + (((lane & 7) ^ r) << 4)) = expand16(t, raw[r]);
+      }
+      const int row = kTokWarp * warp + (lane >> 2);
+      const uint2 t = table[(meta_pe >> (2 * (lane & 2))) & 15];
+      *reinterpret_cast<uint4*>(sm + S::kOffKPe + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) = expand16(t, raw_pe);
+      if ((lane & 3) == 0) sm[S::kOffExp + (g & 1) * kT + row] = static_cast<unsigned char>(meta_pe >> 8);
+      fence_proxy_async_smem();
+      __syncwarp();
+#ifdef MLA_STALL_TEST
+      if (blockIdx.x == 0 && warp == 0 && g + 1 == g_q4_stall) return;
+#endif
+      if (lane == 0) mbar_arrive(bar(kKFull0 + (g & 1)));
+    };
+
+    load_rows();
+    put_query(a.units[u0].req);
+    expand(0);
+    load_rows();
+    Cursor at;
+    at.ui = u0;
+    at.read(a.units);
+    float lx[kJ], lr[kJ];
+    for (int g = 0;; ++g) {
+      const bool first = at.tile == 0, last = at.tile + 1 == at.tiles, end = last && at.ui + 1 == u1;
+      // ---- tile g + 1: its buffer was read by P . V of g - 1, the rope part by the scores of g ----
+      if (!end) {
+        if (g > 0) wait(kPvDone0 + (warp >> 2), g - 1);
+        wait(kSFull0 + (g & 1), g >> 1);
+        expand(g + 1);
+        load_rows();
+      }
+      // ---- scores of this thread's token and query rows, less the reference, in log2 ----
+      wait(kSFull0 + (g & 1), g >> 1);
+      tc_fence_after();
+      float z[kJ];
+      const int exponent = sm[S::kOffExp + (g & 1) * kT + tok];
+      const int e = exponent == kQ4NanExp ? 0 : exponent - 127;
+      {
+        uint32_t hi[kJ], lo[kJ];
+        const uint32_t col = S::kColS + (g & 1) * S::kNS + kJ * cg;
+        tmem_ld(lane_addr + col, hi);
+        tmem_ld(lane_addr + col + kRows, lo);
+        const float unit = exponent == kQ4NanExp ? __int_as_float(0x7fffffff) : pow2(e - 6) * (prm.sm_scale * kLog2e);
+        tmem_ld_wait();
+        const float fe = static_cast<float>(e);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const float ref = first ? 0.f : refs[kJ * cg + j];
+          z[j] = fmaf((__uint_as_float(hi[j]) + __uint_as_float(lo[j])) * unit, scale[kJ * cg + j], fe - ref);
+        }
+      }
+      const int t = at.tok0() + tok;
+      if (at.tok0() + kT > at.tok_end - (prm.q_len > 1 ? prm.q_len - 1 : 0)) {
+        // the query rows that see token t: of query tokens packed into rows, row h sees
+        // the tokens before kv_len - (q_len - 1 - h / heads)
+        int from = t < at.tok_end ? 0 : 128;
+        if (prm.q_len > 1 && t < at.tok_end) from = min(128, prm.heads_per_token * max(0, prm.q_len - a.units[at.ui].kv_len + t));
+        from -= row0 + kJ * cg;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) z[j] = j >= from ? z[j] : -INFINITY;
+      }
+      float top = z[0];
+#pragma unroll
+      for (int j = 1; j < kJ; ++j) top = fmaxf(top, z[j]);
+      if (first) {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) lx[j] = lr[j] = 0.f;
+      }
+      // ---- the reference moves: the four warps of these query rows together ----
+      if (bar_any(1 + cg, 128, first || top > S::kTop)) {
+        float* mine = red + warp * 16;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          float m = z[j];
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+          if (lane == j) mine[j] = m;
+        }
+        named_bar_sync(1 + cg, 128);
+        float alpha[kJ];
+        bool moved = false;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const float* other = red + 4 * cg * 16 + j;
+          const float m = fmaxf(fmaxf(other[0], other[16]), fmaxf(other[32], other[48]));
+          // the largest p becomes 2^(kTop - kSlack); a row that sees no token in its unit's
+          // first tile sees none later, and keeps the reference 0 with p = 0
+          const float up = m > (first ? -INFINITY : S::kTop) ? m - (S::kTop - S::kSlack) : 0.f;
+          alpha[j] = first ? 1.f : fast_exp2(-up);
+          moved |= up != 0.f;
+          z[j] -= up;
+          lx[j] *= alpha[j];
+          lr[j] *= alpha[j];
+          if (q == 0 && lane == j) refs[kJ * cg + j] = (first ? 0.f : refs[kJ * cg + j]) + up;
+        }
+        if (!first && moved) {
+          wait(kPvDone0 + 3, g - 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int p = 0; p < 4; ++p) {
+#pragma unroll 1
+            for (int term = 0; term < (S::kSide ? 3 : 1); ++term) {
+              uint32_t o[kJ];
+              const uint32_t col = p * S::kOBlock + term * kRows + kJ * cg;
+              tmem_ld(lane_addr + col, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < kJ; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
+              tmem_st(lane_addr + col, o);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        named_bar_sync(1 + cg, 128);
+      }
+      // ---- p and its terms ----
+      constexpr int kTerms = S::kSide ? 3 : 2;
+      uint32_t c[kTerms][kJ / 4];
+      const float weight = pow2(-e);
+#pragma unroll
+      for (int j = 0; j < kJ; j += 2) {
+        const float p0 = fast_exp2(z[j]), p1 = fast_exp2(z[j + 1]);
+        lx[j] = fmaf(p0, weight, lx[j]);
+        lx[j + 1] = fmaf(p1, weight, lx[j + 1]);
+        const __half2 p = __floats2half2_rn(p0, p1);
+        uint32_t code[kTerms];
+        code[0] = to_fp8x2<__NV_E5M2>(p);
+        __half2 sum = from_fp8x2<__NV_E5M2>(code[0]);
+        if constexpr (S::kSide) {
+          code[1] = to_fp8x2<__NV_E5M2>(__hsub2(p, sum));
+          sum = __hadd2(sum, from_fp8x2<__NV_E5M2>(code[1]));
+          code[2] = to_fp8x2<__NV_E5M2>(__hsub2(p, sum));
+          sum = __hadd2(sum, from_fp8x2<__NV_E5M2>(code[2]));
+        } else {
+          code[1] = to_fp8x2<__NV_E4M3>(__hsub2(p, sum));
+          sum = __hadd2(sum, from_fp8x2<__NV_E4M3>(code[1]));
+        }
+        const float2 s = __half22float2(sum);
+        lr[j] = fmaf(p0 < S::kFull ? p0 : s.x, weight, lr[j]);
+        lr[j + 1] = fmaf(p1 < S::kFull ? p1 : s.y, weight, lr[j + 1]);
+#pragma unroll
+        for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
+      }
+      if (g > 0) wait(kPvDone0 + q, g - 1);   // P . V of the tile before has read these rows of P
+      unsigned char* prow = sm + S::kOffP + tok * S::kPRow;
+#pragma unroll
+      for (int i = 0; i < kTerms; ++i) {
+        if constexpr (kRows == 64)
+          *reinterpret_cast<uint4*>(prow + i * S::kPPanel + ((cg ^ ((tok >> 1) & 3)) << 4)) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+        else if constexpr (kRows == 32)
+          *reinterpret_cast<uint2*>(prow + (((2 * i + (cg >> 1)) ^ (tok & 7)) << 4) + 8 * (cg & 1)) = make_uint2(c[i][0], c[i][1]);
+        else
+          *reinterpret_cast<uint32_t*>(prow + ((i ^ ((tok >> 1) & 3)) << 4) + 4 * cg) = c[i][0];
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kPReady0 + q));
+      if (last) {
+        // ---- the next unit's query, once every warp has done with this one's ----
+        if (!end) {
+          named_bar_sync(5, kWorkers);
+          put_query(a.units[at.ui + 1].req);
+        }
+        // ---- epilogue: the sums over this tile's tokens of all lanes and quadrants ----
+        const WorkUnit u = a.units[at.ui];
+        const bool split = u.out_slot >= 0;
+        float* mine = red + warp * 16;
+        const float* all = red + 4 * cg * 16;
+        float inv[kJ];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          float s = lx[j];
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+          if (lane == j) mine[j] = s;
+        }
+        named_bar_sync(1 + cg, 128);
+        if (q == 0 && lane < kJ && row0 + kJ * cg + lane < H) {
+          const int h = row0 + kJ * cg + lane;
+          const float s = (all[lane] + all[16 + lane]) + (all[32 + lane] + all[48 + lane]);
+          const float lse = (refs[kJ * cg + lane] + log2f(s)) * kLn2;
+          if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
+          else a.lse[static_cast<size_t>(u.req) * H + h] = lse;
+        }
+        named_bar_sync(1 + cg, 128);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          float s = lr[j];
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+          if (lane == j) mine[j] = s;
+        }
+        named_bar_sync(1 + cg, 128);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const float s = (all[j] + all[16 + j]) + (all[32 + j] + all[48 + j]);
+          inv[j] = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
+        }
+        wait(kPvDone0 + 3, g);
+        tc_fence_after();
+#pragma unroll 1
+        for (int p = 0; p < 4; ++p) {
+          uint32_t o[kJ];
+          float x[kJ];
+          tmem_ld(lane_addr + p * S::kOBlock + kJ * cg, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) x[j] = __uint_as_float(o[j]);
+          if constexpr (S::kSide) {
+#pragma unroll
+            for (int term = 1; term < 3; ++term) {
+              tmem_ld(lane_addr + p * S::kOBlock + term * kRows + kJ * cg, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < kJ; ++j) x[j] += __uint_as_float(o[j]);
+            }
+          }
+          const int d = 128 * p + tok;
+          const int h0 = row0 + kJ * cg;
+          const size_t row = static_cast<size_t>(u.req) * H + h0;
+          if (split) {
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+              if (h0 + j < H) a.o_part[part_offset(u.out_slot, h0 + j, d, H)] = x[j] * inv[j];
+          } else if (kOutF32) {
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+              if (h0 + j < H) static_cast<float*>(a.out)[(row + j) * kDCkv + d] = x[j] * inv[j];
           } else {
-            const uint8_t* row = static_cast<const uint8_t*>(a.ckv) + (static_cast<size_t>(page) * P + (t0 + t) % P) * kQ4Row;
-            q4_expand(reinterpret_cast<const uint32_t*>(row)[w], x);
-            unit = q4_unit(Q4Meta{*reinterpret_cast<const uint4*>(row + kQ4Meta)}, w / 4);
+            // two lanes trade halves of two query rows: each stores two dims of one
+#pragma unroll
+            for (int j = 0; j < kJ; j += 2) {
+              const float x0 = x[j] * inv[j], x1 = x[j + 1] * inv[j + 1];
+              const bool odd = lane & 1;
+              const float got = __shfl_xor_sync(~0u, odd ? x0 : x1, 1);
+              const uint32_t w = odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got);
+              const int h = j + (odd ? 1 : 0);
+              if (h0 + h < H)
+                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row + h) * kDCkv + (d & ~1)) = w;
+            }
           }
         }
-#pragma unroll
-        for (int d = 0; d < 8; ++d) keys[t * kPitch + 8 * w + d] = x[d] * unit;
+        tc_fence_before();   // O is read: the next unit's first P . V waits for P of all warps
+        named_bar_sync(1 + cg, 128);   // red and the references may be written again
       }
-      __syncthreads();
-      float s = 0.f;
-      for (int d = 0; d < kD; ++d) s = fmaf(query[warp * kD + d], keys[lane * kPitch + d], s);
-      s = t0 + lane < end ? s * c : -INFINITY;
-      float m = s;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-      m = fmaxf(m, top);
-      const float base = m == -INFINITY ? 0.f : m, alpha = exp2f(top - base);
-      const float p = exp2f(s - base);
-      sum = sum * alpha + p;
-      top = m;
-#pragma unroll
-      for (int i = 0; i < kDCkv / 32; ++i) o[i] *= alpha;
-      for (int t = 0; t < kTok; ++t) {
-        const float w = __shfl_sync(~0u, p, t);
-#pragma unroll
-        for (int i = 0; i < kDCkv / 32; ++i) o[i] = fmaf(w, keys[t * kPitch + 32 * i + lane], o[i]);
-      }
+      if (end) break;
+      at.next(a.units, u1);
     }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
-    if (h >= H) continue;
-    const bool split = u.out_slot >= 0;
-    const size_t row = static_cast<size_t>(u.req) * H + h;
-    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-    if (lane == 0) {
-      const float lse = (top + log2f(sum)) * kLn2;
-      if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
-      else a.lse[row] = lse;
-    }
-#pragma unroll
-    for (int i = 0; i < kDCkv / 32; ++i) {
-      const int d = 32 * i + lane;
-      if (split) a.o_part[part_offset(u.out_slot, h, d, H)] = o[i] * inv;
-      else if (kOutF32) static_cast<float*>(a.out)[row * kDCkv + d] = o[i] * inv;
-      else static_cast<__nv_bfloat16*>(a.out)[row * kDCkv + d] = __float2bfloat16(o[i] * inv);
-    }
+    if (!ok && lane == 0) report_error(a.err, kErrTimeout);
   }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWorkerWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kRows, bool kOutF32>
+cudaError_t launch(const DecodeArgs& a, int groups, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<kRows, kOutF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<kRows>());
+  if (e != cudaSuccess) return e;
+  return launch_dependent(decode_q4_kernel<kRows, kOutF32>, a.n_workers / groups * groups, kThreads, smem_bytes<kRows>(), 1, s, a);
 }
 
 }  // namespace
 
+#ifdef MLA_STALL_TEST
+// Test build only: the signal CTA 0 leaves out (0: none).
+extern "C" int mla_test_set_q4_stall(int signal) {
+  return static_cast<int>(cudaMemcpyToSymbol(g_q4_stall, &signal, sizeof(signal)));
+}
+#endif
+
+int decode_q4_groups(int rows) { return (rows + 63) / 64; }
+
 cudaError_t launch_decode_q4(const DecodeArgs& a, bool out_f32, cudaStream_t s) {
-  auto kernel = out_f32 ? decode_q4_kernel<true> : decode_q4_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, a.n_workers * ((a.num_heads + kRows - 1) / kRows), kThreads, kSmem, 1, s, a);
+  // as few columns as hold the query rows: N is what both products cost beyond A
+  const int H = a.num_heads, groups = decode_q4_groups(H);
+  if (H <= 16) return out_f32 ? launch<16, true>(a, groups, s) : launch<16, false>(a, groups, s);
+  if (H <= 32) return out_f32 ? launch<32, true>(a, groups, s) : launch<32, false>(a, groups, s);
+  return out_f32 ? launch<64, true>(a, groups, s) : launch<64, false>(a, groups, s);
 }
 
 }  // namespace mla

@@ -106,7 +106,9 @@ bool encode_pair_maps(PairMaps* maps, const void* q_nope, const void* q_pe, cons
 cudaError_t decode_pair_max_workers(int* workers);
 
 // Decode over a 4-bit cache (a.ckv: its rows; kpe and kv_scale unused): units
-// and partials as for the CTA-pair kernel.
+// of 128-token tiles, partials as for the CTA-pair kernel.  decode_q4_groups
+// CTAs share a worker's units, 64 query rows each.
+int decode_q4_groups(int rows);
 cudaError_t launch_decode_q4(const DecodeArgs& a, bool out_f32, cudaStream_t s);
 
 // LSE merge of split partials (and zero-fill of empty requests); the mma.sync

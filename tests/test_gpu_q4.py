@@ -334,24 +334,39 @@ def tolerances(b, values, spread):
     standard deviations of which are 8 sqrt(1152) 2^-24 < 2^-15.8 of A = sm_scale
     * max_t sum |q_i k_ti|; with the exponential's 2^-22 and the sum's as much
     again: 2^-15 (A + 1).
-    Output: p in two or three terms of 8 bits, off by 2^-8 of itself at most, the
-    score's error twice (numerator and normaliser), each relative to the weighted
-    mean of |v|, and once more the first for the normaliser; p below 2^-24 of the
-    largest count as zero."""
+    Output: p is rounded to fp16 (2^-11 of itself at most) and then held in two
+    terms, three and four bits wide: with p in [1, 2) the first leaves a rest of at
+    most 2^-3, whose own four bits leave 2^-8.  So p is off by 2^-8 + 2^-11 of
+    itself; that and the score's error count twice (numerator and normaliser),
+    each relative to the weighted mean of |v|.
+    Small p: what the kernel holds is p_t 2^E_t over its largest, G, which is
+    2^10.5 at least; the last term's least unit is 2^-9, so that each is off by up
+    to 2^-10, 2^-20.5 G, and those below 2^-17 count as nothing.  Times a value of
+    6 at most: roundings like a random walk of n steps, what is lost n times.  Up
+    to 32 query rows: from 2^13.5 down to a unit of 2^-16, 2^-30.5 G."""
     B, Q, H, _ = b.q.shape
     q = np.abs(f64(b.q))
-    A = np.zeros((B, Q, H))
-    top = np.zeros((B, 1, 1, 1))
-    for i, n in enumerate(b.lens):
-        slots = [int(b.ids[b.indptr[i] + t // b.P]) * b.P + t % b.P for t in range(int(n))]
+    A, G, n = np.zeros((B, Q, H)), np.zeros((B, Q, H)), np.zeros((B, 1, 1))
+    for i, length in enumerate(b.lens):
+        slots = [int(b.ids[b.indptr[i] + t // b.P]) * b.P + t % b.P for t in range(int(length))]
+        n[i] = length
         if slots:
-            k = np.abs(values[slots])
-            A[i] = (q[i] @ k.T).max(-1) * b.sm_scale
-            top[i] = k[:, :512].max()
+            A[i] = (q[i] @ np.abs(values[slots]).T).max(-1) * b.sm_scale
+            s = f64(b.q)[i] @ values[slots].T * b.sm_scale
+            w = np.exp(s - s.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            G[i] = (w * 2.0 ** (b.bytes[slots, 297].astype(float) - 127)).max(-1)
+            if b.q_len > 1:            # the first query tokens see fewer tokens
+                for j in range(Q):
+                    seen = int(length) - Q + 1 + j
+                    x = np.exp(s[j, :, :seen] - s[j, :, :seen].max(-1, keepdims=True))
+                    G[i, j] = (x / x.sum(-1, keepdims=True) * 2.0 ** (b.bytes[slots[:seen], 297].astype(float) - 127)).max(-1)
     lse = 2.0 ** -15 * (A + 1)
-    n = np.array([float(x) for x in b.lens]).reshape(B, 1, 1, 1)
-    out = (2 * 2.0 ** -8 + 2 * lse[..., None]) * spread + n * 2.0 ** -24 * top + 1e-30
-    return out, lse
+    if b.q_len * H > 32:
+        small = 5 * np.sqrt(n) * 2.0 ** -20.5 + n * 2.0 ** -27.5
+    else:
+        small = (5 * np.sqrt(n) + n) * 2.0 ** -30.5
+    return (2 * (2.0 ** -8 + 2.0 ** -11) + 2 * lse[..., None]) * spread + (6 * small * G)[..., None] + 1e-30, lse
 
 
 def check_decode(b, out, lse, what=""):
