@@ -36,12 +36,12 @@
 // all its bits enters both sums as it is: the row of a small E_t may weigh much
 // and hold little, so that its p is rounded coarsely, or away.
 //
-// 16 worker warps expand tile g + 1 and make P of tile g; a further warp issues
-// the MMAs: scores of g + 1, then P . V of g.  The raw rows of g + 2 are on their
-// way into registers meanwhile.  Waits are bounded (2 s): a warp that gives up
-// says so, and goes on without waiting, so that the named barriers and commits
-// of the others still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is
-// recorded.
+// Roles: eight warps expand tiles, up to a tile ahead of the products, with the
+// raw rows of the next one on their way into registers; 16 warps make P; one
+// issues the MMAs, scores of tile g + 1 before P . V of tile g.  Registers are
+// dealt out by role.  Waits are bounded (2 s): a warp that gives up says so, and
+// goes on without waiting, so that the named barriers and commits of the others
+// still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is recorded.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -64,13 +64,17 @@ __device__ int g_q4_stall;
 #endif
 
 constexpr int kT = kTileTc;                   // 128 tokens to a tile
-constexpr int kWorkerWarps = 16;
-constexpr int kWorkers = 32 * kWorkerWarps;
-constexpr int kThreads = kWorkers + 32;
-constexpr int kTokWarp = kT / kWorkerWarps;   // rows that a warp expands
+constexpr int kSoftmaxWarps = 16;             // warps 0 ..: a lane quadrant and a quarter of the query rows each
+constexpr int kExpandWarps = 8;               // warps 16 ..
+constexpr int kIssueWarp = kSoftmaxWarps + kExpandWarps;
+constexpr int kThreads = 32 * (kIssueWarp + 4);   // whole warpgroups
+constexpr int kTokWarp = kT / kExpandWarps;   // rows that a warp expands
+// Registers a thread: 72 at launch (896 x 72 = 64512 of 65536), then by role.
+constexpr int kRegsSoftmax = 88, kRegsExpand = 64, kRegsIssue = 24;
+static_assert(32 * (kSoftmaxWarps * kRegsSoftmax + kExpandWarps * kRegsExpand + 4 * kRegsIssue) <= kThreads * 72, "registers");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-static_assert(kTokWarp == 8, "rows of a warp lie in one page of 16 or more");
+static_assert(kTokWarp == 16, "rows of a warp lie in one page");
 
 template <int kRows>
 struct Shape {
@@ -82,7 +86,7 @@ struct Shape {
   static constexpr SmemSwizzle kPSwizzle = kRows == 32 ? kSw128 : kSw64;
   static constexpr int kWarpRows = kRows / 4;              // query rows of a warp's softmax
   // p reaches 2^kTop: the reference is set to leave kSlack of that, and moves when it is used up
-  static constexpr float kTop = kSide ? 15.f : 12.f, kSlack = 1.5f;
+  static constexpr float kTop = kSide ? 15.f : 12.f, kSlack = 5.f;
   // p from here on has all its bits (the last term's least unit is 2^-16, 2^-9)
   static constexpr float kFull = kSide ? 0x1p-8f : 0x1p-2f;
   // tensor memory columns
@@ -98,16 +102,16 @@ struct Shape {
   static constexpr int kPanel = kT * 128;                  // 128 tokens x 128 dims
   static constexpr int kOffKPe = kOffK + 2 * 4 * kPanel;
   static constexpr int kOffExp = kOffKPe + kT * 64;        // [2][128] exponent bytes
-  static constexpr int kOffScale = kOffExp + 2 * kT;       // [64] 1 / query scale
-  static constexpr int kOffRef = kOffScale + 64 * 4;       // [64] reference, less kTop - kSlack
-  static constexpr int kOffTable = kOffRef + 64 * 4;       // [16] e4m3 codes of the magnitudes, by shift
-  static constexpr int kOffRed = kOffTable + 16 * 8;       // [16 warps][16] floats
-  static constexpr int kOffBar = kOffRed + kWorkerWarps * 16 * 4;
+  static constexpr int kOffScale = kOffExp + 2 * kT;       // [2][rows] 1 / query scale, by unit parity
+  static constexpr int kOffRef = kOffScale + 2 * kRows * 4;   // [rows] reference, less kTop - kSlack
+  static constexpr int kOffTable = kOffRef + kRows * 4;    // [4] e4m3 codes of the magnitudes, for shifts 12 ..
+  static constexpr int kOffRed = kOffTable + 4 * 8;        // [16 warps][kWarpRows] floats
+  static constexpr int kOffBar = kOffRed + kSoftmaxWarps * kWarpRows * 4;
   static_assert(kOffP % 1024 == 0 && kOffK % 1024 == 0 && kOffKPe % 1024 == 0, "swizzle atoms");
 };
 
 enum Bar {
-  kKFull0,                   // [2] tile expanded (a signal of every worker warp)
+  kKFull0,                   // [2] tile expanded (a signal of every expanding warp)
   kSFull0 = kKFull0 + 2,     // [2] scores made
   kPReady0 = kSFull0 + 2,    // [4] P of 32 tokens written (4 warps)
   kPvDone0 = kPReady0 + 4,   // [4] P . V over 32 tokens made: their rows of K and P may be written again
@@ -117,7 +121,7 @@ enum Bar {
 };
 template <int kRows>
 constexpr int smem_bytes() {
-  return Shape<kRows>::kOffBar + 8 * kNumBars + 16 + 1024;   // flags, and slack to align
+  return Shape<kRows>::kOffBar + 8 * kNumBars + 16;   // tensor memory's address, abort flag
 }
 static_assert(smem_bytes<64>() <= 232448, "shared memory budget");
 
@@ -126,7 +130,34 @@ constexpr uint32_t idesc_f8(int N, int b_format, bool mn) {
   return (1u << 4) | (static_cast<uint32_t>(b_format) << 10) | (static_cast<uint32_t>(mn) << 15) |
          (static_cast<uint32_t>(mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
+// The second MMA of two with the same A takes it from where the first left it.
+enum class KeepA { kNo, kFill, kLast };
+template <KeepA kKeep = KeepA::kNo>
 __device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kKeep == KeepA::kFill) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "elect.sync _|q, 0xffffffff;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+    return;
+  }
+  if constexpr (kKeep == KeepA::kLast) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "elect.sync _|q, 0xffffffff;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+    return;
+  }
   asm volatile(
       "{\n"
       ".reg .pred p, q;\n"
@@ -213,6 +244,61 @@ __device__ __forceinline__ uint4 expand16(uint2 table, uint2 w) {
   return make_uint4(expand4(table, a, w.x), expand4(table, a >> 16, w.x << 4), expand4(table, b, w.y),
                     expand4(table, b >> 16, w.y << 4));
 }
+// e4m3 codes of magnitude * 2^(6 - shift): up to a shift of 11 all are normal
+// numbers, whose exponent field starts at bit 3.
+__device__ __forceinline__ uint2 normal_table(uint32_t shift) {
+  return make_uint2(0x6c686000u - shift * 0x08080800u, 0x7c787470u - shift * 0x08080808u);
+}
+
+// max or sum over a warp's lanes of each of N values, each step handing half of
+// them on: lane l ends with value l >> (5 - log2 N).
+template <bool kMax, int N>
+__device__ __forceinline__ float warp_reduce(const float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  float x[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) x[j] = v[j];
+  int d = 16;
+#pragma unroll
+  for (int half = N / 2; half > 0; half >>= 1, d >>= 1) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int j = 0; j < half; ++j) {
+      const float keep = upper ? x[half + j] : x[j], got = __shfl_xor_sync(~0u, upper ? x[j] : x[half + j], d);
+      x[j] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+#pragma unroll
+  for (; d > 0; d >>= 1) {
+    const float got = __shfl_xor_sync(~0u, x[0], d);
+    x[0] = kMax ? fmaxf(x[0], got) : x[0] + got;
+  }
+  return x[0];
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 d, a, b;\nmov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 d, a, b;\nmov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\nfma.rn.f32x2 d, a, b, c;\n"
+      "mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
 
 // Where the walk over a worker's tiles stands.
 struct Cursor {
@@ -242,8 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using S = Shape<kRows>;
   constexpr int kJ = S::kWarpRows;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) unsigned char sm[];
   const uint32_t base = smem_u32(sm);
   auto bar = [&](int i) { return base + S::kOffBar + 8 * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kOffBar + 8 * kNumBars);
@@ -261,13 +346,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i < kSFull0 || i == kQReady ? kWorkerWarps : i >= kPReady0 && i < kPvDone0 ? 4 : 1);
+      mbar_init(bar(i), i < kSFull0 || i == kQReady ? kExpandWarps : i >= kPReady0 && i < kPvDone0 ? 4 : 1);
     fence_barrier_init();
   }
-  if (threadIdx.x < 16) {
-    // e4m3 codes of magnitude * 2^(6 - shift); a shift of 15 (which no row has) as 14
+  if (threadIdx.x < 4) {
+    // e4m3 codes of magnitude * 2^(6 - shift), subnormal numbers among them (a shift
+    // of 15, which no row has, as 14)
     uint32_t t[2] = {0, 0};
-    const int shift = min(static_cast<int>(threadIdx.x), kQ4MaxShift);
+    const int shift = min(12 + static_cast<int>(threadIdx.x), kQ4MaxShift);
     for (int m = 1; m < 8; ++m) {
       // magnitude m = (2 + m % 2) 2^(m / 2) / 4 from index 2 on, m / 2 below
       const float v = (m < 2 ? 0.5f * m : (2 + (m & 1)) * pow2((m >> 1) - 2)) * pow2(6 - shift);
@@ -275,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
     }
     reinterpret_cast<uint2*>(sm + S::kOffTable)[threadIdx.x] = make_uint2(t[0], t[1]);
   }
-  if (warp == kWorkerWarps) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == kIssueWarp) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -283,413 +369,419 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
   bool ok = true;
   auto wait = [&](int i, int phase) { ok &= mbar_spin<false>(bar(i), phase & 1, abort_flag); };
 
-  if (warp == kWorkerWarps) {
-    // ================= the issuing warp =================
-    const uint64_t k_desc = smem_desc(base + S::kOffK, 16, 1024, kSw128);
-    const uint64_t kpe_desc = smem_desc(base + S::kOffKPe, 16, 512, kSw64);
-    const uint64_t q_desc = smem_desc(base + S::kOffQ, 16, 1024, kSw128);
-    const uint64_t qpe_desc = smem_desc(base + S::kOffQPe, 16, 512, kSw64);
-    const uint64_t p_desc = smem_desc(base + S::kOffP, 16, 8 * S::kPRow, S::kPSwizzle);
-    constexpr uint32_t id_s = idesc_f8(S::kNS, 0, false), id_hi = idesc_f8(S::kPN, 1, true), id_lo = idesc_f8(S::kPN, 0, true);
-    auto scores = [&](int g) {
-      wait(kKFull0 + (g & 1), g >> 1);
-      tc_fence_after();
-      const uint32_t d = tmem + S::kColS + (g & 1) * S::kNS;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint64_t ka = k_desc + static_cast<uint64_t>((((g & 1) * 4 + p) * S::kPanel) >> 4);
-        const uint64_t qb = q_desc + static_cast<uint64_t>((p * S::kQPanel) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_f8_elect(d, ka + 2 * kk, qb + 2 * kk, id_s, (p | kk) != 0);
-      }
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) mma_f8_elect(d, kpe_desc + 2 * kk, qpe_desc + 2 * kk, id_s, 1);
-      mma_commit_elect(bar(kSFull0 + (g & 1)));
-    };
-    auto values = [&](int g, bool first) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {   // 32 tokens
-        wait(kPReady0 + j, g);
+  if (warp >= kIssueWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == kIssueWarp) {
+      // ================= the issuing warp =================
+      const uint64_t k_desc = smem_desc(base + S::kOffK, 16, 1024, kSw128);
+      const uint64_t kpe_desc = smem_desc(base + S::kOffKPe, 16, 512, kSw64);
+      const uint64_t q_desc = smem_desc(base + S::kOffQ, 16, 1024, kSw128);
+      const uint64_t qpe_desc = smem_desc(base + S::kOffQPe, 16, 512, kSw64);
+      const uint64_t p_desc = smem_desc(base + S::kOffP, 16, 8 * S::kPRow, S::kPSwizzle);
+      constexpr uint32_t id_s = idesc_f8(S::kNS, 0, false), id_hi = idesc_f8(S::kPN, 1, true), id_lo = idesc_f8(S::kPN, 0, true);
+      auto scores = [&](int g) {
+        wait(kKFull0 + (g & 1), g >> 1);
         tc_fence_after();
-        const uint64_t pb = p_desc + static_cast<uint64_t>((j * 32 * S::kPRow) >> 4);
+        const uint32_t d = tmem + S::kColS + (g & 1) * S::kNS;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const uint64_t va = k_desc + static_cast<uint64_t>((((g & 1) * 4 + p) * S::kPanel + j * 32 * 128) >> 4);
-          mma_f8_elect(tmem + p * S::kOBlock, va, pb, id_hi, !first || j > 0);
-          if (!S::kSide) mma_f8_elect(tmem + p * S::kOBlock, va, pb + static_cast<uint64_t>(S::kPPanel >> 4), id_lo, 1);
+          const uint64_t ka = k_desc + static_cast<uint64_t>((((g & 1) * 4 + p) * S::kPanel) >> 4);
+          const uint64_t qb = q_desc + static_cast<uint64_t>((p * S::kQPanel) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_f8_elect(d, ka + 2 * kk, qb + 2 * kk, id_s, (p | kk) != 0);
         }
-        mma_commit_elect(bar(kPvDone0 + j));
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) mma_f8_elect(d, kpe_desc + 2 * kk, qpe_desc + 2 * kk, id_s, 1);
+        mma_commit_elect(bar(kSFull0 + (g & 1)));
+      };
+      auto values = [&](int g, bool first) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // 32 tokens
+          wait(kPReady0 + j, g);
+          tc_fence_after();
+          const uint64_t pb = p_desc + static_cast<uint64_t>((j * 32 * S::kPRow) >> 4);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint64_t va = k_desc + static_cast<uint64_t>((((g & 1) * 4 + p) * S::kPanel + j * 32 * 128) >> 4);
+            if constexpr (S::kSide) {
+              mma_f8_elect(tmem + p * S::kOBlock, va, pb, id_hi, !first || j > 0);
+            } else {
+              mma_f8_elect(tmem + p * S::kOBlock, va, pb, id_hi, !first || j > 0);
+              mma_f8_elect(tmem + p * S::kOBlock, va, pb + static_cast<uint64_t>(S::kPPanel >> 4), id_lo, 1);
+            }
+          }
+          mma_commit_elect(bar(kPvDone0 + j));
+        }
+      };
+      // S of tile g + 1 before P . V of tile g, but where g + 1 begins a unit, whose
+      // query comes a while after g's scores
+      int g = 0;
+      for (int ui = u0; ui < u1; ++ui) {
+        const int n = (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
+        wait(kQReady, ui - u0);
+        scores(g);
+        for (int i = 0; i < n; ++i, ++g) {
+          if (i + 1 < n) scores(g + 1);
+          values(g, i == 0);
+        }
       }
-    };
-    // S of tile g + 1 before P . V of tile g, but where g + 1 begins a unit, whose
-    // query is written after g's scores are read
-    int g = 0;
-    for (int ui = u0; ui < u1; ++ui) {
-      const WorkUnit u = a.units[ui];
-      const int n = (u.tok_end - u.tok_begin + kT - 1) / kT;
-      wait(kQReady, ui - u0);
-      scores(g);
-      for (int i = 0; i < n; ++i, ++g) {
-        if (i + 1 < n) scores(g + 1);
-        values(g, i == 0);
-      }
+      mma_commit_elect(bar(kFinal));
+      if (!ok && lane == 0) report_error(a.err, kErrTimeout);
+      mbar_wait_drain(bar(kFinal), 0);   // every MMA issued is done before tensor memory is freed
+      __syncwarp();
     }
-    mma_commit_elect(bar(kFinal));
-    if (!ok && lane == 0) report_error(a.err, kErrTimeout);
-    mbar_wait_drain(bar(kFinal), 0);   // every MMA issued is done before tensor memory is freed
-    __syncwarp();
-  } else if (u0 < u1) {
-    // ================= workers =================
+  } else if (warp >= kSoftmaxWarps) {
+    // ================= expanding warps =================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
+    if (u0 < u1) {
+      const int ew = warp - kSoftmaxWarps;
+      const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
+      const uint2* table = reinterpret_cast<const uint2*>(sm + S::kOffTable);
+      Cursor ld;
+      ld.ui = u0;
+      ld.read(a.units);
+      bool more = true;          // ld stands on a tile
+      int page = 0;              // of this warp's rows of that tile
+      auto next_page = [&]() {
+        const int t = ld.tok0() + kTokWarp * ew;
+        if (more && t < ld.tok_end) page = a.kv_indices[ld.page_base + (t >> page_shift)];
+      };
+      // 16 rows: 16 codes of ckv a lane and row; of kpe and the shifts a quarter of rows
+      // lane / 4 and 8 + lane / 4
+      uint2 raw[kTokWarp], raw_pe[2];
+      uint32_t shifts[2], meta_pe[2];
+      auto load_rows = [&]() {
+        const int t = ld.tok0() + kTokWarp * ew;
+        int n = more ? min(kTokWarp, ld.tok_end - t) : 0;
+        if (n > 0 && (page < 0 || page >= a.num_pages)) {   // its rows count as zeros
+          if (lane == 0) report_error(a.err, kErrBounds);
+          n = 0;
+        }
+        const uint8_t* src = cache + ((static_cast<size_t>(n > 0 ? page : 0) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * i + (lane >> 2);
+          const uint8_t* row = src + r * kQ4Row + kDCkv / 2;
+          raw_pe[i] = make_uint2(0, 0);
+          shifts[i] = 0;
+          meta_pe[i] = 127 << 8;
+          if (r < n) {
+            raw_pe[i] = __ldg(reinterpret_cast<const uint2*>(row) + (lane & 3));
+            shifts[i] = __ldg(reinterpret_cast<const uint16_t*>(row + 32) + (lane & 3));
+            meta_pe[i] = __ldg(reinterpret_cast<const uint16_t*>(row + 40));
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kTokWarp; ++r) {
+          raw[r] = make_uint2(0, 0);
+          if (r < n) raw[r] = __ldg(reinterpret_cast<const uint2*>(src + r * kQ4Row) + lane);
+        }
+        if (more) more = ld.next(a.units, u1);
+        next_page();
+      };
+      auto expand = [&](int g) {
+        unsigned char* dst = sm + S::kOffK + (g & 1) * 4 * S::kPanel + (lane >> 3) * S::kPanel + kTokWarp * ew * 128;
+        // shifts past 11 lead to subnormal numbers, by a table
+        const uint32_t both = shifts[0] | shifts[1] << 16;
+        const bool far = __any_sync(~0u, ((both & (both << 1)) & 0x88888888u) | ((meta_pe[0] & (meta_pe[0] << 1)) & 0x88u) |
+                                             ((meta_pe[1] & (meta_pe[1] << 1)) & 0x88u));
+        auto table_of = [&](uint32_t k) { return far && k >= 12 ? table[k - 12] : normal_table(k); };
+#pragma unroll
+        for (int r = 0; r < kTokWarp; ++r) {
+          const uint32_t mine = __shfl_sync(~0u, shifts[r / 8], 4 * (r % 8) + (lane >> 3));   // groups lane / 8 * 4 ..
+          *reinterpret_cast<uint4*>(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
+              expand16(table_of((mine >> (2 * (lane & 6))) & 15), raw[r]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = kTokWarp * ew + 8 * i + (lane >> 2);
+          *reinterpret_cast<uint4*>(sm + S::kOffKPe + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) =
+              expand16(table_of((meta_pe[i] >> (2 * (lane & 2))) & 15), raw_pe[i]);
+          if ((lane & 3) == 0) sm[S::kOffExp + (g & 1) * kT + row] = static_cast<unsigned char>(meta_pe[i] >> 8);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+#ifdef MLA_STALL_TEST
+        if (blockIdx.x == 0 && ew == 0 && g + 1 == g_q4_stall) return;
+#endif
+        if (lane == 0) mbar_arrive(bar(kKFull0 + (g & 1)));
+      };
+      // ---- the query of a unit, kRows / 8 rows a warp ----
+      auto put_query = [&](int ui) {
+        const size_t first_row = static_cast<size_t>(a.units[ui].req) * H + row0;
+        float* scale = reinterpret_cast<float*>(sm + S::kOffScale) + ((ui - u0) & 1) * kRows;
+#pragma unroll 1
+        for (int k = 0; k < kRows / kExpandWarps; ++k) {
+          const int r = ew * (kRows / kExpandWarps) + k;
+          uint32_t w[9] = {};   // dims 16 lane .. + 15 of q_nope, 2 lane and + 1 of q_pe
+          if (row0 + r < H) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_nope) + (first_row + r) * kDCkv + 16 * lane);
+            const uint4 v0 = src[0], v1 = src[1];
+            w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w, w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
+            w[8] = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q_pe) + (first_row + r) * kDKpe)[lane];
+          }
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 9; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+          const uint32_t top = __reduce_max_sync(~0u, max(m >> 16, m & 0xffffu));   // bits of the largest magnitude
+          const int e = top == 0 ? 0 : min(max(7 - (static_cast<int>(top >> 7) - 127), -100), 100);
+          const float up = pow2(e);
+          uint32_t hi[9], lo[9];
+#pragma unroll
+          for (int i = 0; i < 9; ++i)
+            split_query(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up, hi[i], lo[i]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t* c = t ? lo : hi;
+            const int row = t * kRows + r;
+            *reinterpret_cast<uint4*>(sm + S::kOffQ + (lane >> 3) * S::kQPanel + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+                make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+            *reinterpret_cast<uint16_t*>(sm + S::kOffQPe + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7)) =
+                static_cast<uint16_t>(c[8]);
+          }
+          // an infinite or NaN query has NaN scores
+          if (lane == 0) scale[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff) : pow2(-e);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kQReady));
+      };
+      next_page();
+      load_rows();
+      put_query(u0);
+      int g = 0;
+      for (int ui = u0; ui < u1; ++ui) {
+        const int n = (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
+        for (int i = 0; i < n; ++i, ++g) {
+          // the buffer was read by P . V of g - 2, the rope part and the query by the scores of g - 1
+          if (g > 1) wait(kPvDone0 + (ew >> 1), g - 2);
+          if (g > 0) wait(kSFull0 + ((g - 1) & 1), (g - 1) >> 1);
+          expand(g);
+          load_rows();
+          if (i == 0 && ui > u0) put_query(ui);
+        }
+      }
+      if (!ok && lane == 0) report_error(a.err, kErrTimeout);
+    }
+  } else {
+    // ================= softmax and epilogue =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int q = warp & 3, cg = warp >> 2;             // tokens 32 q .. of a tile (lane quadrant), query rows kJ cg ..
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const int tok = 32 * q + lane;
-    const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
-    float* scale = reinterpret_cast<float*>(sm + S::kOffScale);
-    float* refs = reinterpret_cast<float*>(sm + S::kOffRef);
-    float* red = reinterpret_cast<float*>(sm + S::kOffRed);
-    const uint2* table = reinterpret_cast<const uint2*>(sm + S::kOffTable);
-
-    // ---- the query of a unit ----
-    auto put_query = [&](int req) {
-#pragma unroll 1
-      for (int k = 0; k < kRows / kWorkerWarps; ++k) {
-        const int r = warp * (kRows / kWorkerWarps) + k;
-        uint32_t w[9] = {};   // dims 16 lane .. + 15 of q_nope, 2 lane and + 1 of q_pe
-        if (row0 + r < H) {
-          const size_t row = static_cast<size_t>(req) * H + row0 + r;
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_nope) + row * kDCkv + 16 * lane);
-          const uint4 v0 = src[0], v1 = src[1];
-          w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w, w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
-          w[8] = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q_pe) + row * kDKpe)[lane];
-        }
-        uint32_t m = 0;
+    float* refs = reinterpret_cast<float*>(sm + S::kOffRef) + kJ * cg;
+    float* red = reinterpret_cast<float*>(sm + S::kOffRed) + 4 * cg * kJ;   // of the four warps of these query rows
+    constexpr int kLaneShift = kJ == 16 ? 1 : kJ == 8 ? 2 : 3;              // the row that warp_reduce leaves in a lane
+    int g = 0;
+    for (int ui = u0; ui < u1; ++ui) {
+      const WorkUnit u = a.units[ui];
+      const float* scale = reinterpret_cast<const float*>(sm + S::kOffScale) + ((ui - u0) & 1) * kRows + kJ * cg;
+      float lx[kJ], lr[kJ];
 #pragma unroll
-        for (int i = 0; i < 9; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-        const uint32_t top = __reduce_max_sync(~0u, max(m >> 16, m & 0xffffu));   // bits of the largest magnitude
-        const int e = top == 0 ? 0 : min(max(7 - (static_cast<int>(top >> 7) - 127), -100), 100);
-        const float up = pow2(e);
-        uint32_t hi[9], lo[9];
-#pragma unroll
-        for (int i = 0; i < 9; ++i)
-          split_query(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up, hi[i], lo[i]);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t* c = t ? lo : hi;
-          const int row = t * kRows + r;
-          *reinterpret_cast<uint4*>(sm + S::kOffQ + (lane >> 3) * S::kQPanel + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
-              make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
-          *reinterpret_cast<uint16_t*>(sm + S::kOffQPe + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7)) =
-              static_cast<uint16_t>(c[8]);
-        }
-        // an infinite or NaN query has NaN scores
-        if (lane == 0) scale[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff) : pow2(-e);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kQReady));
-    };
-
-    // ---- raw rows: a tile's 8 rows of this warp, 16 codes of ckv a lane and row, and
-    // of kpe 16 codes a lane (row lane / 4) ----
-    uint2 raw[kTokWarp], raw_pe;
-    uint32_t shifts, meta_pe;   // of row lane / 4: the shifts of groups 4 (lane % 4) ..; of kpe, and the exponent
-    Cursor ld;
-    ld.ui = u0;
-    ld.read(a.units);
-    bool ld_more = true;
-    int page = 0;
-    auto next_page = [&]() {
-      const int t = ld.tok0() + kTokWarp * warp;
-      page = ld_more && t < ld.tok_end ? a.kv_indices[ld.page_base + (t >> page_shift)] : 0;
-    };
-    next_page();
-    auto load_rows = [&]() {
-      const int t = ld.tok0() + kTokWarp * warp;
-      int n = ld_more ? min(kTokWarp, ld.tok_end - t) : 0;
-      if (n > 0 && (page < 0 || page >= a.num_pages)) {   // its rows count as zeros
-        if (lane == 0) report_error(a.err, kErrBounds);
-        n = 0;
-      }
-      const uint8_t* src = cache + ((static_cast<size_t>(n > 0 ? page : 0) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
-#pragma unroll
-      for (int r = 0; r < kTokWarp; ++r) {
-        raw[r] = make_uint2(0, 0);
-        if (r < n) raw[r] = __ldg(reinterpret_cast<const uint2*>(src + r * kQ4Row) + lane);
-      }
-      raw_pe = make_uint2(0, 0);
-      shifts = 0;
-      meta_pe = 127 << 8;
-      if ((lane >> 2) < n) {
-        const uint8_t* row = src + (lane >> 2) * kQ4Row;
-        raw_pe = __ldg(reinterpret_cast<const uint2*>(row + kDCkv / 2) + (lane & 3));
-        shifts = __ldg(reinterpret_cast<const uint16_t*>(row + kQ4Meta) + (lane & 3));
-        meta_pe = __ldg(reinterpret_cast<const uint16_t*>(row + kQ4Meta + 8));
-      }
-      if (ld_more) ld_more = ld.next(a.units, u1);
-      next_page();
-    };
-    auto expand = [&](int g) {
-      unsigned char* dst = sm + S::kOffK + (g & 1) * 4 * S::kPanel + (lane >> 3) * S::kPanel + kTokWarp * warp * 128;
-#pragma unroll
-      for (int r = 0; r < kTokWarp; ++r) {
-        const uint32_t mine = __shfl_sync(~0u, shifts, 4 * r + (lane >> 3));   // groups lane / 8 * 4 ..
-        const uint2 t = table[(mine >> (4 * ((lane >> 1) & 3))) & 15];
-        *reinterpret_cast<uint4*>(dst + r * 128 + (((lane & 7) ^ r) << 4)) = expand16(t, raw[r]);
-      }
-      const int row = kTokWarp * warp + (lane >> 2);
-      const uint2 t = table[(meta_pe >> (2 * (lane & 2))) & 15];
-      *reinterpret_cast<uint4*>(sm + S::kOffKPe + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) = expand16(t, raw_pe);
-      if ((lane & 3) == 0) sm[S::kOffExp + (g & 1) * kT + row] = static_cast<unsigned char>(meta_pe >> 8);
-      fence_proxy_async_smem();
-      __syncwarp();
-#ifdef MLA_STALL_TEST
-      if (blockIdx.x == 0 && warp == 0 && g + 1 == g_q4_stall) return;
-#endif
-      if (lane == 0) mbar_arrive(bar(kKFull0 + (g & 1)));
-    };
-
-    load_rows();
-    put_query(a.units[u0].req);
-    expand(0);
-    load_rows();
-    Cursor at;
-    at.ui = u0;
-    at.read(a.units);
-    float lx[kJ], lr[kJ];
-    for (int g = 0;; ++g) {
-      const bool first = at.tile == 0, last = at.tile + 1 == at.tiles, end = last && at.ui + 1 == u1;
-      // ---- tile g + 1: its buffer was read by P . V of g - 1, the rope part by the scores of g ----
-      if (!end) {
-        if (g > 0) wait(kPvDone0 + (warp >> 2), g - 1);
+      for (int j = 0; j < kJ; ++j) lx[j] = lr[j] = 0.f;
+      for (int t0 = u.tok_begin; t0 < u.tok_end; t0 += kT, ++g) {
+        const bool first = t0 == u.tok_begin;
+        // ---- scores of this thread's token and query rows, less the reference, in log2 ----
         wait(kSFull0 + (g & 1), g >> 1);
-        expand(g + 1);
-        load_rows();
-      }
-      // ---- scores of this thread's token and query rows, less the reference, in log2 ----
-      wait(kSFull0 + (g & 1), g >> 1);
-      tc_fence_after();
-      float z[kJ];
-      const int exponent = sm[S::kOffExp + (g & 1) * kT + tok];
-      const int e = exponent == kQ4NanExp ? 0 : exponent - 127;
-      {
-        uint32_t hi[kJ], lo[kJ];
-        const uint32_t col = S::kColS + (g & 1) * S::kNS + kJ * cg;
-        tmem_ld(lane_addr + col, hi);
-        tmem_ld(lane_addr + col + kRows, lo);
-        const float unit = exponent == kQ4NanExp ? __int_as_float(0x7fffffff) : pow2(e - 6) * (prm.sm_scale * kLog2e);
-        tmem_ld_wait();
-        const float fe = static_cast<float>(e);
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const float ref = first ? 0.f : refs[kJ * cg + j];
-          z[j] = fmaf((__uint_as_float(hi[j]) + __uint_as_float(lo[j])) * unit, scale[kJ * cg + j], fe - ref);
-        }
-      }
-      const int t = at.tok0() + tok;
-      if (at.tok0() + kT > at.tok_end - (prm.q_len > 1 ? prm.q_len - 1 : 0)) {
-        // the query rows that see token t: of query tokens packed into rows, row h sees
-        // the tokens before kv_len - (q_len - 1 - h / heads)
-        int from = t < at.tok_end ? 0 : 128;
-        if (prm.q_len > 1 && t < at.tok_end) from = min(128, prm.heads_per_token * max(0, prm.q_len - a.units[at.ui].kv_len + t));
-        from -= row0 + kJ * cg;
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) z[j] = j >= from ? z[j] : -INFINITY;
-      }
-      float top = z[0];
-#pragma unroll
-      for (int j = 1; j < kJ; ++j) top = fmaxf(top, z[j]);
-      if (first) {
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) lx[j] = lr[j] = 0.f;
-      }
-      // ---- the reference moves: the four warps of these query rows together ----
-      if (bar_any(1 + cg, 128, first || top > S::kTop)) {
-        float* mine = red + warp * 16;
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          float m = z[j];
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-          if (lane == j) mine[j] = m;
-        }
-        named_bar_sync(1 + cg, 128);
-        float alpha[kJ];
-        bool moved = false;
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const float* other = red + 4 * cg * 16 + j;
-          const float m = fmaxf(fmaxf(other[0], other[16]), fmaxf(other[32], other[48]));
-          // the largest p becomes 2^(kTop - kSlack); a row that sees no token in its unit's
-          // first tile sees none later, and keeps the reference 0 with p = 0
-          const float up = m > (first ? -INFINITY : S::kTop) ? m - (S::kTop - S::kSlack) : 0.f;
-          alpha[j] = first ? 1.f : fast_exp2(-up);
-          moved |= up != 0.f;
-          z[j] -= up;
-          lx[j] *= alpha[j];
-          lr[j] *= alpha[j];
-          if (q == 0 && lane == j) refs[kJ * cg + j] = (first ? 0.f : refs[kJ * cg + j]) + up;
-        }
-        if (!first && moved) {
-          wait(kPvDone0 + 3, g - 1);
-          tc_fence_after();
-#pragma unroll 1
-          for (int p = 0; p < 4; ++p) {
-#pragma unroll 1
-            for (int term = 0; term < (S::kSide ? 3 : 1); ++term) {
-              uint32_t o[kJ];
-              const uint32_t col = p * S::kOBlock + term * kRows + kJ * cg;
-              tmem_ld(lane_addr + col, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < kJ; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
-              tmem_st(lane_addr + col, o);
-            }
-          }
-          tmem_st_wait();
-          tc_fence_before();
-        }
-        named_bar_sync(1 + cg, 128);
-      }
-      // ---- p and its terms ----
-      constexpr int kTerms = S::kSide ? 3 : 2;
-      uint32_t c[kTerms][kJ / 4];
-      const float weight = pow2(-e);
-#pragma unroll
-      for (int j = 0; j < kJ; j += 2) {
-        const float p0 = fast_exp2(z[j]), p1 = fast_exp2(z[j + 1]);
-        lx[j] = fmaf(p0, weight, lx[j]);
-        lx[j + 1] = fmaf(p1, weight, lx[j + 1]);
-        const __half2 p = __floats2half2_rn(p0, p1);
-        uint32_t code[kTerms];
-        code[0] = to_fp8x2<__NV_E5M2>(p);
-        __half2 sum = from_fp8x2<__NV_E5M2>(code[0]);
-        if constexpr (S::kSide) {
-          code[1] = to_fp8x2<__NV_E5M2>(__hsub2(p, sum));
-          sum = __hadd2(sum, from_fp8x2<__NV_E5M2>(code[1]));
-          code[2] = to_fp8x2<__NV_E5M2>(__hsub2(p, sum));
-          sum = __hadd2(sum, from_fp8x2<__NV_E5M2>(code[2]));
-        } else {
-          code[1] = to_fp8x2<__NV_E4M3>(__hsub2(p, sum));
-          sum = __hadd2(sum, from_fp8x2<__NV_E4M3>(code[1]));
-        }
-        const float2 s = __half22float2(sum);
-        lr[j] = fmaf(p0 < S::kFull ? p0 : s.x, weight, lr[j]);
-        lr[j + 1] = fmaf(p1 < S::kFull ? p1 : s.y, weight, lr[j + 1]);
-#pragma unroll
-        for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
-      }
-      if (g > 0) wait(kPvDone0 + q, g - 1);   // P . V of the tile before has read these rows of P
-      unsigned char* prow = sm + S::kOffP + tok * S::kPRow;
-#pragma unroll
-      for (int i = 0; i < kTerms; ++i) {
-        if constexpr (kRows == 64)
-          *reinterpret_cast<uint4*>(prow + i * S::kPPanel + ((cg ^ ((tok >> 1) & 3)) << 4)) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
-        else if constexpr (kRows == 32)
-          *reinterpret_cast<uint2*>(prow + (((2 * i + (cg >> 1)) ^ (tok & 7)) << 4) + 8 * (cg & 1)) = make_uint2(c[i][0], c[i][1]);
-        else
-          *reinterpret_cast<uint32_t*>(prow + ((i ^ ((tok >> 1) & 3)) << 4) + 4 * cg) = c[i][0];
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kPReady0 + q));
-      if (last) {
-        // ---- the next unit's query, once every warp has done with this one's ----
-        if (!end) {
-          named_bar_sync(5, kWorkers);
-          put_query(a.units[at.ui + 1].req);
-        }
-        // ---- epilogue: the sums over this tile's tokens of all lanes and quadrants ----
-        const WorkUnit u = a.units[at.ui];
-        const bool split = u.out_slot >= 0;
-        float* mine = red + warp * 16;
-        const float* all = red + 4 * cg * 16;
-        float inv[kJ];
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          float s = lx[j];
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-          if (lane == j) mine[j] = s;
-        }
-        named_bar_sync(1 + cg, 128);
-        if (q == 0 && lane < kJ && row0 + kJ * cg + lane < H) {
-          const int h = row0 + kJ * cg + lane;
-          const float s = (all[lane] + all[16 + lane]) + (all[32 + lane] + all[48 + lane]);
-          const float lse = (refs[kJ * cg + lane] + log2f(s)) * kLn2;
-          if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
-          else a.lse[static_cast<size_t>(u.req) * H + h] = lse;
-        }
-        named_bar_sync(1 + cg, 128);
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          float s = lr[j];
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-          if (lane == j) mine[j] = s;
-        }
-        named_bar_sync(1 + cg, 128);
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const float s = (all[j] + all[16 + j]) + (all[32 + j] + all[48 + j]);
-          inv[j] = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
-        }
-        wait(kPvDone0 + 3, g);
         tc_fence_after();
-#pragma unroll 1
-        for (int p = 0; p < 4; ++p) {
-          uint32_t o[kJ];
-          float x[kJ];
-          tmem_ld(lane_addr + p * S::kOBlock + kJ * cg, o);
+        float z[kJ];
+        const int exponent = sm[S::kOffExp + (g & 1) * kT + tok];
+        const int e = exponent == kQ4NanExp ? 0 : exponent - 127;
+        {
+          uint32_t hi[kJ], lo[kJ];
+          const uint32_t col = S::kColS + (g & 1) * S::kNS + kJ * cg;
+          tmem_ld(lane_addr + col, hi);
+          tmem_ld(lane_addr + col + kRows, lo);
+          const float unit = exponent == kQ4NanExp ? __int_as_float(0x7fffffff) : pow2(e - 6) * (prm.sm_scale * kLog2e);
+          const float fe = static_cast<float>(e);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) x[j] = __uint_as_float(o[j]);
-          if constexpr (S::kSide) {
-#pragma unroll
-            for (int term = 1; term < 3; ++term) {
-              tmem_ld(lane_addr + p * S::kOBlock + term * kRows + kJ * cg, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < kJ; ++j) x[j] += __uint_as_float(o[j]);
-            }
-          }
-          const int d = 128 * p + tok;
-          const int h0 = row0 + kJ * cg;
-          const size_t row = static_cast<size_t>(u.req) * H + h0;
-          if (split) {
-#pragma unroll
-            for (int j = 0; j < kJ; ++j)
-              if (h0 + j < H) a.o_part[part_offset(u.out_slot, h0 + j, d, H)] = x[j] * inv[j];
-          } else if (kOutF32) {
-#pragma unroll
-            for (int j = 0; j < kJ; ++j)
-              if (h0 + j < H) static_cast<float*>(a.out)[(row + j) * kDCkv + d] = x[j] * inv[j];
-          } else {
-            // two lanes trade halves of two query rows: each stores two dims of one
-#pragma unroll
-            for (int j = 0; j < kJ; j += 2) {
-              const float x0 = x[j] * inv[j], x1 = x[j + 1] * inv[j + 1];
-              const bool odd = lane & 1;
-              const float got = __shfl_xor_sync(~0u, odd ? x0 : x1, 1);
-              const uint32_t w = odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got);
-              const int h = j + (odd ? 1 : 0);
-              if (h0 + h < H)
-                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row + h) * kDCkv + (d & ~1)) = w;
-            }
+          for (int j = 0; j < kJ; j += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(scale + j);
+            const float2 ref = *reinterpret_cast<const float2*>(refs + j);
+            const float2 s = add2(make_float2(__uint_as_float(hi[j]), __uint_as_float(hi[j + 1])),
+                                  make_float2(__uint_as_float(lo[j]), __uint_as_float(lo[j + 1])));
+            const float2 b = first ? make_float2(fe, fe) : make_float2(fe - ref.x, fe - ref.y);
+            const float2 y = fma2(mul2(s, make_float2(unit, unit)), f, b);
+            z[j] = y.x;
+            z[j + 1] = y.y;
           }
         }
-        tc_fence_before();   // O is read: the next unit's first P . V waits for P of all warps
-        named_bar_sync(1 + cg, 128);   // red and the references may be written again
+        if (t0 + kT > u.tok_end - (prm.q_len > 1 ? prm.q_len - 1 : 0)) {
+          // the query rows that see token t: of query tokens packed into rows, row h sees
+          // the tokens before kv_len - (q_len - 1 - h / heads)
+          const int t = t0 + tok;
+          int from = t < u.tok_end ? 0 : 128;
+          if (prm.q_len > 1 && t < u.tok_end) from = min(128, prm.heads_per_token * max(0, prm.q_len - u.kv_len + t));
+          from -= row0 + kJ * cg;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) z[j] = j >= from ? z[j] : -INFINITY;
+        }
+        float top = z[0];
+#pragma unroll
+        for (int j = 1; j < kJ; ++j) top = fmaxf(top, z[j]);
+        // ---- the reference moves: the four warps of these query rows together ----
+        if (bar_any(1 + cg, 128, first || top > S::kTop)) {
+          const float most = warp_reduce<true>(z);
+          if ((lane & ((1 << kLaneShift) - 1)) == 0) red[q * kJ + (lane >> kLaneShift)] = most;
+          named_bar_sync(1 + cg, 128);
+          float alpha[kJ];
+          bool moved = false;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            const float m = fmaxf(fmaxf(red[j], red[kJ + j]), fmaxf(red[2 * kJ + j], red[3 * kJ + j]));
+            // the largest p becomes 2^(kTop - kSlack); a row that sees no token in its unit's
+            // first tile sees none later, and keeps the reference 0 with p = 0
+            const float up = m > (first ? -INFINITY : S::kTop) ? m - (S::kTop - S::kSlack) : 0.f;
+            alpha[j] = first ? 1.f : fast_exp2(-up);
+            moved |= up != 0.f;
+            z[j] -= up;
+            lx[j] *= alpha[j];
+            lr[j] *= alpha[j];
+            if (q == 0 && lane == j) refs[j] = (first ? 0.f : refs[j]) + up;
+          }
+          if (!first && moved) {
+            wait(kPvDone0 + 3, g - 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int p = 0; p < 4; ++p) {
+#pragma unroll 1
+              for (int term = 0; term < (S::kSide ? 3 : 1); ++term) {
+                uint32_t o[kJ];
+                const uint32_t col = p * S::kOBlock + term * kRows + kJ * cg;
+                tmem_ld(lane_addr + col, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
+                tmem_st(lane_addr + col, o);
+              }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          named_bar_sync(1 + cg, 128);
+        }
+        // ---- p and its terms ----
+        constexpr int kTerms = S::kSide ? 3 : 2;
+        uint32_t c[kTerms][kJ / 4];
+        const float2 weight = make_float2(pow2(-e), pow2(-e));
+#pragma unroll
+        for (int j = 0; j < kJ; j += 2) {
+          const float2 p = make_float2(fast_exp2(z[j]), fast_exp2(z[j + 1]));
+          const float2 x = fma2(p, weight, make_float2(lx[j], lx[j + 1]));
+          lx[j] = x.x;
+          lx[j + 1] = x.y;
+          const __half2 h = __floats2half2_rn(p.x, p.y);
+          uint32_t code[kTerms];
+          code[0] = to_fp8x2<__NV_E5M2>(h);
+          __half2 sum = from_fp8x2<__NV_E5M2>(code[0]);
+          if constexpr (S::kSide) {
+            code[1] = to_fp8x2<__NV_E5M2>(__hsub2(h, sum));
+            sum = __hadd2(sum, from_fp8x2<__NV_E5M2>(code[1]));
+            code[2] = to_fp8x2<__NV_E5M2>(__hsub2(h, sum));
+            sum = __hadd2(sum, from_fp8x2<__NV_E5M2>(code[2]));
+          } else {
+            code[1] = to_fp8x2<__NV_E4M3>(__hsub2(h, sum));
+            sum = __hadd2(sum, from_fp8x2<__NV_E4M3>(code[1]));
+          }
+          const float2 r = __half22float2(sum);
+          const float2 y = fma2(make_float2(p.x < S::kFull ? p.x : r.x, p.y < S::kFull ? p.y : r.y), weight, make_float2(lr[j], lr[j + 1]));
+          lr[j] = y.x;
+          lr[j + 1] = y.y;
+#pragma unroll
+          for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
+        }
+        if (g > 0) wait(kPvDone0 + q, g - 1);   // P . V of the tile before has read these rows of P
+        unsigned char* prow = sm + S::kOffP + tok * S::kPRow;
+#pragma unroll
+        for (int i = 0; i < kTerms; ++i) {
+          if constexpr (kRows == 64)
+            *reinterpret_cast<uint4*>(prow + i * S::kPPanel + ((cg ^ ((tok >> 1) & 3)) << 4)) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+          else if constexpr (kRows == 32)
+            *reinterpret_cast<uint2*>(prow + (((2 * i + (cg >> 1)) ^ (tok & 7)) << 4) + 8 * (cg & 1)) = make_uint2(c[i][0], c[i][1]);
+          else
+            *reinterpret_cast<uint32_t*>(prow + ((i ^ ((tok >> 1) & 3)) << 4) + 4 * cg) = c[i][0];
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPReady0 + q));
       }
-      if (end) break;
-      at.next(a.units, u1);
+      // ---- epilogue: the sums over the unit's tokens of all lanes and quadrants ----
+      const bool split = u.out_slot >= 0;
+      const float sx = warp_reduce<false>(lx);
+      if ((lane & ((1 << kLaneShift) - 1)) == 0) red[q * kJ + (lane >> kLaneShift)] = sx;
+      named_bar_sync(1 + cg, 128);
+      if (q == 0 && lane < kJ && row0 + kJ * cg + lane < H) {
+        const int h = row0 + kJ * cg + lane;
+        const float s = (red[lane] + red[kJ + lane]) + (red[2 * kJ + lane] + red[3 * kJ + lane]);
+        const float lse = (refs[lane] + log2f(s)) * kLn2;
+        if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
+        else a.lse[static_cast<size_t>(u.req) * H + h] = lse;
+      }
+      named_bar_sync(1 + cg, 128);
+      const float sr = warp_reduce<false>(lr);
+      if ((lane & ((1 << kLaneShift) - 1)) == 0) red[q * kJ + (lane >> kLaneShift)] = sr;
+      named_bar_sync(1 + cg, 128);
+      float inv[kJ];
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const float s = (red[j] + red[kJ + j]) + (red[2 * kJ + j] + red[3 * kJ + j]);
+        inv[j] = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
+      }
+      wait(kPvDone0 + 3, g - 1);
+      tc_fence_after();
+#pragma unroll 1
+      for (int p = 0; p < 4; ++p) {
+        uint32_t o[kJ];
+        float x[kJ];
+        tmem_ld(lane_addr + p * S::kOBlock + kJ * cg, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) x[j] = __uint_as_float(o[j]);
+        if constexpr (S::kSide) {
+#pragma unroll
+          for (int term = 1; term < 3; ++term) {
+            tmem_ld(lane_addr + p * S::kOBlock + term * kRows + kJ * cg, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) x[j] += __uint_as_float(o[j]);
+          }
+        }
+        const int d = 128 * p + tok;
+        const int h0 = row0 + kJ * cg;
+        const size_t row = static_cast<size_t>(u.req) * H + h0;
+        if (split) {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+            if (h0 + j < H) a.o_part[part_offset(u.out_slot, h0 + j, d, H)] = x[j] * inv[j];
+        } else if (kOutF32) {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+            if (h0 + j < H) static_cast<float*>(a.out)[(row + j) * kDCkv + d] = x[j] * inv[j];
+        } else {
+          // two lanes trade halves of two query rows: each stores two dims of one
+#pragma unroll
+          for (int j = 0; j < kJ; j += 2) {
+            const float x0 = x[j] * inv[j], x1 = x[j + 1] * inv[j + 1];
+            const bool odd = lane & 1;
+            const float got = __shfl_xor_sync(~0u, odd ? x0 : x1, 1);
+            const uint32_t w = odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got);
+            const int h = j + (odd ? 1 : 0);
+            if (h0 + h < H)
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row + h) * kDCkv + (d & ~1)) = w;
+          }
+        }
+      }
+      tc_fence_before();             // O is read: the next unit's first P . V waits for P of all warps
+      named_bar_sync(1 + cg, 128);   // red and the references may be written again
     }
     if (!ok && lane == 0) report_error(a.err, kErrTimeout);
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWorkerWarps) {
+  if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
