@@ -31,15 +31,16 @@
 //
 // The softmax's state is kept per query row: a reference that moves (and O with
 // it) when a score passes it by more than kSlack, and two sums in fp32 per
-// thread: of the exact p for the lse, and for the output of the p that its terms
-// stand for.  A weight is p / 2^E_t, one more factor a token.  A p too small for
-// all its bits enters both sums as it is: the row of a small E_t may weigh much
-// and hold little, so that its p is rounded coarsely, or away.
+// thread: of the exact p, for the lse, and of what the terms leave of it, for the
+// output is divided by the sum of the p that P stands for.  A weight is p / 2^E_t,
+// one more factor a token.  A p too small for all its bits counts as it is in
+// both: the row of a small E_t may weigh much and hold little, so that its p is
+// rounded coarsely, or away.
 //
-// Roles: eight warps expand tiles, up to a tile ahead of the products, with the
-// raw rows of the next one on their way into registers; 16 warps make P; one
-// issues the MMAs, scores of tile g + 1 before P . V of tile g.  Registers are
-// dealt out by role.  Waits are bounded (2 s): a warp that gives up says so, and
+// Roles: 8 or 16 warps expand tiles, up to a tile ahead of the products, with the
+// raw rows of the next one on their way into registers; a warp for each 32 tokens
+// and 16 query rows makes P; one issues the MMAs, scores of tile g + 1 before P . V
+// of tile g.  Registers are dealt out by role.  Waits are bounded (2 s): a warp that gives up says so, and
 // goes on without waiting, so that the named barriers and commits of the others
 // still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is recorded.
 #include <cuda_bf16.h>
@@ -64,17 +65,9 @@ __device__ int g_q4_stall;
 #endif
 
 constexpr int kT = kTileTc;                   // 128 tokens to a tile
-constexpr int kSoftmaxWarps = 16;             // warps 0 ..: a lane quadrant and a quarter of the query rows each
-constexpr int kExpandWarps = 8;               // warps 16 ..
-constexpr int kIssueWarp = kSoftmaxWarps + kExpandWarps;
-constexpr int kThreads = 32 * (kIssueWarp + 4);   // whole warpgroups
-constexpr int kTokWarp = kT / kExpandWarps;   // rows that a warp expands
-// Registers a thread: 72 at launch (896 x 72 = 64512 of 65536), then by role.
-constexpr int kRegsSoftmax = 88, kRegsExpand = 64, kRegsIssue = 24;
-static_assert(32 * (kSoftmaxWarps * kRegsSoftmax + kExpandWarps * kRegsExpand + 4 * kRegsIssue) <= kThreads * 72, "registers");
+constexpr int kJ = 16;                        // query rows of a softmax warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-static_assert(kTokWarp == 16, "rows of a warp lie in one page");
 
 template <int kRows>
 struct Shape {
@@ -84,9 +77,20 @@ struct Shape {
   static constexpr int kPRow = kRows == 32 ? 128 : 64;     // bytes of a token's row of P
   static constexpr int kPPanel = kT * kPRow;
   static constexpr SmemSwizzle kPSwizzle = kRows == 32 ? kSw128 : kSw64;
-  static constexpr int kWarpRows = kRows / 4;              // query rows of a warp's softmax
+  // warps: softmax (a lane quadrant and kJ query rows each), expanding, issue (a whole
+  // warpgroup, for the registers)
+  static constexpr int kSoftmaxWarps = kRows / 4;
+  static constexpr int kExpandWarps = kRows == 64 ? 8 : 16;
+  static constexpr int kIssueWarp = kSoftmaxWarps + kExpandWarps;
+  static constexpr int kThreads = 32 * (kIssueWarp + 4);
+  static constexpr int kTokWarp = kT / kExpandWarps;       // rows that a warp expands, of one page
+  // registers a thread at launch, then by role
+  static constexpr int kRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kRegsSoftmax = kRows == 16 ? 128 : kRows == 32 ? 104 : 88, kRegsExpand = kRows == 16 ? 72 : 64;
+  static constexpr int kRegsIssue = 24;
+  static_assert(32 * (kSoftmaxWarps * kRegsSoftmax + kExpandWarps * kRegsExpand + 4 * kRegsIssue) <= kThreads * kRegs, "registers");
   // p reaches 2^kTop: the reference is set to leave kSlack of that, and moves when it is used up
-  static constexpr float kTop = kSide ? 15.f : 12.f, kSlack = 5.f;
+  static constexpr float kTop = kSide ? 15.f : 12.f, kSlack = kSide ? 8.f : 7.f;
   // p from here on has all its bits (the last term's least unit is 2^-16, 2^-9)
   static constexpr float kFull = kSide ? 0x1p-8f : 0x1p-2f;
   // tensor memory columns
@@ -105,15 +109,15 @@ struct Shape {
   static constexpr int kOffScale = kOffExp + 2 * kT;       // [2][rows] 1 / query scale, by unit parity
   static constexpr int kOffRef = kOffScale + 2 * kRows * 4;   // [rows] reference, less kTop - kSlack
   static constexpr int kOffTable = kOffRef + kRows * 4;    // [4] e4m3 codes of the magnitudes, for shifts 12 ..
-  static constexpr int kOffRed = kOffTable + 4 * 8;        // [16 warps][kWarpRows] floats
-  static constexpr int kOffBar = kOffRed + kSoftmaxWarps * kWarpRows * 4;
+  static constexpr int kOffRed = kOffTable + 4 * 8;        // [softmax warps][kJ] floats
+  static constexpr int kOffBar = kOffRed + kSoftmaxWarps * kJ * 4;
   static_assert(kOffP % 1024 == 0 && kOffK % 1024 == 0 && kOffKPe % 1024 == 0, "swizzle atoms");
 };
 
 enum Bar {
   kKFull0,                   // [2] tile expanded (a signal of every expanding warp)
   kSFull0 = kKFull0 + 2,     // [2] scores made
-  kPReady0 = kSFull0 + 2,    // [4] P of 32 tokens written (4 warps)
+  kPReady0 = kSFull0 + 2,    // [4] P of 32 tokens written (a signal for every 16 query rows)
   kPvDone0 = kPReady0 + 4,   // [4] P . V over 32 tokens made: their rows of K and P may be written again
   kQReady = kPvDone0 + 4,    // the unit's query in place
   kFinal,
@@ -130,34 +134,7 @@ constexpr uint32_t idesc_f8(int N, int b_format, bool mn) {
   return (1u << 4) | (static_cast<uint32_t>(b_format) << 10) | (static_cast<uint32_t>(mn) << 15) |
          (static_cast<uint32_t>(mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
-// The second MMA of two with the same A takes it from where the first left it.
-enum class KeepA { kNo, kFill, kLast };
-template <KeepA kKeep = KeepA::kNo>
 __device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (kKeep == KeepA::kFill) {
-    asm volatile(
-        "{\n"
-        ".reg .pred p, q;\n"
-        "elect.sync _|q, 0xffffffff;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-    return;
-  }
-  if constexpr (kKeep == KeepA::kLast) {
-    asm volatile(
-        "{\n"
-        ".reg .pred p, q;\n"
-        "elect.sync _|q, 0xffffffff;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-    return;
-  }
   asm volatile(
       "{\n"
       ".reg .pred p, q;\n"
@@ -169,17 +146,7 @@ __device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
-// A warp's 32 lanes x N consecutive columns of tensor memory.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
+// A warp's 32 lanes x 16 consecutive columns of tensor memory.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -187,22 +154,12 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
 }
 
 // A barrier of `threads` threads that also tells whether any of them says so.
@@ -239,10 +196,10 @@ __device__ __forceinline__ void split_query(float x0, float x1, uint32_t& hi, ui
 __device__ __forceinline__ uint32_t expand4(uint2 table, uint32_t select, uint32_t signs) {
   return __byte_perm(table.x, table.y, select) | (signs & 0x80808080u);
 }
-__device__ __forceinline__ uint4 expand16(uint2 table, uint2 w) {
-  const uint32_t a = w.x & 0x77777777u, b = w.y & 0x77777777u;
-  return make_uint4(expand4(table, a, w.x), expand4(table, a >> 16, w.x << 4), expand4(table, b, w.y),
-                    expand4(table, b >> 16, w.y << 4));
+__device__ __forceinline__ uint4 expand16(uint2 table, uint32_t w0, uint32_t w1) {
+  const uint32_t a = w0 & 0x77777777u, b = w1 & 0x77777777u;
+  return make_uint4(expand4(table, a, w0), expand4(table, a >> 16, w0 << 4), expand4(table, b, w1),
+                    expand4(table, b >> 16, w1 << 4));
 }
 // e4m3 codes of magnitude * 2^(6 - shift): up to a shift of 11 all are normal
 // numbers, whose exponent field starts at bit 3.
@@ -323,11 +280,11 @@ struct Cursor {
 };
 
 template <int kRows, bool kOutF32>
-__global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(const DecodeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using S = Shape<kRows>;
-  constexpr int kJ = S::kWarpRows;
+  constexpr int kSoftmaxWarps = S::kSoftmaxWarps, kExpandWarps = S::kExpandWarps, kIssueWarp = S::kIssueWarp, kTokWarp = S::kTokWarp;
   extern __shared__ __align__(1024) unsigned char sm[];
   const uint32_t base = smem_u32(sm);
   auto bar = [&](int i) { return base + S::kOffBar + 8 * i; };
@@ -346,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i < kSFull0 || i == kQReady ? kExpandWarps : i >= kPReady0 && i < kPvDone0 ? 4 : 1);
+      mbar_init(bar(i), i < kSFull0 || i == kQReady ? kExpandWarps : i >= kPReady0 && i < kPvDone0 ? kSoftmaxWarps / 4 : 1);
     fence_barrier_init();
   }
   if (threadIdx.x < 4) {
@@ -370,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
   auto wait = [&](int i, int phase) { ok &= mbar_spin<false>(bar(i), phase & 1, abort_flag); };
 
   if (warp >= kIssueWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsIssue));
     if (warp == kIssueWarp) {
       // ================= the issuing warp =================
       const uint64_t k_desc = smem_desc(base + S::kOffK, 16, 1024, kSw128);
@@ -432,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
     }
   } else if (warp >= kSoftmaxWarps) {
     // ================= expanding warps =================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsExpand));
     if (u0 < u1) {
       const int ew = warp - kSoftmaxWarps;
       const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
@@ -446,10 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
         const int t = ld.tok0() + kTokWarp * ew;
         if (more && t < ld.tok_end) page = a.kv_indices[ld.page_base + (t >> page_shift)];
       };
-      // 16 rows: 16 codes of ckv a lane and row; of kpe and the shifts a quarter of rows
-      // lane / 4 and 8 + lane / 4
-      uint2 raw[kTokWarp], raw_pe[2];
-      uint32_t shifts[2], meta_pe[2];
+      // A lane takes whole groups (16 bytes of codes): of ckv, group 4 (lane / 8) + lane % 4
+      // of row 2 i + lane / 4 % 2 for each i, so that eight lanes write to eight groups of
+      // banks; of kpe, group lane % 2 of row lane / 2.  Shifts of ckv: four of row 8 i +
+      // lane / 4 a lane.
+      const int panel = lane >> 3, odd = (lane >> 2) & 1, pair = lane & 3;
+      uint4 raw[kTokWarp / 2], raw_pe;
+      uint32_t shifts[kTokWarp / 8], meta_pe;
       auto load_rows = [&]() {
         const int t = ld.tok0() + kTokWarp * ew;
         int n = more ? min(kTokWarp, ld.tok_end - t) : 0;
@@ -459,46 +419,51 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
         }
         const uint8_t* src = cache + ((static_cast<size_t>(n > 0 ? page : 0) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 8 * i + (lane >> 2);
-          const uint8_t* row = src + r * kQ4Row + kDCkv / 2;
-          raw_pe[i] = make_uint2(0, 0);
-          shifts[i] = 0;
-          meta_pe[i] = 127 << 8;
-          if (r < n) {
-            raw_pe[i] = __ldg(reinterpret_cast<const uint2*>(row) + (lane & 3));
-            shifts[i] = __ldg(reinterpret_cast<const uint16_t*>(row + 32) + (lane & 3));
-            meta_pe[i] = __ldg(reinterpret_cast<const uint16_t*>(row + 40));
-          }
+        for (int i = 0; i < kTokWarp / 2; ++i) {
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (2 * i + odd < n) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (2 * i + odd) * kQ4Row) + 4 * panel + pair);
         }
 #pragma unroll
-        for (int r = 0; r < kTokWarp; ++r) {
-          raw[r] = make_uint2(0, 0);
-          if (r < n) raw[r] = __ldg(reinterpret_cast<const uint2*>(src + r * kQ4Row) + lane);
+        for (int i = 0; i < kTokWarp / 8; ++i) {
+          shifts[i] = 0;
+          if (8 * i + (lane >> 2) < n) shifts[i] = __ldg(reinterpret_cast<const uint16_t*>(src + (8 * i + (lane >> 2)) * kQ4Row + kQ4Meta) + pair);
+        }
+        raw_pe = make_uint4(0, 0, 0, 0);
+        meta_pe = 127 << 8;
+        if ((lane >> 1) < n) {
+          const uint8_t* row = src + (lane >> 1) * kQ4Row;
+          raw_pe = __ldg(reinterpret_cast<const uint4*>(row + kDCkv / 2) + (lane & 1));
+          meta_pe = __ldg(reinterpret_cast<const uint16_t*>(row + kQ4Meta + 8));
         }
         if (more) more = ld.next(a.units, u1);
         next_page();
       };
       auto expand = [&](int g) {
-        unsigned char* dst = sm + S::kOffK + (g & 1) * 4 * S::kPanel + (lane >> 3) * S::kPanel + kTokWarp * ew * 128;
         // shifts past 11 lead to subnormal numbers, by a table
-        const uint32_t both = shifts[0] | shifts[1] << 16;
-        const bool far = __any_sync(~0u, ((both & (both << 1)) & 0x88888888u) | ((meta_pe[0] & (meta_pe[0] << 1)) & 0x88u) |
-                                             ((meta_pe[1] & (meta_pe[1] << 1)) & 0x88u));
-        auto table_of = [&](uint32_t k) { return far && k >= 12 ? table[k - 12] : normal_table(k); };
+        uint32_t large = (meta_pe & (meta_pe << 1)) & 0x88u;
 #pragma unroll
-        for (int r = 0; r < kTokWarp; ++r) {
-          const uint32_t mine = __shfl_sync(~0u, shifts[r / 8], 4 * (r % 8) + (lane >> 3));   // groups lane / 8 * 4 ..
-          *reinterpret_cast<uint4*>(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) =
-              expand16(table_of((mine >> (2 * (lane & 6))) & 15), raw[r]);
-        }
+        for (int i = 0; i < kTokWarp / 8; ++i) large |= shifts[i] & (shifts[i] << 1) & 0x8888u;
+        auto fill = [&](auto table_of) {
+          unsigned char* dst = sm + S::kOffK + (g & 1) * 4 * S::kPanel + panel * S::kPanel + (kTokWarp * ew + odd) * 128;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = kTokWarp * ew + 8 * i + (lane >> 2);
-          *reinterpret_cast<uint4*>(sm + S::kOffKPe + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) =
-              expand16(table_of((meta_pe[i] >> (2 * (lane & 2))) & 15), raw_pe[i]);
-          if ((lane & 3) == 0) sm[S::kOffExp + (g & 1) * kT + row] = static_cast<unsigned char>(meta_pe[i] >> 8);
-        }
+          for (int i = 0; i < kTokWarp / 2; ++i) {
+            const uint32_t mine = __shfl_sync(~0u, shifts[i / 4], 8 * (i % 4) + 4 * odd + panel);   // of groups 4 panel ..
+            const uint2 t = table_of((mine >> (4 * pair)) & 15);
+            const int at = 256 * i + ((2 * pair ^ ((2 * i + odd) & 7)) << 4);
+            *reinterpret_cast<uint4*>(dst + at) = expand16(t, raw[i].x, raw[i].y);
+            *reinterpret_cast<uint4*>(dst + (at ^ 16)) = expand16(t, raw[i].z, raw[i].w);
+          }
+          if (kTokWarp == 16 || lane < 16) {
+            const int row = kTokWarp * ew + (lane >> 1);
+            const uint2 t = table_of((meta_pe >> (4 * (lane & 1))) & 15);
+            const int at = row * 64 + (((2 * (lane & 1)) ^ ((row >> 1) & 3)) << 4);
+            *reinterpret_cast<uint4*>(sm + S::kOffKPe + at) = expand16(t, raw_pe.x, raw_pe.y);
+            *reinterpret_cast<uint4*>(sm + S::kOffKPe + (at ^ 16)) = expand16(t, raw_pe.z, raw_pe.w);
+            if ((lane & 1) == 0) sm[S::kOffExp + (g & 1) * kT + row] = static_cast<unsigned char>(meta_pe >> 8);
+          }
+        };
+        if (__any_sync(~0u, large)) fill([&](uint32_t k) { return k >= 12 ? table[k - 12] : normal_table(k); });
+        else fill([](uint32_t k) { return normal_table(k); });
         fence_proxy_async_smem();
         __syncwarp();
 #ifdef MLA_STALL_TEST
@@ -554,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
         const int n = (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
         for (int i = 0; i < n; ++i, ++g) {
           // the buffer was read by P . V of g - 2, the rope part and the query by the scores of g - 1
-          if (g > 1) wait(kPvDone0 + (ew >> 1), g - 2);
+          if (g > 1) wait(kPvDone0 + ew * kTokWarp / 32, g - 2);
           if (g > 0) wait(kSFull0 + ((g - 1) & 1), (g - 1) >> 1);
           expand(g);
           load_rows();
@@ -565,20 +530,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
     }
   } else {
     // ================= softmax and epilogue =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoftmax));
     const int q = warp & 3, cg = warp >> 2;             // tokens 32 q .. of a tile (lane quadrant), query rows kJ cg ..
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const int tok = 32 * q + lane;
     float* refs = reinterpret_cast<float*>(sm + S::kOffRef) + kJ * cg;
     float* red = reinterpret_cast<float*>(sm + S::kOffRed) + 4 * cg * kJ;   // of the four warps of these query rows
-    constexpr int kLaneShift = kJ == 16 ? 1 : kJ == 8 ? 2 : 3;              // the row that warp_reduce leaves in a lane
     int g = 0;
     for (int ui = u0; ui < u1; ++ui) {
       const WorkUnit u = a.units[ui];
       const float* scale = reinterpret_cast<const float*>(sm + S::kOffScale) + ((ui - u0) & 1) * kRows + kJ * cg;
-      float lx[kJ], lr[kJ];
+      float lx[kJ], ld[kJ];
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) lx[j] = lr[j] = 0.f;
+      for (int j = 0; j < kJ; ++j) lx[j] = ld[j] = 0.f;
       for (int t0 = u.tok_begin; t0 < u.tok_end; t0 += kT, ++g) {
         const bool first = t0 == u.tok_begin;
         // ---- scores of this thread's token and query rows, less the reference, in log2 ----
@@ -623,39 +587,42 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
         // ---- the reference moves: the four warps of these query rows together ----
         if (bar_any(1 + cg, 128, first || top > S::kTop)) {
           const float most = warp_reduce<true>(z);
-          if ((lane & ((1 << kLaneShift) - 1)) == 0) red[q * kJ + (lane >> kLaneShift)] = most;
+          if ((lane & 1) == 0) red[q * kJ + (lane >> 1)] = most;
           named_bar_sync(1 + cg, 128);
-          float alpha[kJ];
-          bool moved = false;
+          uint32_t moved = 0;
+          float mine = 1.f;   // lane j: the factor of row j
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             const float m = fmaxf(fmaxf(red[j], red[kJ + j]), fmaxf(red[2 * kJ + j], red[3 * kJ + j]));
             // the largest p becomes 2^(kTop - kSlack); a row that sees no token in its unit's
             // first tile sees none later, and keeps the reference 0 with p = 0
             const float up = m > (first ? -INFINITY : S::kTop) ? m - (S::kTop - S::kSlack) : 0.f;
-            alpha[j] = first ? 1.f : fast_exp2(-up);
-            moved |= up != 0.f;
             z[j] -= up;
-            lx[j] *= alpha[j];
-            lr[j] *= alpha[j];
+            if (!first && up != 0.f) {
+              moved |= 1u << j;
+              const float alpha = fast_exp2(-up);
+              lx[j] *= alpha;
+              ld[j] *= alpha;
+              if (lane == j) mine = alpha;
+            }
             if (q == 0 && lane == j) refs[j] = (first ? 0.f : refs[j]) + up;
           }
-          if (!first && moved) {
+          if (moved) {   // their columns of O, a row at a time: few move at once
             wait(kPvDone0 + 3, g - 1);
             tc_fence_after();
-#pragma unroll 1
-            for (int p = 0; p < 4; ++p) {
-#pragma unroll 1
-              for (int term = 0; term < (S::kSide ? 3 : 1); ++term) {
-                uint32_t o[kJ];
-                const uint32_t col = p * S::kOBlock + term * kRows + kJ * cg;
-                tmem_ld(lane_addr + col, o);
-                tmem_ld_wait();
+            do {
+              const int j = __ffs(moved) - 1;
+              moved &= moved - 1;
+              constexpr int kCols = S::kSide ? 12 : 4;
+              uint32_t o[kCols];
 #pragma unroll
-                for (int j = 0; j < kJ; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
-                tmem_st(lane_addr + col, o);
-              }
-            }
+              for (int i = 0; i < kCols; ++i) tmem_ld(lane_addr + (i & 3) * S::kOBlock + (i >> 2) * kRows + kJ * cg + j, o[i]);
+              const float alpha = __shfl_sync(~0u, mine, j);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < kCols; ++i)
+                tmem_st(lane_addr + (i & 3) * S::kOBlock + (i >> 2) * kRows + kJ * cg + j, __float_as_uint(__uint_as_float(o[i]) * alpha));
+            } while (moved);
             tmem_st_wait();
             tc_fence_before();
           }
@@ -674,20 +641,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
           const __half2 h = __floats2half2_rn(p.x, p.y);
           uint32_t code[kTerms];
           code[0] = to_fp8x2<__NV_E5M2>(h);
-          __half2 sum = from_fp8x2<__NV_E5M2>(code[0]);
+          __half2 rest = __hsub2(h, from_fp8x2<__NV_E5M2>(code[0]));   // exact
           if constexpr (S::kSide) {
-            code[1] = to_fp8x2<__NV_E5M2>(__hsub2(h, sum));
-            sum = __hadd2(sum, from_fp8x2<__NV_E5M2>(code[1]));
-            code[2] = to_fp8x2<__NV_E5M2>(__hsub2(h, sum));
-            sum = __hadd2(sum, from_fp8x2<__NV_E5M2>(code[2]));
+            code[1] = to_fp8x2<__NV_E5M2>(rest);
+            rest = __hsub2(rest, from_fp8x2<__NV_E5M2>(code[1]));
+            code[2] = to_fp8x2<__NV_E5M2>(rest);
+            rest = __hsub2(rest, from_fp8x2<__NV_E5M2>(code[2]));
           } else {
-            code[1] = to_fp8x2<__NV_E4M3>(__hsub2(h, sum));
-            sum = __hadd2(sum, from_fp8x2<__NV_E4M3>(code[1]));
+            code[1] = to_fp8x2<__NV_E4M3>(rest);
+            rest = __hsub2(rest, from_fp8x2<__NV_E4M3>(code[1]));
           }
-          const float2 r = __half22float2(sum);
-          const float2 y = fma2(make_float2(p.x < S::kFull ? p.x : r.x, p.y < S::kFull ? p.y : r.y), weight, make_float2(lr[j], lr[j + 1]));
-          lr[j] = y.x;
-          lr[j + 1] = y.y;
+          // what the terms leave of p, counted in full from kFull on and less below
+          const float2 share = mul2(make_float2(__saturatef(p.x * (1 / S::kFull)), __saturatef(p.y * (1 / S::kFull))), weight);
+          const float2 y = fma2(__half22float2(rest), share, make_float2(ld[j], ld[j + 1]));
+          ld[j] = y.x;
+          ld[j + 1] = y.y;
 #pragma unroll
           for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
         }
@@ -695,12 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
         unsigned char* prow = sm + S::kOffP + tok * S::kPRow;
 #pragma unroll
         for (int i = 0; i < kTerms; ++i) {
-          if constexpr (kRows == 64)
-            *reinterpret_cast<uint4*>(prow + i * S::kPPanel + ((cg ^ ((tok >> 1) & 3)) << 4)) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
-          else if constexpr (kRows == 32)
-            *reinterpret_cast<uint2*>(prow + (((2 * i + (cg >> 1)) ^ (tok & 7)) << 4) + 8 * (cg & 1)) = make_uint2(c[i][0], c[i][1]);
-          else
-            *reinterpret_cast<uint32_t*>(prow + ((i ^ ((tok >> 1) & 3)) << 4) + 4 * cg) = c[i][0];
+          const int at = kRows == 64   ? i * S::kPPanel + ((cg ^ ((tok >> 1) & 3)) << 4)
+                         : kRows == 32 ? ((2 * i + cg) ^ (tok & 7)) << 4
+                                       : (i ^ ((tok >> 1) & 3)) << 4;
+          *reinterpret_cast<uint4*>(prow + at) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -710,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
       // ---- epilogue: the sums over the unit's tokens of all lanes and quadrants ----
       const bool split = u.out_slot >= 0;
       const float sx = warp_reduce<false>(lx);
-      if ((lane & ((1 << kLaneShift) - 1)) == 0) red[q * kJ + (lane >> kLaneShift)] = sx;
+      if ((lane & 1) == 0) red[q * kJ + (lane >> 1)] = sx;
       named_bar_sync(1 + cg, 128);
       if (q == 0 && lane < kJ && row0 + kJ * cg + lane < H) {
         const int h = row0 + kJ * cg + lane;
@@ -720,8 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q4_kernel(const DecodeArgs
         else a.lse[static_cast<size_t>(u.req) * H + h] = lse;
       }
       named_bar_sync(1 + cg, 128);
-      const float sr = warp_reduce<false>(lr);
-      if ((lane & ((1 << kLaneShift) - 1)) == 0) red[q * kJ + (lane >> kLaneShift)] = sr;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) lx[j] -= ld[j];   // of what P stands for
+      const float sr = warp_reduce<false>(lx);
+      if ((lane & 1) == 0) red[q * kJ + (lane >> 1)] = sr;
       named_bar_sync(1 + cg, 128);
       float inv[kJ];
 #pragma unroll
@@ -791,7 +759,7 @@ template <int kRows, bool kOutF32>
 cudaError_t launch(const DecodeArgs& a, int groups, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<kRows, kOutF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<kRows>());
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_q4_kernel<kRows, kOutF32>, a.n_workers / groups * groups, kThreads, smem_bytes<kRows>(), 1, s, a);
+  return launch_dependent(decode_q4_kernel<kRows, kOutF32>, a.n_workers / groups * groups, Shape<kRows>::kThreads, smem_bytes<kRows>(), 1, s, a);
 }
 
 }  // namespace

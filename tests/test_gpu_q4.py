@@ -339,11 +339,11 @@ def tolerances(b, values, spread):
     most 2^-3, whose own four bits leave 2^-8.  So p is off by 2^-8 + 2^-11 of
     itself; that and the score's error count twice (numerator and normaliser),
     each relative to the weighted mean of |v|.
-    Small p: what the kernel holds is p_t 2^E_t over its largest, G, which is 2^7
+    Small p: what the kernel holds is p_t 2^E_t over its largest, G, which is 2^5
     at least; the last term's least unit is 2^-9, so that each is off by up to
-    2^-10, 2^-17 G, and those below 2^-17 count as nothing.  Times a value of 6 at
+    2^-10, 2^-15 G, and those below 2^-17 count as nothing.  Times a value of 6 at
     most: roundings like a random walk of n steps, what is lost n times.  Up to 32
-    query rows: from 2^10 down to a unit of 2^-16, 2^-27 G."""
+    query rows: from 2^7 down to a unit of 2^-16, 2^-24 G."""
     B, Q, H, _ = b.q.shape
     q = np.abs(f64(b.q))
     A, G, n = np.zeros((B, Q, H)), np.zeros((B, Q, H)), np.zeros((B, 1, 1))
@@ -363,9 +363,9 @@ def tolerances(b, values, spread):
                     G[i, j] = (x / x.sum(-1, keepdims=True) * 2.0 ** (b.bytes[slots[:seen], 297].astype(float) - 127)).max(-1)
     lse = 2.0 ** -15 * (A + 1)
     if b.q_len * H > 32:
-        small = 5 * np.sqrt(n) * 2.0 ** -17 + n * 2.0 ** -24
+        small = 5 * np.sqrt(n) * 2.0 ** -15 + n * 2.0 ** -22
     else:
-        small = (5 * np.sqrt(n) + n) * 2.0 ** -27
+        small = (5 * np.sqrt(n) + n) * 2.0 ** -24
     return (2 * (2.0 ** -8 + 2.0 ** -11) + 2 * lse[..., None]) * spread + (6 * small * G)[..., None] + 1e-30, lse
 
 
