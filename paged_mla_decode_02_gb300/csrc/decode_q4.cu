@@ -39,7 +39,7 @@
 //
 // Roles: 8 or 16 warps expand tiles, up to a tile ahead of the products, with the
 // raw rows of the next one on their way into registers; a warp for each 32 tokens
-// and 16 query rows makes P; one issues the MMAs, scores of tile g + 1 before P . V
+// and 8 or 16 query rows makes P; one issues the MMAs, scores of tile g + 1 before P . V
 // of tile g.  Registers are dealt out by role.  Waits are bounded (2 s): a warp that gives up says so, and
 // goes on without waiting, so that the named barriers and commits of the others
 // still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is recorded.
@@ -65,7 +65,6 @@ __device__ int g_q4_stall;
 #endif
 
 constexpr int kT = kTileTc;                   // 128 tokens to a tile
-constexpr int kJ = 16;                        // query rows of a softmax warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -79,14 +78,15 @@ struct Shape {
   static constexpr SmemSwizzle kPSwizzle = kRows == 32 ? kSw128 : kSw64;
   // warps: softmax (a lane quadrant and kJ query rows each), expanding, issue (a whole
   // warpgroup, for the registers)
-  static constexpr int kSoftmaxWarps = kRows / 4;
+  static constexpr int kJ = kRows == 16 ? 8 : 16;
+  static constexpr int kSoftmaxWarps = 4 * kRows / kJ;
   static constexpr int kExpandWarps = kRows == 64 ? 8 : 16;
   static constexpr int kIssueWarp = kSoftmaxWarps + kExpandWarps;
   static constexpr int kThreads = 32 * (kIssueWarp + 4);
   static constexpr int kTokWarp = kT / kExpandWarps;       // rows that a warp expands, of one page
   // registers a thread at launch, then by role
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kRegsSoftmax = kRows == 16 ? 128 : kRows == 32 ? 104 : 88, kRegsExpand = kRows == 16 ? 72 : 64;
+  static constexpr int kRegsSoftmax = kRows == 64 ? 80 : 88, kRegsExpand = kRows == 64 ? 80 : 72;
   static constexpr int kRegsIssue = 24;
   static_assert(32 * (kSoftmaxWarps * kRegsSoftmax + kExpandWarps * kRegsExpand + 4 * kRegsIssue) <= kThreads * kRegs, "registers");
   // p reaches 2^kTop: the reference is set to leave kSlack of that, and moves when it is used up
@@ -105,7 +105,8 @@ struct Shape {
   static constexpr int kOffK = kOffP + (kSide ? 1 : 2) * kPPanel;
   static constexpr int kPanel = kT * 128;                  // 128 tokens x 128 dims
   static constexpr int kOffKPe = kOffK + 2 * 4 * kPanel;
-  static constexpr int kOffExp = kOffKPe + kT * 64;        // [2][128] exponent bytes
+  static constexpr int kPeBufs = kRows == 64 ? 1 : 2;      // of the rope part
+  static constexpr int kOffExp = kOffKPe + kPeBufs * kT * 64;   // [2][128] exponent bytes
   static constexpr int kOffScale = kOffExp + 2 * kT;       // [2][rows] 1 / query scale, by unit parity
   static constexpr int kOffRef = kOffScale + 2 * kRows * 4;   // [rows] reference, less kTop - kSlack
   static constexpr int kOffTable = kOffRef + kRows * 4;    // [4] e4m3 codes of the magnitudes, for shifts 12 ..
@@ -117,11 +118,13 @@ struct Shape {
 enum Bar {
   kKFull0,                   // [2] tile expanded (a signal of every expanding warp)
   kSFull0 = kKFull0 + 2,     // [2] scores made
-  kPReady0 = kSFull0 + 2,    // [4] P of 32 tokens written (a signal for every 16 query rows)
-  kPvDone0 = kPReady0 + 4,   // [4] P . V over 32 tokens made: their rows of K and P may be written again
-  kQReady = kPvDone0 + 4,    // the unit's query in place
-  kFinal,
-  kNumBars
+  kSFree0 = kSFull0 + 2,     // [2] scores read (a signal of every softmax warp)
+  kPReady0 = kSFree0 + 2,    // [4] P of 32 tokens written (a signal for every kJ query rows)
+  kPvDone0 = kPReady0 + 4,   // [2][4] P . V over 32 tokens made: their rows of K and P may be written again
+                             // (by tile parity: the next tile's may be made before an expanding warp looks)
+  kQReady = kPvDone0 + 8,    // the unit's query in place
+  kFinal0,                   // [2] every MMA of an issuing warp made
+  kNumBars = kFinal0 + 2
 };
 template <int kRows>
 constexpr int smem_bytes() {
@@ -146,7 +149,12 @@ __device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
-// A warp's 32 lanes x 16 consecutive columns of tensor memory.
+// A warp's 32 lanes x N consecutive columns of tensor memory.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -160,6 +168,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t& r) {
 }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, uint32_t r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+
+// A warpgroup's registers a thread, from those at launch.  Each direction has its
+// own instruction; one that goes the other way is an illegal instruction.
+template <int kFrom, int kTo>
+__device__ __forceinline__ void set_registers() {
+  static_assert(kTo % 8 == 0 && kTo >= 24 && kTo <= 256, "register count");
+  if constexpr (kTo > kFrom) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTo));
+  else if constexpr (kTo < kFrom) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTo));
 }
 
 // A barrier of `threads` threads that also tells whether any of them says so.
@@ -196,10 +213,22 @@ __device__ __forceinline__ void split_query(float x0, float x1, uint32_t& hi, ui
 __device__ __forceinline__ uint32_t expand4(uint2 table, uint32_t select, uint32_t signs) {
   return __byte_perm(table.x, table.y, select) | (signs & 0x80808080u);
 }
+// w >> 16 and w << 4 by multiplication: what is left of the expansion is bound by
+// the integer pipe, and these run on another.
+__device__ __forceinline__ uint32_t upper_half(uint32_t w) {
+  uint32_t d;
+  asm("mul.hi.u32 %0, %1, 65536;" : "=r"(d) : "r"(w));
+  return d;
+}
+__device__ __forceinline__ uint32_t times16(uint32_t w) {
+  uint32_t d;
+  asm("mul.lo.u32 %0, %1, 16;" : "=r"(d) : "r"(w));
+  return d;
+}
 __device__ __forceinline__ uint4 expand16(uint2 table, uint32_t w0, uint32_t w1) {
   const uint32_t a = w0 & 0x77777777u, b = w1 & 0x77777777u;
-  return make_uint4(expand4(table, a, w0), expand4(table, a >> 16, w0 << 4), expand4(table, b, w1),
-                    expand4(table, b >> 16, w1 << 4));
+  return make_uint4(expand4(table, a, w0), expand4(table, upper_half(a), times16(w0)), expand4(table, b, w1),
+                    expand4(table, upper_half(b), times16(w1)));
 }
 // e4m3 codes of magnitude * 2^(6 - shift): up to a shift of 11 all are normal
 // numbers, whose exponent field starts at bit 3.
@@ -284,7 +313,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using S = Shape<kRows>;
-  constexpr int kSoftmaxWarps = S::kSoftmaxWarps, kExpandWarps = S::kExpandWarps, kIssueWarp = S::kIssueWarp, kTokWarp = S::kTokWarp;
+  constexpr int kJ = S::kJ, kSoftmaxWarps = S::kSoftmaxWarps, kExpandWarps = S::kExpandWarps, kIssueWarp = S::kIssueWarp, kTokWarp = S::kTokWarp;
   extern __shared__ __align__(1024) unsigned char sm[];
   const uint32_t base = smem_u32(sm);
   auto bar = [&](int i) { return base + S::kOffBar + 8 * i; };
@@ -303,7 +332,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i < kSFull0 || i == kQReady ? kExpandWarps : i >= kPReady0 && i < kPvDone0 ? kSoftmaxWarps / 4 : 1);
+      mbar_init(bar(i), i < kSFull0 || i == kQReady           ? kExpandWarps
+                        : i == kSFree0 || i == kSFree0 + 1    ? kSoftmaxWarps
+                        : i >= kPReady0 && i < kPvDone0       ? kSoftmaxWarps / 4
+                                                              : 1);
     fence_barrier_init();
   }
   if (threadIdx.x < 4) {
@@ -327,9 +359,9 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   auto wait = [&](int i, int phase) { ok &= mbar_spin<false>(bar(i), phase & 1, abort_flag); };
 
   if (warp >= kIssueWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsIssue));
-    if (warp == kIssueWarp) {
-      // ================= the issuing warp =================
+    set_registers<S::kRegs, S::kRegsIssue>();
+    if (warp <= kIssueWarp + 1) {
+      // ================= the issuing warps =================
       const uint64_t k_desc = smem_desc(base + S::kOffK, 16, 1024, kSw128);
       const uint64_t kpe_desc = smem_desc(base + S::kOffKPe, 16, 512, kSw64);
       const uint64_t q_desc = smem_desc(base + S::kOffQ, 16, 1024, kSw128);
@@ -337,6 +369,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       const uint64_t p_desc = smem_desc(base + S::kOffP, 16, 8 * S::kPRow, S::kPSwizzle);
       constexpr uint32_t id_s = idesc_f8(S::kNS, 0, false), id_hi = idesc_f8(S::kPN, 1, true), id_lo = idesc_f8(S::kPN, 0, true);
       auto scores = [&](int g) {
+        if (g > 1) wait(kSFree0 + (g & 1), (g - 2) >> 1);
         wait(kKFull0 + (g & 1), g >> 1);
         tc_fence_after();
         const uint32_t d = tmem + S::kColS + (g & 1) * S::kNS;
@@ -348,7 +381,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           for (int kk = 0; kk < 4; ++kk) mma_f8_elect(d, ka + 2 * kk, qb + 2 * kk, id_s, (p | kk) != 0);
         }
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) mma_f8_elect(d, kpe_desc + 2 * kk, qpe_desc + 2 * kk, id_s, 1);
+        for (int kk = 0; kk < 2; ++kk)
+          mma_f8_elect(d, kpe_desc + static_cast<uint64_t>(((S::kPeBufs == 2 ? (g & 1) * kT * 64 : 0) >> 4) + 2 * kk), qpe_desc + 2 * kk, id_s, 1);
         mma_commit_elect(bar(kSFull0 + (g & 1)));
       };
       auto values = [&](int g, bool first) {
@@ -367,33 +401,41 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
               mma_f8_elect(tmem + p * S::kOBlock, va, pb + static_cast<uint64_t>(S::kPPanel >> 4), id_lo, 1);
             }
           }
-          mma_commit_elect(bar(kPvDone0 + j));
+          mma_commit_elect(bar(kPvDone0 + 4 * (g & 1) + j));
         }
       };
-      // S of tile g + 1 before P . V of tile g, but where g + 1 begins a unit, whose
-      // query comes a while after g's scores
+      // The scores of a tile need its rows, P . V of the tile before its P: whichever
+      // comes first goes first, so each has a warp of its own (with one warp for both,
+      // in a fixed order, the rows of a tile waited for those of the one before:
+      // 2.4 us a tile of 16 query rows, against 1.5).
+      const int role = warp - kIssueWarp;
       int g = 0;
       for (int ui = u0; ui < u1; ++ui) {
         const int n = (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
-        wait(kQReady, ui - u0);
-        scores(g);
+        if (role == 0) wait(kQReady, ui - u0);
         for (int i = 0; i < n; ++i, ++g) {
-          if (i + 1 < n) scores(g + 1);
-          values(g, i == 0);
+          if (role == 0) scores(g);
+          else values(g, i == 0);
         }
       }
-      mma_commit_elect(bar(kFinal));
+      mma_commit_elect(bar(kFinal0 + role));
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
-      mbar_wait_drain(bar(kFinal), 0);   // every MMA issued is done before tensor memory is freed
+      mbar_wait_drain(bar(kFinal0 + role), 0);   // every MMA issued is done before tensor memory is freed
       __syncwarp();
     }
   } else if (warp >= kSoftmaxWarps) {
     // ================= expanding warps =================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsExpand));
+    set_registers<S::kRegs, S::kRegsExpand>();
     if (u0 < u1) {
       const int ew = warp - kSoftmaxWarps;
       const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
       const uint2* table = reinterpret_cast<const uint2*>(sm + S::kOffTable);
+      // This warp's rows of a tile: the first of them and how many.  Rows are read into
+      // registers a tile ahead, their page id a tile before that.
+      struct Rows {
+        const uint8_t* src;
+        int n;
+      };
       Cursor ld;
       ld.ui = u0;
       ld.read(a.units);
@@ -403,6 +445,19 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         const int t = ld.tok0() + kTokWarp * ew;
         if (more && t < ld.tok_end) page = a.kv_indices[ld.page_base + (t >> page_shift)];
       };
+      auto next_rows = [&]() {
+        const int t = ld.tok0() + kTokWarp * ew;
+        Rows r;
+        r.n = more ? max(0, min(kTokWarp, ld.tok_end - t)) : 0;
+        if (r.n > 0 && (page < 0 || page >= a.num_pages)) {   // its rows count as zeros
+          if (lane == 0) report_error(a.err, kErrBounds);
+          r.n = 0;
+        }
+        r.src = cache + ((static_cast<size_t>(r.n > 0 ? page : 0) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
+        if (more) more = ld.next(a.units, u1);
+        next_page();
+        return r;
+      };
       // A lane takes whole groups (16 bytes of codes): of ckv, group 4 (lane / 8) + lane % 4
       // of row 2 i + lane / 4 % 2 for each i, so that eight lanes write to eight groups of
       // banks; of kpe, group lane % 2 of row lane / 2.  Shifts of ckv: four of row 8 i +
@@ -410,56 +465,66 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       const int panel = lane >> 3, odd = (lane >> 2) & 1, pair = lane & 3;
       uint4 raw[kTokWarp / 2], raw_pe;
       uint32_t shifts[kTokWarp / 8], meta_pe;
-      auto load_rows = [&]() {
-        const int t = ld.tok0() + kTokWarp * ew;
-        int n = more ? min(kTokWarp, ld.tok_end - t) : 0;
-        if (n > 0 && (page < 0 || page >= a.num_pages)) {   // its rows count as zeros
-          if (lane == 0) report_error(a.err, kErrBounds);
-          n = 0;
-        }
-        const uint8_t* src = cache + ((static_cast<size_t>(n > 0 ? page : 0) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
-#pragma unroll
-        for (int i = 0; i < kTokWarp / 2; ++i) {
-          raw[i] = make_uint4(0, 0, 0, 0);
-          if (2 * i + odd < n) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (2 * i + odd) * kQ4Row) + 4 * panel + pair);
-        }
+      auto load_ckv = [&](const Rows& r, int i) {   // rows 2 i and 2 i + 1
+        return __ldg(reinterpret_cast<const uint4*>(r.src + (2 * i + odd) * kQ4Row) + 4 * panel + pair);
+      };
+      auto load_rest = [&](const Rows& r) {
 #pragma unroll
         for (int i = 0; i < kTokWarp / 8; ++i) {
           shifts[i] = 0;
-          if (8 * i + (lane >> 2) < n) shifts[i] = __ldg(reinterpret_cast<const uint16_t*>(src + (8 * i + (lane >> 2)) * kQ4Row + kQ4Meta) + pair);
+          if (8 * i + (lane >> 2) < r.n) shifts[i] = __ldg(reinterpret_cast<const uint16_t*>(r.src + (8 * i + (lane >> 2)) * kQ4Row + kQ4Meta) + pair);
         }
         raw_pe = make_uint4(0, 0, 0, 0);
         meta_pe = 127 << 8;
-        if ((lane >> 1) < n) {
-          const uint8_t* row = src + (lane >> 1) * kQ4Row;
+        if ((lane >> 1) < r.n) {
+          const uint8_t* row = r.src + (lane >> 1) * kQ4Row;
           raw_pe = __ldg(reinterpret_cast<const uint4*>(row + kDCkv / 2) + (lane & 1));
           meta_pe = __ldg(reinterpret_cast<const uint16_t*>(row + kQ4Meta + 8));
         }
-        if (more) more = ld.next(a.units, u1);
-        next_page();
       };
-      auto expand = [&](int g) {
-        // shifts past 11 lead to subnormal numbers, by a table
-        uint32_t large = (meta_pe & (meta_pe << 1)) & 0x88u;
+      auto load_part = [&](const Rows& r) {   // not all of a warp's rows: the others hold zeros
 #pragma unroll
-        for (int i = 0; i < kTokWarp / 8; ++i) large |= shifts[i] & (shifts[i] << 1) & 0x8888u;
+        for (int i = 0; i < kTokWarp / 2; ++i) {
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (2 * i + odd < r.n) raw[i] = load_ckv(r, i);
+        }
+      };
+      // Tile g from registers, which take the rows `next` meanwhile.
+      auto expand = [&](int g, const Rows& next) {
+        uint32_t shift[kTokWarp / 8];
+#pragma unroll
+        for (int i = 0; i < kTokWarp / 8; ++i) shift[i] = shifts[i];
+        const uint4 codes_pe = raw_pe;
+        const uint32_t meta = meta_pe;
+        load_rest(next);
+        // shifts past 11 lead to subnormal numbers, by a table
+        uint32_t large = (meta & (meta << 1)) & 0x88u;
+#pragma unroll
+        for (int i = 0; i < kTokWarp / 8; ++i) large |= shift[i] & (shift[i] << 1) & 0x8888u;
+        const bool whole = next.n == kTokWarp;
         auto fill = [&](auto table_of) {
+          // chunk 2 pair of row 2 i + odd is at 2 pair ^ odd ^ (2 i & 7)
           unsigned char* dst = sm + S::kOffK + (g & 1) * 4 * S::kPanel + panel * S::kPanel + (kTokWarp * ew + odd) * 128;
+          uint32_t mine[kTokWarp / 2];   // shifts of groups 4 panel ..
+#pragma unroll
+          for (int i = 0; i < kTokWarp / 2; ++i) mine[i] = __shfl_sync(~0u, shift[i / 4], 8 * (i % 4) + 4 * odd + panel);
 #pragma unroll
           for (int i = 0; i < kTokWarp / 2; ++i) {
-            const uint32_t mine = __shfl_sync(~0u, shifts[i / 4], 8 * (i % 4) + 4 * odd + panel);   // of groups 4 panel ..
-            const uint2 t = table_of((mine >> (4 * pair)) & 15);
-            const int at = 256 * i + ((2 * pair ^ ((2 * i + odd) & 7)) << 4);
-            *reinterpret_cast<uint4*>(dst + at) = expand16(t, raw[i].x, raw[i].y);
-            *reinterpret_cast<uint4*>(dst + (at ^ 16)) = expand16(t, raw[i].z, raw[i].w);
+            const uint2 t = table_of((mine[i] >> (4 * pair)) & 15);
+            unsigned char* at = dst + (((2 * pair) ^ odd ^ (2 * i & 6)) << 4);
+            unsigned char* at2 = dst + (((2 * pair + 1) ^ odd ^ (2 * i & 6)) << 4);
+            *reinterpret_cast<uint4*>(at + 256 * i) = expand16(t, raw[i].x, raw[i].y);
+            *reinterpret_cast<uint4*>(at2 + 256 * i) = expand16(t, raw[i].z, raw[i].w);
+            if (whole) raw[i] = load_ckv(next, i);
           }
+          if (S::kPeBufs == 1 && g > 0) wait(kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read it
           if (kTokWarp == 16 || lane < 16) {
             const int row = kTokWarp * ew + (lane >> 1);
-            const uint2 t = table_of((meta_pe >> (4 * (lane & 1))) & 15);
-            const int at = row * 64 + (((2 * (lane & 1)) ^ ((row >> 1) & 3)) << 4);
-            *reinterpret_cast<uint4*>(sm + S::kOffKPe + at) = expand16(t, raw_pe.x, raw_pe.y);
-            *reinterpret_cast<uint4*>(sm + S::kOffKPe + (at ^ 16)) = expand16(t, raw_pe.z, raw_pe.w);
-            if ((lane & 1) == 0) sm[S::kOffExp + (g & 1) * kT + row] = static_cast<unsigned char>(meta_pe >> 8);
+            const uint2 t = table_of((meta >> (4 * (lane & 1))) & 15);
+            const int at = (S::kPeBufs == 2 ? (g & 1) * kT * 64 : 0) + row * 64 + (((2 * (lane & 1)) ^ ((row >> 1) & 3)) << 4);
+            *reinterpret_cast<uint4*>(sm + S::kOffKPe + at) = expand16(t, codes_pe.x, codes_pe.y);
+            *reinterpret_cast<uint4*>(sm + S::kOffKPe + (at ^ 16)) = expand16(t, codes_pe.z, codes_pe.w);
+            if ((lane & 1) == 0) sm[S::kOffExp + (g & 1) * kT + row] = static_cast<unsigned char>(meta >> 8);
           }
         };
         if (__any_sync(~0u, large)) fill([&](uint32_t k) { return k >= 12 ? table[k - 12] : normal_table(k); });
@@ -470,6 +535,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (blockIdx.x == 0 && ew == 0 && g + 1 == g_q4_stall) return;
 #endif
         if (lane == 0) mbar_arrive(bar(kKFull0 + (g & 1)));
+        if (!whole) load_part(next);
       };
       // ---- the query of a unit, kRows / 8 rows a warp ----
       auto put_query = [&](int ui) {
@@ -512,25 +578,30 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (lane == 0) mbar_arrive(bar(kQReady));
       };
       next_page();
-      load_rows();
+      const Rows rows = next_rows();
+      Rows ahead = next_rows();
+      load_part(rows);
+      load_rest(rows);
       put_query(u0);
       int g = 0;
       for (int ui = u0; ui < u1; ++ui) {
         const int n = (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
         for (int i = 0; i < n; ++i, ++g) {
-          // the buffer was read by P . V of g - 2, the rope part and the query by the scores of g - 1
-          if (g > 1) wait(kPvDone0 + ew * kTokWarp / 32, g - 2);
-          if (g > 0) wait(kSFull0 + ((g - 1) & 1), (g - 1) >> 1);
-          expand(g);
-          load_rows();
-          if (i == 0 && ui > u0) put_query(ui);
+          // the buffer was read by P . V of g - 2
+          if (g > 1) wait(kPvDone0 + 4 * (g & 1) + ew * kTokWarp / 32, (g - 2) >> 1);
+          expand(g, ahead);
+          ahead = next_rows();
+          if (i == 0 && ui > u0) {
+            wait(kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read the last one
+            put_query(ui);
+          }
         }
       }
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
     }
   } else {
     // ================= softmax and epilogue =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoftmax));
+    set_registers<S::kRegs, S::kRegsSoftmax>();
     const int q = warp & 3, cg = warp >> 2;             // tokens 32 q .. of a tile (lane quadrant), query rows kJ cg ..
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const int tok = 32 * q + lane;
@@ -570,6 +641,9 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             z[j] = y.x;
             z[j + 1] = y.y;
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kSFree0 + (g & 1)));
         }
         if (t0 + kT > u.tok_end - (prm.q_len > 1 ? prm.q_len - 1 : 0)) {
           // the query rows that see token t: of query tokens packed into rows, row h sees
@@ -587,7 +661,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         // ---- the reference moves: the four warps of these query rows together ----
         if (bar_any(1 + cg, 128, first || top > S::kTop)) {
           const float most = warp_reduce<true>(z);
-          if ((lane & 1) == 0) red[q * kJ + (lane >> 1)] = most;
+          if ((lane & (32 / kJ - 1)) == 0) red[q * kJ + lane * kJ / 32] = most;
           named_bar_sync(1 + cg, 128);
           uint32_t moved = 0;
           float mine = 1.f;   // lane j: the factor of row j
@@ -608,7 +682,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             if (q == 0 && lane == j) refs[j] = (first ? 0.f : refs[j]) + up;
           }
           if (moved) {   // their columns of O, a row at a time: few move at once
-            wait(kPvDone0 + 3, g - 1);
+            wait(kPvDone0 + 4 * ((g - 1) & 1) + 3, (g - 1) >> 1);
             tc_fence_after();
             do {
               const int j = __ffs(moved) - 1;
@@ -659,14 +733,16 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #pragma unroll
           for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
         }
-        if (g > 0) wait(kPvDone0 + q, g - 1);   // P . V of the tile before has read these rows of P
+        if (g > 0) wait(kPvDone0 + 4 * ((g - 1) & 1) + q, (g - 1) >> 1);   // P . V of the tile before has read these rows of P
         unsigned char* prow = sm + S::kOffP + tok * S::kPRow;
 #pragma unroll
         for (int i = 0; i < kTerms; ++i) {
-          const int at = kRows == 64   ? i * S::kPPanel + ((cg ^ ((tok >> 1) & 3)) << 4)
-                         : kRows == 32 ? ((2 * i + cg) ^ (tok & 7)) << 4
-                                       : (i ^ ((tok >> 1) & 3)) << 4;
-          *reinterpret_cast<uint4*>(prow + at) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+          if constexpr (kRows == 64)
+            *reinterpret_cast<uint4*>(prow + i * S::kPPanel + ((cg ^ ((tok >> 1) & 3)) << 4)) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+          else if constexpr (kRows == 32)
+            *reinterpret_cast<uint4*>(prow + (((2 * i + cg) ^ (tok & 7)) << 4)) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+          else
+            *reinterpret_cast<uint2*>(prow + ((i ^ ((tok >> 1) & 3)) << 4) + 8 * cg) = make_uint2(c[i][0], c[i][1]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -676,7 +752,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       // ---- epilogue: the sums over the unit's tokens of all lanes and quadrants ----
       const bool split = u.out_slot >= 0;
       const float sx = warp_reduce<false>(lx);
-      if ((lane & 1) == 0) red[q * kJ + (lane >> 1)] = sx;
+      if ((lane & (32 / kJ - 1)) == 0) red[q * kJ + lane * kJ / 32] = sx;
       named_bar_sync(1 + cg, 128);
       if (q == 0 && lane < kJ && row0 + kJ * cg + lane < H) {
         const int h = row0 + kJ * cg + lane;
@@ -689,7 +765,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #pragma unroll
       for (int j = 0; j < kJ; ++j) lx[j] -= ld[j];   // of what P stands for
       const float sr = warp_reduce<false>(lx);
-      if ((lane & 1) == 0) red[q * kJ + (lane >> 1)] = sr;
+      if ((lane & (32 / kJ - 1)) == 0) red[q * kJ + lane * kJ / 32] = sr;
       named_bar_sync(1 + cg, 128);
       float inv[kJ];
 #pragma unroll
@@ -697,7 +773,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         const float s = (red[j] + red[kJ + j]) + (red[2 * kJ + j] + red[3 * kJ + j]);
         inv[j] = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
       }
-      wait(kPvDone0 + 3, g - 1);
+      wait(kPvDone0 + 4 * ((g - 1) & 1) + 3, (g - 1) >> 1);
       tc_fence_after();
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
