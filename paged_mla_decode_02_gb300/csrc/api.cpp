@@ -336,6 +336,8 @@ mla_status_t plan_requests(mla_plan_t plan, const int32_t* page_base, const int3
   if (plan->kernel == MLA_KERNEL_Q4) n_workers = std::max(1, n_workers / decode_q4_groups(num_heads));
   if (plan->kernel == MLA_KERNEL_PAIR)
     partition_batch_pair(page_base, len, n_req, n_workers, num_heads, &part);
+  else if (plan->kernel == MLA_KERNEL_Q4)
+    partition_batch_q4(page_base, len, n_req, n_workers, num_heads, &part);
   else
     partition_batch(page_base, len, n_req, n_workers, plan->tile_tokens, &part);
   if (static_cast<int>(part.units.size()) > plan->units_cap || part.n_slots > plan->slots_cap ||
@@ -490,7 +492,7 @@ DecodeArgs decode_args(mla_plan_t plan, const void* q_nope, const void* q_pe, co
 }
 
 // Combines the split requests of a run and fills the empty ones.
-mla_status_t merge_shares(mla_plan_t plan, const DecodeArgs& a, bool out_f32, cudaStream_t s) {
+mla_status_t merge_shares(mla_plan_t plan, const DecodeArgs& a, bool out_f32, cudaStream_t s, bool q4 = false) {
   MergeArgs m{};
   m.merge = a.merge;
   m.params = a.params;
@@ -500,7 +502,7 @@ mla_status_t merge_shares(mla_plan_t plan, const DecodeArgs& a, bool out_f32, cu
   m.lse = a.lse;
   m.num_heads = plan->params.num_heads;
   m.merge_cap = plan->merge_cap;
-  const cudaError_t e = launch_merge(m, out_f32, s);
+  const cudaError_t e = q4 ? launch_merge_shares(m, out_f32, s) : launch_merge(m, out_f32, s);
   return e == cudaSuccess ? MLA_OK : cuda_fail(plan, e, "merge kernel launch");
 }
 
@@ -598,7 +600,7 @@ mla_status_t mla_decode_run_q4(mla_plan_t plan, const void* q_nope, const void* 
   if ((e = launch_decode_q4(a, out_f32, s)) != cudaSuccess) return cuda_fail(plan, e, "decode kernel launch");
   if (plan->prof_stop && (e = cudaEventRecord(plan->prof_stop, s)) != cudaSuccess)
     return cuda_fail(plan, e, "cudaEventRecord");
-  return merge_shares(plan, a, out_f32, s);
+  return merge_shares(plan, a, out_f32, s, true);
 }
 
 mla_status_t mla_decode_run_host(mla_plan_t plan, const void* q_nope_host, const void* q_pe_host,

@@ -114,5 +114,8 @@ cudaError_t launch_decode_q4(const DecodeArgs& a, bool out_f32, cudaStream_t s);
 // LSE merge of split partials (and zero-fill of empty requests); the mma.sync
 // and CTA-pair paths -- the one-CTA tcgen05 kernel merges in its own epilogue.
 cudaError_t launch_merge(const MergeArgs& a, bool out_f32, cudaStream_t s);
+// The same after the 4-bit decode, whose plans cut a few requests of any number
+// of query rows into many shares.
+cudaError_t launch_merge_shares(const MergeArgs& a, bool out_f32, cudaStream_t s);
 
 }  // namespace mla

@@ -235,7 +235,10 @@ void partition_batch(const int32_t* kv_indptr, const int32_t* kv_len, int batch,
 }
 
 long long partition_makespan(const Partition& p, int tile_tokens) {
-  const PlanCosts c = plan_costs(tile_tokens);
+  return partition_makespan(p, tile_tokens, plan_costs(tile_tokens));
+}
+
+long long partition_makespan(const Partition& p, int tile_tokens, const PlanCosts& c) {
   long long worst = 0;
   for (size_t w = 0; w + 1 < p.worker_ptr.size(); ++w) {
     long long used = 0;
@@ -268,6 +271,36 @@ void partition_batch_pair(const int32_t* kv_indptr, const int32_t* kv_len, int b
   few.split = kFewSplitsCost;
   partition_batch(kv_indptr, kv_len, batch, n_workers, kTilePair, few, &whole);
   if (pair_step_estimate_us(whole, rows) < pair_step_estimate_us(*out, rows)) *out = std::move(whole);
+}
+
+namespace {
+double q4_tile_us(int rows) { return rows <= 16 ? 1.7 : rows <= 32 ? 2.0 : 2.8; }
+}  // namespace
+
+PlanCosts q4_costs(int rows) {
+  const int unit = static_cast<int>(4 * 5.0 / q4_tile_us(rows));
+  return PlanCosts{4, unit, 2, 1};
+}
+
+double q4_step_estimate_us(const Partition& p, int rows) {
+  constexpr double kMergeFixedUs = 3.0;      // a merge pass that combines something
+  constexpr double kMergeBytesPerUs = 3e6;   // its shares, written and read
+  double us = partition_makespan(p, kTileTc, q4_costs(rows)) * (q4_tile_us(rows) / 4.0);
+  if (p.n_slots > 0)
+    us += kMergeFixedUs + static_cast<double>(p.n_slots) * rows * kDCkv * sizeof(float) / kMergeBytesPerUs;
+  return us;
+}
+
+void partition_batch_q4(const int32_t* kv_indptr, const int32_t* kv_len, int batch, int n_workers,
+                        int rows, Partition* out) {
+  const PlanCosts even = q4_costs(rows);
+  partition_batch(kv_indptr, kv_len, batch, n_workers, kTileTc, even, out);
+  if (out->n_slots == 0) return;
+  Partition whole;
+  PlanCosts few = even;
+  few.split = kFewSplitsCost;
+  partition_batch(kv_indptr, kv_len, batch, n_workers, kTileTc, few, &whole);
+  if (q4_step_estimate_us(whole, rows) < q4_step_estimate_us(*out, rows)) *out = std::move(whole);
 }
 
 }  // namespace mla

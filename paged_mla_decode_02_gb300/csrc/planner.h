@@ -60,8 +60,9 @@ void partition_batch(const int32_t* kv_indptr, const int32_t* kv_len, int batch,
 void partition_batch(const int32_t* kv_indptr, const int32_t* kv_len, int batch,
                      int n_workers, int tile_tokens, const PlanCosts& c, Partition* out);
 
-// The largest worker cost of a partition under the default costs.
+// The largest worker cost of a partition under the default costs, or given ones.
 long long partition_makespan(const Partition& p, int tile_tokens);
+long long partition_makespan(const Partition& p, int tile_tokens, const PlanCosts& c);
 
 // The CTA-pair kernel's partition (256-token tiles, `rows` query rows per
 // request).  A split request costs its workers the stores of its shares (the
@@ -78,6 +79,18 @@ constexpr int kFewSplitsCost = 12;
 double pair_step_estimate_us(const Partition& p, int rows);
 void partition_batch_pair(const int32_t* kv_indptr, const int32_t* kv_len, int batch, int n_workers,
                           int rows, Partition* out);
+
+// The 4-bit kernel's partition (128-token tiles, `rows` query rows per request),
+// chosen in the same way between splits where they even the workers out and
+// splits where a request must be cut.  A tile takes 1.7 us with up to 16 query
+// rows, 2.0 with 32 and 2.8 with more (of which a CTA takes 64), a unit 5 us
+// more (its query, the first rows, the sums and the output), so a short request
+// is worth cutting down to single tiles (4 requests of up to 2000 tokens, 16
+// heads: 28 us in pieces of four tiles or more, 19 with single ones).
+PlanCosts q4_costs(int rows);
+double q4_step_estimate_us(const Partition& p, int rows);
+void partition_batch_q4(const int32_t* kv_indptr, const int32_t* kv_len, int batch, int n_workers,
+                        int rows, Partition* out);
 
 // Upper bounds of the partition sizes, used to size plan buffers at creation:
 // a request is cut only where a worker ends, so each worker adds at most one

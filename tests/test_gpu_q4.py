@@ -787,3 +787,24 @@ def test_a_serving_step_together():
             s = f64(torch.cat([q_nope, q_pe], -1)[r]) @ k.T / math.sqrt(192.0)
             np.testing.assert_allclose(f64(lse[r]), np.log(np.exp(s - s.max(1, keepdims=True)).sum(1)) + s.max(1), atol=2.0 ** -9)
     dec.close()
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_decode_nan_in_a_split_request(H):
+    """A NaN row in one share of a request: out and lse of the whole request."""
+    b = Batch(rng_of(55, H), [9000, 300], H, 64)
+    slot = int(b.ids[b.indptr[0] + 100]) * 64 + 7
+    b.bytes[slot, 297] = 255
+    b.cache = torch.from_numpy(b.bytes.reshape(b.pages, 64, 304)).cuda()
+    dec = b.decoder()
+    assert dec.info()["num_partial_slots"] > 1
+    out, lse = dec.run_q4(b.q_nope, b.q_pe, b.cache, out_dtype=torch.float32)
+    dec.check_status()
+    assert out[0].isnan().all() and lse[0].isnan().all()
+    assert out[1].isfinite().all() and lse[1].isfinite().all()
+    dec.close()
+
+
+@pytest.mark.parametrize("H, lens", [(1, [20000, 0, 150, 9000]), (20, [30000]), (64, [9000] * 4), (100, [5000, 5000]), (128, [12000, 1])])
+def test_decode_many_shares(H, lens):
+    run_check(Batch(rng_of(56, H), lens, H, 64), torch.bfloat16)
