@@ -68,6 +68,14 @@ constexpr int kT = kTileTc;                   // 128 tokens to a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int kRowsAhead = 4;                 // tiles whose rows are known ahead
+
+// An expanding warp's rows of a tile: the first of them and how many.
+struct Rows {
+  const uint8_t* src;
+  int64_t n;
+};
+
 template <int kRows>
 struct Shape {
   static constexpr int kNS = 2 * kRows;                    // columns of S^T
@@ -111,7 +119,9 @@ struct Shape {
   static constexpr int kOffRef = kOffScale + 2 * kRows * 4;   // [rows] reference, less kTop - kSlack
   static constexpr int kOffTable = kOffRef + kRows * 4;    // [4] e4m3 codes of the magnitudes, for shifts 12 ..
   static constexpr int kOffRed = kOffTable + 4 * 8;        // [softmax warps][kJ] floats
-  static constexpr int kOffBar = kOffRed + kSoftmaxWarps * kJ * 4;
+  static constexpr int kOffRows = kOffRed + kSoftmaxWarps * kJ * 4;   // [kRowsAhead][expanding warps] Rows
+  static constexpr int kOffBar = kOffRows + kRowsAhead * kExpandWarps * 16;
+  static_assert(kOffTable % 16 == 0 && kOffRows % 16 == 0, "aligned parts");
   static_assert(kOffP % 1024 == 0 && kOffK % 1024 == 0 && kOffKPe % 1024 == 0, "swizzle atoms");
 };
 
@@ -122,7 +132,9 @@ enum Bar {
   kPReady0 = kSFree0 + 2,    // [4] P of 32 tokens written (a signal for every kJ query rows)
   kPvDone0 = kPReady0 + 4,   // [2][4] P . V over 32 tokens made: their rows of K and P may be written again
                              // (by tile parity: the next tile's may be made before an expanding warp looks)
-  kQReady = kPvDone0 + 8,    // the unit's query in place
+  kRowsFull0 = kPvDone0 + 8, // [4] where the expanding warps find a tile's rows
+  kRowsFree0 = kRowsFull0 + kRowsAhead,   // [4] that place read (a signal of every expanding warp)
+  kQReady = kRowsFree0 + kRowsAhead,    // the unit's query in place
   kFinal0,                   // [2] every MMA of an issuing warp made
   kNumBars = kFinal0 + 2
 };
@@ -332,7 +344,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i < kSFull0 || i == kQReady           ? kExpandWarps
+      mbar_init(bar(i), i < kSFull0 || (i >= kRowsFree0 && i <= kQReady) ? kExpandWarps
                         : i == kSFree0 || i == kSFree0 + 1    ? kSoftmaxWarps
                         : i >= kPReady0 && i < kPvDone0       ? kSoftmaxWarps / 4
                                                               : 1);
@@ -360,7 +372,37 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 
   if (warp >= kIssueWarp) {
     set_registers<S::kRegs, S::kRegsIssue>();
-    if (warp <= kIssueWarp + 1) {
+    if (warp == kIssueWarp + 2 && u0 < u1) {
+      // ================= the warp that finds the rows =================
+      // Lane e: where expanding warp e has its rows of each tile, kRowsAhead tiles ahead,
+      // and the request for them into L2.  After the last tile, one without rows.
+      const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
+      Cursor at;
+      at.ui = u0;
+      at.read(a.units);
+      bool more = true;
+      for (int g = 0;; ++g) {
+        const int t = at.tok0() + kTokWarp * lane;
+        Rows r = {cache, 0};
+        if (more && lane < kExpandWarps && t < at.tok_end) {
+          const int page = a.kv_indices[at.page_base + (t >> page_shift)];
+          if (page < 0 || page >= a.num_pages) {   // its rows count as zeros
+            report_error(a.err, kErrBounds);
+          } else {
+            r.n = min(kTokWarp, at.tok_end - t);
+            r.src += ((static_cast<size_t>(page) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(r.src), "r"(static_cast<int>(r.n) * kQ4Row) : "memory");
+          }
+        }
+        if (g >= kRowsAhead) wait(kRowsFree0 + g % kRowsAhead, (g - kRowsAhead) / kRowsAhead);
+        if (lane < kExpandWarps) reinterpret_cast<Rows*>(sm + S::kOffRows)[g % kRowsAhead * kExpandWarps + lane] = r;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kRowsFull0 + g % kRowsAhead));
+        if (!more) break;
+        more = at.next(a.units, u1);
+      }
+      if (!ok && lane == 0) report_error(a.err, kErrTimeout);
+    } else if (warp <= kIssueWarp + 1) {
       // ================= the issuing warps =================
       const uint64_t k_desc = smem_desc(base + S::kOffK, 16, 1024, kSw128);
       const uint64_t kpe_desc = smem_desc(base + S::kOffKPe, 16, 512, kSw64);
@@ -428,34 +470,12 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     set_registers<S::kRegs, S::kRegsExpand>();
     if (u0 < u1) {
       const int ew = warp - kSoftmaxWarps;
-      const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
       const uint2* table = reinterpret_cast<const uint2*>(sm + S::kOffTable);
-      // This warp's rows of a tile: the first of them and how many.  Rows are read into
-      // registers a tile ahead, their page id a tile before that.
-      struct Rows {
-        const uint8_t* src;
-        int n;
-      };
-      Cursor ld;
-      ld.ui = u0;
-      ld.read(a.units);
-      bool more = true;          // ld stands on a tile
-      int page = 0;              // of this warp's rows of that tile
-      auto next_page = [&]() {
-        const int t = ld.tok0() + kTokWarp * ew;
-        if (more && t < ld.tok_end) page = a.kv_indices[ld.page_base + (t >> page_shift)];
-      };
-      auto next_rows = [&]() {
-        const int t = ld.tok0() + kTokWarp * ew;
-        Rows r;
-        r.n = more ? max(0, min(kTokWarp, ld.tok_end - t)) : 0;
-        if (r.n > 0 && (page < 0 || page >= a.num_pages)) {   // its rows count as zeros
-          if (lane == 0) report_error(a.err, kErrBounds);
-          r.n = 0;
-        }
-        r.src = cache + ((static_cast<size_t>(r.n > 0 ? page : 0) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
-        if (more) more = ld.next(a.units, u1);
-        next_page();
+      auto rows_of = [&](int g) {
+        wait(kRowsFull0 + g % kRowsAhead, g / kRowsAhead);
+        const Rows r = reinterpret_cast<const Rows*>(sm + S::kOffRows)[g % kRowsAhead * kExpandWarps + ew];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kRowsFree0 + g % kRowsAhead));
         return r;
       };
       // A lane takes whole groups (16 bytes of codes): of ckv, group 4 (lane / 8) + lane % 4
@@ -577,11 +597,11 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kQReady));
       };
-      next_page();
-      const Rows rows = next_rows();
-      Rows ahead = next_rows();
-      load_part(rows);
-      load_rest(rows);
+      {
+        const Rows rows = rows_of(0);
+        load_part(rows);
+        load_rest(rows);
+      }
       put_query(u0);
       int g = 0;
       for (int ui = u0; ui < u1; ++ui) {
@@ -589,8 +609,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         for (int i = 0; i < n; ++i, ++g) {
           // the buffer was read by P . V of g - 2
           if (g > 1) wait(kPvDone0 + 4 * (g & 1) + ew * kTokWarp / 32, (g - 2) >> 1);
-          expand(g, ahead);
-          ahead = next_rows();
+          expand(g, rows_of(g + 1));
           if (i == 0 && ui > u0) {
             wait(kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read the last one
             put_query(ui);
