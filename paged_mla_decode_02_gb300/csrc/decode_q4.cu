@@ -68,12 +68,15 @@ constexpr int kT = kTileTc;                   // 128 tokens to a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int kRowsAhead = 4;                 // tiles whose rows are known ahead
-
-// An expanding warp's rows of a tile: the first of them and how many.
+// An expanding warp's rows of a tile in one word: the address of the first and,
+// in the bits that no address has, how many.
+__device__ __forceinline__ uint64_t pack_rows(const uint8_t* src, int n) {
+  return reinterpret_cast<uint64_t>(src) | static_cast<uint64_t>(n) << 59;
+}
 struct Rows {
   const uint8_t* src;
-  int64_t n;
+  int n;
+  __device__ __forceinline__ explicit Rows(uint64_t w) : src(reinterpret_cast<const uint8_t*>(w & ((1ull << 59) - 1))), n(static_cast<int>(w >> 59)) {}
 };
 
 template <int kRows>
@@ -105,6 +108,22 @@ struct Shape {
   static constexpr int kOBlock = kRows == 16 ? 64 : kPN;   // of 128 dims
   static constexpr int kColS = 4 * kOBlock;
   static_assert(kColS + 2 * kNS <= 512, "tensor memory");
+  static constexpr int kBufs = kRows == 16 ? 3 : 2;        // expanded tiles
+  static constexpr int kPeBufs = kRows == 32 ? 2 : 1;      // of the rope part
+  static constexpr int kRowsAhead = kRows == 16 ? 2 : 4;   // tiles whose rows are known ahead
+  // barriers
+  static constexpr int kKFull0 = 0;                        // [kBufs] tile expanded (a signal of every expanding warp)
+  static constexpr int kSFull0 = kKFull0 + kBufs;          // [2] scores made
+  static constexpr int kSFree0 = kSFull0 + 2;              // [2] scores read (a signal of every softmax warp)
+  static constexpr int kPReady0 = kSFree0 + 2;             // [4] P of 32 tokens written (a signal for every kJ query rows)
+  // [kBufs][4] P . V over 32 tokens made: their rows of K and P may be written again (by
+  // buffer: the next tile's may be made before an expanding warp looks)
+  static constexpr int kPvDone0 = kPReady0 + 4;
+  static constexpr int kRowsFull0 = kPvDone0 + 4 * kBufs;  // [kRowsAhead] where the expanding warps find a tile's rows
+  static constexpr int kRowsFree0 = kRowsFull0 + kRowsAhead;   // that place read (a signal of every expanding warp)
+  static constexpr int kQReady = kRowsFree0 + kRowsAhead;  // the unit's query in place (a signal of every softmax warp)
+  static constexpr int kFinal0 = kQReady + 1;              // [2] every MMA of an issuing warp made
+  static constexpr int kNumBars = kFinal0 + 2;
   // shared memory
   static constexpr int kOffQ = 0;
   static constexpr int kQPanel = kNS * 128;                // 128 dims of every term
@@ -112,37 +131,27 @@ struct Shape {
   static constexpr int kOffP = kOffQPe + kNS * 64;
   static constexpr int kOffK = kOffP + (kSide ? 1 : 2) * kPPanel;
   static constexpr int kPanel = kT * 128;                  // 128 tokens x 128 dims
-  static constexpr int kOffKPe = kOffK + 2 * 4 * kPanel;
-  static constexpr int kPeBufs = kRows == 64 ? 1 : 2;      // of the rope part
-  static constexpr int kOffExp = kOffKPe + kPeBufs * kT * 64;   // [2][128] exponent bytes
-  static constexpr int kOffScale = kOffExp + 2 * kT;       // [2][rows] 1 / query scale, by unit parity
+  static constexpr int kOffKPe = kOffK + kBufs * 4 * kPanel;
+  // exponent bytes by buffer and token: with 16 query rows in what their row of P leaves
+  static constexpr bool kExpInP = kRows == 16;
+  static constexpr int kOffExp = kOffKPe + kPeBufs * kT * 64;
+  static __device__ __forceinline__ int exp_at(int buf, int tok) {
+    return kExpInP ? kOffP + tok * kPRow + ((3 ^ ((tok >> 1) & 3)) << 4) + buf : kOffExp + buf * kT + tok;
+  }
+  static constexpr int kOffScale = kOffExp + (kExpInP ? 0 : kBufs * kT);   // [2][rows] 1 / query scale, by unit parity
   static constexpr int kOffRef = kOffScale + 2 * kRows * 4;   // [rows] reference, less kTop - kSlack
   static constexpr int kOffTable = kOffRef + kRows * 4;    // [4] e4m3 codes of the magnitudes, for shifts 12 ..
   static constexpr int kOffRed = kOffTable + 4 * 8;        // [softmax warps][kJ] floats
-  static constexpr int kOffRows = kOffRed + kSoftmaxWarps * kJ * 4;   // [kRowsAhead][expanding warps] Rows
-  static constexpr int kOffBar = kOffRows + kRowsAhead * kExpandWarps * 16;
-  static_assert(kOffTable % 16 == 0 && kOffRows % 16 == 0, "aligned parts");
+  static constexpr int kOffRows = kOffRed + kSoftmaxWarps * kJ * 4;   // [kRowsAhead][expanding warps] packed rows
+  static constexpr int kOffBar = kOffRows + kRowsAhead * kExpandWarps * 8;
   static_assert(kOffP % 1024 == 0 && kOffK % 1024 == 0 && kOffKPe % 1024 == 0, "swizzle atoms");
 };
 
-enum Bar {
-  kKFull0,                   // [2] tile expanded (a signal of every expanding warp)
-  kSFull0 = kKFull0 + 2,     // [2] scores made
-  kSFree0 = kSFull0 + 2,     // [2] scores read (a signal of every softmax warp)
-  kPReady0 = kSFree0 + 2,    // [4] P of 32 tokens written (a signal for every kJ query rows)
-  kPvDone0 = kPReady0 + 4,   // [2][4] P . V over 32 tokens made: their rows of K and P may be written again
-                             // (by tile parity: the next tile's may be made before an expanding warp looks)
-  kRowsFull0 = kPvDone0 + 8, // [4] where the expanding warps find a tile's rows
-  kRowsFree0 = kRowsFull0 + kRowsAhead,   // [4] that place read (a signal of every expanding warp)
-  kQReady = kRowsFree0 + kRowsAhead,    // the unit's query in place
-  kFinal0,                   // [2] every MMA of an issuing warp made
-  kNumBars = kFinal0 + 2
-};
 template <int kRows>
 constexpr int smem_bytes() {
-  return Shape<kRows>::kOffBar + 8 * kNumBars + 16;   // tensor memory's address, abort flag
+  return Shape<kRows>::kOffBar + 8 * Shape<kRows>::kNumBars + 8;   // tensor memory's address, abort flag
 }
-static_assert(smem_bytes<64>() <= 232448, "shared memory budget");
+static_assert(smem_bytes<16>() <= 232448 && smem_bytes<32>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory budget");
 
 // A and B of kind::f8f6f4: format 0 e4m3, 1 e5m2; D f32.
 constexpr uint32_t idesc_f8(int N, int b_format, bool mn) {
@@ -326,10 +335,11 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using S = Shape<kRows>;
   constexpr int kJ = S::kJ, kSoftmaxWarps = S::kSoftmaxWarps, kExpandWarps = S::kExpandWarps, kIssueWarp = S::kIssueWarp, kTokWarp = S::kTokWarp;
+  constexpr int kBufs = S::kBufs;
   extern __shared__ __align__(1024) unsigned char sm[];
   const uint32_t base = smem_u32(sm);
   auto bar = [&](int i) { return base + S::kOffBar + 8 * i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kOffBar + 8 * kNumBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kOffBar + 8 * S::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -343,11 +353,11 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i < kSFull0 || (i >= kRowsFree0 && i <= kQReady) ? kExpandWarps
-                        : i == kSFree0 || i == kSFree0 + 1    ? kSoftmaxWarps
-                        : i >= kPReady0 && i < kPvDone0       ? kSoftmaxWarps / 4
-                                                              : 1);
+    for (int i = 0; i < S::kNumBars; ++i)
+      mbar_init(bar(i), i < S::kSFull0 || (i >= S::kRowsFree0 && i < S::kQReady) ? kExpandWarps
+                        : (i >= S::kSFree0 && i < S::kPReady0) || i == S::kQReady ? kSoftmaxWarps
+                        : i >= S::kPReady0 && i < S::kPvDone0                     ? kSoftmaxWarps / 4
+                                                                                  : 1);
     fence_barrier_init();
   }
   if (threadIdx.x < 4) {
@@ -362,6 +372,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     }
     reinterpret_cast<uint2*>(sm + S::kOffTable)[threadIdx.x] = make_uint2(t[0], t[1]);
   }
+  if (threadIdx.x < kRows) reinterpret_cast<float*>(sm + S::kOffRef)[threadIdx.x] = 0.f;
   if (warp == kIssueWarp) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     set_registers<S::kRegs, S::kRegsIssue>();
     if (warp == kIssueWarp + 2 && u0 < u1) {
       // ================= the warp that finds the rows =================
-      // Lane e: where expanding warp e has its rows of each tile, kRowsAhead tiles ahead,
+      // Lane e: where expanding warp e has its rows of each tile, S::kRowsAhead tiles ahead,
       // and the request for them into L2.  After the last tile, one without rows.
       const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
       Cursor at;
@@ -383,21 +394,22 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       bool more = true;
       for (int g = 0;; ++g) {
         const int t = at.tok0() + kTokWarp * lane;
-        Rows r = {cache, 0};
+        uint64_t r = 0;
         if (more && lane < kExpandWarps && t < at.tok_end) {
           const int page = a.kv_indices[at.page_base + (t >> page_shift)];
           if (page < 0 || page >= a.num_pages) {   // its rows count as zeros
             report_error(a.err, kErrBounds);
           } else {
-            r.n = min(kTokWarp, at.tok_end - t);
-            r.src += ((static_cast<size_t>(page) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(r.src), "r"(static_cast<int>(r.n) * kQ4Row) : "memory");
+            const int n = min(kTokWarp, at.tok_end - t);
+            const uint8_t* src = cache + ((static_cast<size_t>(page) << page_shift) + (t & ((1 << page_shift) - 1))) * kQ4Row;
+            r = pack_rows(src, n);
+            bulk_prefetch_l2(src, n * kQ4Row);
           }
         }
-        if (g >= kRowsAhead) wait(kRowsFree0 + g % kRowsAhead, (g - kRowsAhead) / kRowsAhead);
-        if (lane < kExpandWarps) reinterpret_cast<Rows*>(sm + S::kOffRows)[g % kRowsAhead * kExpandWarps + lane] = r;
+        if (g >= S::kRowsAhead) wait(S::kRowsFree0 + g % S::kRowsAhead, (g - S::kRowsAhead) / S::kRowsAhead);
+        if (lane < kExpandWarps) reinterpret_cast<uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kExpandWarps + lane] = r;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kRowsFull0 + g % kRowsAhead));
+        if (lane == 0) mbar_arrive(bar(S::kRowsFull0 + g % S::kRowsAhead));
         if (!more) break;
         more = at.next(a.units, u1);
       }
@@ -411,13 +423,13 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       const uint64_t p_desc = smem_desc(base + S::kOffP, 16, 8 * S::kPRow, S::kPSwizzle);
       constexpr uint32_t id_s = idesc_f8(S::kNS, 0, false), id_hi = idesc_f8(S::kPN, 1, true), id_lo = idesc_f8(S::kPN, 0, true);
       auto scores = [&](int g) {
-        if (g > 1) wait(kSFree0 + (g & 1), (g - 2) >> 1);
-        wait(kKFull0 + (g & 1), g >> 1);
+        if (g > 1) wait(S::kSFree0 + (g & 1), (g - 2) >> 1);
+        wait(S::kKFull0 + g % kBufs, g / kBufs);
         tc_fence_after();
         const uint32_t d = tmem + S::kColS + (g & 1) * S::kNS;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const uint64_t ka = k_desc + static_cast<uint64_t>((((g & 1) * 4 + p) * S::kPanel) >> 4);
+          const uint64_t ka = k_desc + static_cast<uint64_t>(((g % kBufs * 4 + p) * S::kPanel) >> 4);
           const uint64_t qb = q_desc + static_cast<uint64_t>((p * S::kQPanel) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_f8_elect(d, ka + 2 * kk, qb + 2 * kk, id_s, (p | kk) != 0);
@@ -425,17 +437,17 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
           mma_f8_elect(d, kpe_desc + static_cast<uint64_t>(((S::kPeBufs == 2 ? (g & 1) * kT * 64 : 0) >> 4) + 2 * kk), qpe_desc + 2 * kk, id_s, 1);
-        mma_commit_elect(bar(kSFull0 + (g & 1)));
+        mma_commit_elect(bar(S::kSFull0 + (g & 1)));
       };
       auto values = [&](int g, bool first) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {   // 32 tokens
-          wait(kPReady0 + j, g);
+          wait(S::kPReady0 + j, g);
           tc_fence_after();
           const uint64_t pb = p_desc + static_cast<uint64_t>((j * 32 * S::kPRow) >> 4);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            const uint64_t va = k_desc + static_cast<uint64_t>((((g & 1) * 4 + p) * S::kPanel + j * 32 * 128) >> 4);
+            const uint64_t va = k_desc + static_cast<uint64_t>(((g % kBufs * 4 + p) * S::kPanel + j * 32 * 128) >> 4);
             if constexpr (S::kSide) {
               mma_f8_elect(tmem + p * S::kOBlock, va, pb, id_hi, !first || j > 0);
             } else {
@@ -443,7 +455,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
               mma_f8_elect(tmem + p * S::kOBlock, va, pb + static_cast<uint64_t>(S::kPPanel >> 4), id_lo, 1);
             }
           }
-          mma_commit_elect(bar(kPvDone0 + 4 * (g & 1) + j));
+          mma_commit_elect(bar(S::kPvDone0 + 4 * (g % kBufs) + j));
         }
       };
       // The scores of a tile need its rows, P . V of the tile before its P: whichever
@@ -454,15 +466,15 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       int g = 0;
       for (int ui = u0; ui < u1; ++ui) {
         const int n = (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
-        if (role == 0) wait(kQReady, ui - u0);
+        if (role == 0) wait(S::kQReady, ui - u0);
         for (int i = 0; i < n; ++i, ++g) {
           if (role == 0) scores(g);
           else values(g, i == 0);
         }
       }
-      mma_commit_elect(bar(kFinal0 + role));
+      mma_commit_elect(bar(S::kFinal0 + role));
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
-      mbar_wait_drain(bar(kFinal0 + role), 0);   // every MMA issued is done before tensor memory is freed
+      mbar_wait_drain(bar(S::kFinal0 + role), 0);   // every MMA issued is done before tensor memory is freed
       __syncwarp();
     }
   } else if (warp >= kSoftmaxWarps) {
@@ -472,10 +484,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       const int ew = warp - kSoftmaxWarps;
       const uint2* table = reinterpret_cast<const uint2*>(sm + S::kOffTable);
       auto rows_of = [&](int g) {
-        wait(kRowsFull0 + g % kRowsAhead, g / kRowsAhead);
-        const Rows r = reinterpret_cast<const Rows*>(sm + S::kOffRows)[g % kRowsAhead * kExpandWarps + ew];
+        wait(S::kRowsFull0 + g % S::kRowsAhead, g / S::kRowsAhead);
+        const Rows r(reinterpret_cast<const uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kExpandWarps + ew]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kRowsFree0 + g % kRowsAhead));
+        if (lane == 0) mbar_arrive(bar(S::kRowsFree0 + g % S::kRowsAhead));
         return r;
       };
       // A lane takes whole groups (16 bytes of codes): of ckv, group 4 (lane / 8) + lane % 4
@@ -524,7 +536,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         const bool whole = next.n == kTokWarp;
         auto fill = [&](auto table_of) {
           // chunk 2 pair of row 2 i + odd is at 2 pair ^ odd ^ (2 i & 7)
-          unsigned char* dst = sm + S::kOffK + (g & 1) * 4 * S::kPanel + panel * S::kPanel + (kTokWarp * ew + odd) * 128;
+          unsigned char* dst = sm + S::kOffK + g % kBufs * 4 * S::kPanel + panel * S::kPanel + (kTokWarp * ew + odd) * 128;
           uint32_t mine[kTokWarp / 2];   // shifts of groups 4 panel ..
 #pragma unroll
           for (int i = 0; i < kTokWarp / 2; ++i) mine[i] = __shfl_sync(~0u, shift[i / 4], 8 * (i % 4) + 4 * odd + panel);
@@ -537,14 +549,14 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             *reinterpret_cast<uint4*>(at2 + 256 * i) = expand16(t, raw[i].z, raw[i].w);
             if (whole) raw[i] = load_ckv(next, i);
           }
-          if (S::kPeBufs == 1 && g > 0) wait(kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read it
+          if (S::kPeBufs == 1 && g > 0) wait(S::kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read it
           if (kTokWarp == 16 || lane < 16) {
             const int row = kTokWarp * ew + (lane >> 1);
             const uint2 t = table_of((meta >> (4 * (lane & 1))) & 15);
             const int at = (S::kPeBufs == 2 ? (g & 1) * kT * 64 : 0) + row * 64 + (((2 * (lane & 1)) ^ ((row >> 1) & 3)) << 4);
             *reinterpret_cast<uint4*>(sm + S::kOffKPe + at) = expand16(t, codes_pe.x, codes_pe.y);
             *reinterpret_cast<uint4*>(sm + S::kOffKPe + (at ^ 16)) = expand16(t, codes_pe.z, codes_pe.w);
-            if ((lane & 1) == 0) sm[S::kOffExp + (g & 1) * kT + row] = static_cast<unsigned char>(meta >> 8);
+            if ((lane & 1) == 0) sm[S::exp_at(g % kBufs, row)] = static_cast<unsigned char>(meta >> 8);
           }
         };
         if (__any_sync(~0u, large)) fill([&](uint32_t k) { return k >= 12 ? table[k - 12] : normal_table(k); });
@@ -554,66 +566,21 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #ifdef MLA_STALL_TEST
         if (blockIdx.x == 0 && ew == 0 && g + 1 == g_q4_stall) return;
 #endif
-        if (lane == 0) mbar_arrive(bar(kKFull0 + (g & 1)));
+        if (lane == 0) mbar_arrive(bar(S::kKFull0 + g % kBufs));
         if (!whole) load_part(next);
-      };
-      // ---- the query of a unit, kRows / 8 rows a warp ----
-      auto put_query = [&](int ui) {
-        const size_t first_row = static_cast<size_t>(a.units[ui].req) * H + row0;
-        float* scale = reinterpret_cast<float*>(sm + S::kOffScale) + ((ui - u0) & 1) * kRows;
-#pragma unroll 1
-        for (int k = 0; k < kRows / kExpandWarps; ++k) {
-          const int r = ew * (kRows / kExpandWarps) + k;
-          uint32_t w[9] = {};   // dims 16 lane .. + 15 of q_nope, 2 lane and + 1 of q_pe
-          if (row0 + r < H) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_nope) + (first_row + r) * kDCkv + 16 * lane);
-            const uint4 v0 = src[0], v1 = src[1];
-            w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w, w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
-            w[8] = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q_pe) + (first_row + r) * kDKpe)[lane];
-          }
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < 9; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-          const uint32_t top = __reduce_max_sync(~0u, max(m >> 16, m & 0xffffu));   // bits of the largest magnitude
-          const int e = top == 0 ? 0 : min(max(7 - (static_cast<int>(top >> 7) - 127), -100), 100);
-          const float up = pow2(e);
-          uint32_t hi[9], lo[9];
-#pragma unroll
-          for (int i = 0; i < 9; ++i)
-            split_query(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up, hi[i], lo[i]);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t* c = t ? lo : hi;
-            const int row = t * kRows + r;
-            *reinterpret_cast<uint4*>(sm + S::kOffQ + (lane >> 3) * S::kQPanel + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
-                make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
-            *reinterpret_cast<uint16_t*>(sm + S::kOffQPe + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7)) =
-                static_cast<uint16_t>(c[8]);
-          }
-          // an infinite or NaN query has NaN scores
-          if (lane == 0) scale[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff) : pow2(-e);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kQReady));
       };
       {
         const Rows rows = rows_of(0);
         load_part(rows);
         load_rest(rows);
       }
-      put_query(u0);
       int g = 0;
       for (int ui = u0; ui < u1; ++ui) {
         const int n = (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
         for (int i = 0; i < n; ++i, ++g) {
-          // the buffer was read by P . V of g - 2
-          if (g > 1) wait(kPvDone0 + 4 * (g & 1) + ew * kTokWarp / 32, (g - 2) >> 1);
+          // the buffer was read by P . V of g - kBufs
+          if (g >= kBufs) wait(S::kPvDone0 + 4 * (g % kBufs) + ew * kTokWarp / 32, g / kBufs - 1);
           expand(g, rows_of(g + 1));
-          if (i == 0 && ui > u0) {
-            wait(kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read the last one
-            put_query(ui);
-          }
         }
       }
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
@@ -626,6 +593,47 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     const int tok = 32 * q + lane;
     float* refs = reinterpret_cast<float*>(sm + S::kOffRef) + kJ * cg;
     float* red = reinterpret_cast<float*>(sm + S::kOffRed) + 4 * cg * kJ;   // of the four warps of these query rows
+    // ---- the query of a unit, a few rows a warp ----
+    auto put_query = [&](int ui) {
+      const size_t first_row = static_cast<size_t>(a.units[ui].req) * H + row0;
+      float* out = reinterpret_cast<float*>(sm + S::kOffScale) + ((ui - u0) & 1) * kRows;
+#pragma unroll 1
+      for (int k = 0; k < kRows / kSoftmaxWarps; ++k) {
+        const int r = warp * (kRows / kSoftmaxWarps) + k;
+        uint32_t w[9] = {};   // dims 16 lane .. + 15 of q_nope, 2 lane and + 1 of q_pe
+        if (row0 + r < H) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_nope) + (first_row + r) * kDCkv + 16 * lane);
+          const uint4 v0 = src[0], v1 = src[1];
+          w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w, w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
+          w[8] = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q_pe) + (first_row + r) * kDKpe)[lane];
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 9; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        const uint32_t top = __reduce_max_sync(~0u, max(m >> 16, m & 0xffffu));   // bits of the largest magnitude
+        const int e = top == 0 ? 0 : min(max(7 - (static_cast<int>(top >> 7) - 127), -100), 100);
+        const float up = pow2(e);
+        uint32_t hi[9], lo[9];
+#pragma unroll
+        for (int i = 0; i < 9; ++i)
+          split_query(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up, hi[i], lo[i]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t* c = t ? lo : hi;
+          const int row = t * kRows + r;
+          *reinterpret_cast<uint4*>(sm + S::kOffQ + (lane >> 3) * S::kQPanel + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+              make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+          *reinterpret_cast<uint16_t*>(sm + S::kOffQPe + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7)) =
+              static_cast<uint16_t>(c[8]);
+        }
+        // an infinite or NaN query has NaN scores
+        if (lane == 0) out[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff) : pow2(-e);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(S::kQReady));
+    };
+    if (u0 < u1) put_query(u0);
     int g = 0;
     for (int ui = u0; ui < u1; ++ui) {
       const WorkUnit u = a.units[ui];
@@ -636,10 +644,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       for (int t0 = u.tok_begin; t0 < u.tok_end; t0 += kT, ++g) {
         const bool first = t0 == u.tok_begin;
         // ---- scores of this thread's token and query rows, less the reference, in log2 ----
-        wait(kSFull0 + (g & 1), g >> 1);
+        wait(S::kSFull0 + (g & 1), g >> 1);
         tc_fence_after();
         float z[kJ];
-        const int exponent = sm[S::kOffExp + (g & 1) * kT + tok];
+        const int exponent = sm[S::exp_at(g % kBufs, tok)];
         const int e = exponent == kQ4NanExp ? 0 : exponent - 127;
         {
           uint32_t hi[kJ], lo[kJ];
@@ -655,14 +663,14 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             const float2 ref = *reinterpret_cast<const float2*>(refs + j);
             const float2 s = add2(make_float2(__uint_as_float(hi[j]), __uint_as_float(hi[j + 1])),
                                   make_float2(__uint_as_float(lo[j]), __uint_as_float(lo[j + 1])));
-            const float2 b = first ? make_float2(fe, fe) : make_float2(fe - ref.x, fe - ref.y);
+            const float2 b = make_float2(fe - ref.x, fe - ref.y);
             const float2 y = fma2(mul2(s, make_float2(unit, unit)), f, b);
             z[j] = y.x;
             z[j + 1] = y.y;
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kSFree0 + (g & 1)));
+          if (lane == 0) mbar_arrive(bar(S::kSFree0 + (g & 1)));
         }
         if (t0 + kT > u.tok_end - (prm.q_len > 1 ? prm.q_len - 1 : 0)) {
           // the query rows that see token t: of query tokens packed into rows, row h sees
@@ -698,10 +706,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
               ld[j] *= alpha;
               if (lane == j) mine = alpha;
             }
-            if (q == 0 && lane == j) refs[j] = (first ? 0.f : refs[j]) + up;
+            if (q == 0 && lane == j) refs[j] += up;
           }
           if (moved) {   // their columns of O, a row at a time: few move at once
-            wait(kPvDone0 + 4 * ((g - 1) & 1) + 3, (g - 1) >> 1);
+            wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + 3, (g - 1) / kBufs);
             tc_fence_after();
             do {
               const int j = __ffs(moved) - 1;
@@ -745,14 +753,14 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             rest = __hsub2(rest, from_fp8x2<__NV_E4M3>(code[1]));
           }
           // what the terms leave of p, counted in full from kFull on and less below
-          const float2 share = mul2(make_float2(__saturatef(p.x * (1 / S::kFull)), __saturatef(p.y * (1 / S::kFull))), weight);
-          const float2 y = fma2(__half22float2(rest), share, make_float2(ld[j], ld[j + 1]));
+          rest = __hmul2(rest, __hmul2_sat(h, __float2half2_rn(1 / S::kFull)));
+          const float2 y = fma2(__half22float2(rest), weight, make_float2(ld[j], ld[j + 1]));
           ld[j] = y.x;
           ld[j + 1] = y.y;
 #pragma unroll
           for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
         }
-        if (g > 0) wait(kPvDone0 + 4 * ((g - 1) & 1) + q, (g - 1) >> 1);   // P . V of the tile before has read these rows of P
+        if (g > 0) wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + q, (g - 1) / kBufs);   // P . V of the tile before has read these rows of P
         unsigned char* prow = sm + S::kOffP + tok * S::kPRow;
 #pragma unroll
         for (int i = 0; i < kTerms; ++i) {
@@ -766,8 +774,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPReady0 + q));
+        if (lane == 0) mbar_arrive(bar(S::kPReady0 + q));
       }
+      // the next unit's query: every score of this one is made
+      if (ui + 1 < u1) put_query(ui + 1);
       // ---- epilogue: the sums over the unit's tokens of all lanes and quadrants ----
       const bool split = u.out_slot >= 0;
       const float sx = warp_reduce<false>(lx);
@@ -792,7 +802,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         const float s = (red[j] + red[kJ + j]) + (red[2 * kJ + j] + red[3 * kJ + j]);
         inv[j] = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
       }
-      wait(kPvDone0 + 4 * ((g - 1) & 1) + 3, (g - 1) >> 1);
+      wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + 3, (g - 1) / kBufs);
       tc_fence_after();
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
@@ -836,6 +846,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           }
         }
       }
+      if (q == 0 && lane < kJ) refs[lane] = 0.f;   // the next unit's first tile sets them
       tc_fence_before();             // O is read: the next unit's first P . V waits for P of all warps
       named_bar_sync(1 + cg, 128);   // red and the references may be written again
     }
