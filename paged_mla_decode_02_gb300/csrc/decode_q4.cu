@@ -495,8 +495,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       // banks; of kpe, group lane % 2 of row lane / 2.  Shifts of ckv: four of row 8 i +
       // lane / 4 a lane.
       const int panel = lane >> 3, odd = (lane >> 2) & 1, pair = lane & 3;
+      // Of kpe with eight rows a warp: half a group a lane, a quarter of row lane / 4.
       uint4 raw[kTokWarp / 2], raw_pe;
       uint32_t shifts[kTokWarp / 8], meta_pe;
+      constexpr int kPeShift = kTokWarp == 16 ? 1 : 2;   // lanes of a row's kpe
       auto load_ckv = [&](const Rows& r, int i) {   // rows 2 i and 2 i + 1
         return __ldg(reinterpret_cast<const uint4*>(r.src + (2 * i + odd) * kQ4Row) + 4 * panel + pair);
       };
@@ -508,9 +510,14 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         }
         raw_pe = make_uint4(0, 0, 0, 0);
         meta_pe = 127 << 8;
-        if ((lane >> 1) < r.n) {
-          const uint8_t* row = r.src + (lane >> 1) * kQ4Row;
-          raw_pe = __ldg(reinterpret_cast<const uint4*>(row + kDCkv / 2) + (lane & 1));
+        if ((lane >> kPeShift) < r.n) {
+          const uint8_t* row = r.src + (lane >> kPeShift) * kQ4Row;
+          if constexpr (kTokWarp == 16) {
+            raw_pe = __ldg(reinterpret_cast<const uint4*>(row + kDCkv / 2) + (lane & 1));
+          } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + kDCkv / 2) + (lane & 3));
+            raw_pe.x = v.x, raw_pe.y = v.y;
+          }
           meta_pe = __ldg(reinterpret_cast<const uint16_t*>(row + kQ4Meta + 8));
         }
       };
@@ -550,14 +557,17 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             if (whole) raw[i] = load_ckv(next, i);
           }
           if (S::kPeBufs == 1 && g > 0) wait(S::kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read it
-          if (kTokWarp == 16 || lane < 16) {
-            const int row = kTokWarp * ew + (lane >> 1);
-            const uint2 t = table_of((meta >> (4 * (lane & 1))) & 15);
-            const int at = (S::kPeBufs == 2 ? (g & 1) * kT * 64 : 0) + row * 64 + (((2 * (lane & 1)) ^ ((row >> 1) & 3)) << 4);
-            *reinterpret_cast<uint4*>(sm + S::kOffKPe + at) = expand16(t, codes_pe.x, codes_pe.y);
-            *reinterpret_cast<uint4*>(sm + S::kOffKPe + (at ^ 16)) = expand16(t, codes_pe.z, codes_pe.w);
-            if ((lane & 1) == 0) sm[S::exp_at(g % kBufs, row)] = static_cast<unsigned char>(meta >> 8);
+          const int row = kTokWarp * ew + (lane >> kPeShift);
+          unsigned char* pe = sm + S::kOffKPe + (S::kPeBufs == 2 ? (g & 1) * kT * 64 : 0) + row * 64;
+          const uint2 t = table_of((meta >> (kTokWarp == 16 ? 4 * (lane & 1) : 2 * (lane & 2))) & 15);
+          if constexpr (kTokWarp == 16) {
+            const int at = ((2 * (lane & 1)) ^ ((row >> 1) & 3)) << 4;
+            *reinterpret_cast<uint4*>(pe + at) = expand16(t, codes_pe.x, codes_pe.y);
+            *reinterpret_cast<uint4*>(pe + (at ^ 16)) = expand16(t, codes_pe.z, codes_pe.w);
+          } else {
+            *reinterpret_cast<uint4*>(pe + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) = expand16(t, codes_pe.x, codes_pe.y);
           }
+          if ((lane & ((1 << kPeShift) - 1)) == 0) sm[S::exp_at(g % kBufs, row)] = static_cast<unsigned char>(meta >> 8);
         };
         if (__any_sync(~0u, large)) fill([&](uint32_t k) { return k >= 12 ? table[k - 12] : normal_table(k); });
         else fill([](uint32_t k) { return normal_table(k); });
