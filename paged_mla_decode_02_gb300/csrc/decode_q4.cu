@@ -94,10 +94,14 @@ struct Shape {
   static constexpr int kExpandWarps = kRows == 64 ? 8 : 16;
   static constexpr int kIssueWarp = kSoftmaxWarps + kExpandWarps;
   static constexpr int kThreads = 32 * (kIssueWarp + 4);
-  static constexpr int kTokWarp = kT / kExpandWarps;       // rows that a warp expands, of one page
+  // With three tiles in flight the expanding warps are two groups, for the even and the
+  // odd tiles: what a tile costs a warp besides its rows counts half.
+  static constexpr int kGroups = kRows == 16 ? 2 : 1;
+  static constexpr int kTileWarps = kExpandWarps / kGroups;
+  static constexpr int kTokWarp = kT / kTileWarps;         // rows that a warp expands, of one page
   // registers a thread at launch, then by role
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kRegsSoftmax = kRows == 64 ? 80 : 88, kRegsExpand = kRows == 64 ? 80 : 72;
+  static constexpr int kRegsSoftmax = kRows == 32 ? 88 : 80, kRegsExpand = kRows == 32 ? 72 : 80;
   static constexpr int kRegsIssue = 24;
   static_assert(32 * (kSoftmaxWarps * kRegsSoftmax + kExpandWarps * kRegsExpand + 4 * kRegsIssue) <= kThreads * kRegs, "registers");
   // p reaches 2^kTop: the reference is set to leave kSlack of that, and moves when it is used up
@@ -110,9 +114,9 @@ struct Shape {
   static_assert(kColS + 2 * kNS <= 512, "tensor memory");
   static constexpr int kBufs = kRows == 16 ? 3 : 2;        // expanded tiles
   static constexpr int kPeBufs = kRows == 32 ? 2 : 1;      // of the rope part
-  static constexpr int kRowsAhead = kRows == 16 ? 2 : 4;   // tiles whose rows are known ahead
+  static constexpr int kRowsAhead = 4;                     // tiles whose rows are known ahead
   // barriers
-  static constexpr int kKFull0 = 0;                        // [kBufs] tile expanded (a signal of every expanding warp)
+  static constexpr int kKFull0 = 0;                        // [kBufs] tile expanded (a signal of each of its warps)
   static constexpr int kSFull0 = kKFull0 + kBufs;          // [2] scores made
   static constexpr int kSFree0 = kSFull0 + 2;              // [2] scores read (a signal of every softmax warp)
   static constexpr int kPReady0 = kSFree0 + 2;             // [4] P of 32 tokens written (a signal for every kJ query rows)
@@ -120,7 +124,7 @@ struct Shape {
   // buffer: the next tile's may be made before an expanding warp looks)
   static constexpr int kPvDone0 = kPReady0 + 4;
   static constexpr int kRowsFull0 = kPvDone0 + 4 * kBufs;  // [kRowsAhead] where the expanding warps find a tile's rows
-  static constexpr int kRowsFree0 = kRowsFull0 + kRowsAhead;   // that place read (a signal of every expanding warp)
+  static constexpr int kRowsFree0 = kRowsFull0 + kRowsAhead;   // that place read (a signal of each)
   static constexpr int kQReady = kRowsFree0 + kRowsAhead;  // the unit's query in place (a signal of every softmax warp)
   static constexpr int kFinal0 = kQReady + 1;              // [2] every MMA of an issuing warp made
   static constexpr int kNumBars = kFinal0 + 2;
@@ -142,8 +146,8 @@ struct Shape {
   static constexpr int kOffRef = kOffScale + 2 * kRows * 4;   // [rows] reference, less kTop - kSlack
   static constexpr int kOffTable = kOffRef + kRows * 4;    // [4] e4m3 codes of the magnitudes, for shifts 12 ..
   static constexpr int kOffRed = kOffTable + 4 * 8;        // [softmax warps][kJ] floats
-  static constexpr int kOffRows = kOffRed + kSoftmaxWarps * kJ * 4;   // [kRowsAhead][expanding warps] packed rows
-  static constexpr int kOffBar = kOffRows + kRowsAhead * kExpandWarps * 8;
+  static constexpr int kOffRows = kOffRed + kSoftmaxWarps * kJ * 4;   // [kRowsAhead][warps of a tile] packed rows
+  static constexpr int kOffBar = kOffRows + kRowsAhead * kTileWarps * 8;
   static_assert(kOffP % 1024 == 0 && kOffK % 1024 == 0 && kOffKPe % 1024 == 0, "swizzle atoms");
 };
 
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using S = Shape<kRows>;
-  constexpr int kJ = S::kJ, kSoftmaxWarps = S::kSoftmaxWarps, kExpandWarps = S::kExpandWarps, kIssueWarp = S::kIssueWarp, kTokWarp = S::kTokWarp;
+  constexpr int kJ = S::kJ, kSoftmaxWarps = S::kSoftmaxWarps, kTileWarps = S::kTileWarps, kIssueWarp = S::kIssueWarp, kTokWarp = S::kTokWarp;
   constexpr int kBufs = S::kBufs;
   extern __shared__ __align__(1024) unsigned char sm[];
   const uint32_t base = smem_u32(sm);
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < S::kNumBars; ++i)
-      mbar_init(bar(i), i < S::kSFull0 || (i >= S::kRowsFree0 && i < S::kQReady) ? kExpandWarps
+      mbar_init(bar(i), i < S::kSFull0 || (i >= S::kRowsFree0 && i < S::kQReady) ? kTileWarps
                         : (i >= S::kSFree0 && i < S::kPReady0) || i == S::kQReady ? kSoftmaxWarps
                         : i >= S::kPReady0 && i < S::kPvDone0                     ? kSoftmaxWarps / 4
                                                                                   : 1);
@@ -386,16 +390,18 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     if (warp == kIssueWarp + 2 && u0 < u1) {
       // ================= the warp that finds the rows =================
       // Lane e: where expanding warp e has its rows of each tile, S::kRowsAhead tiles ahead,
-      // and the request for them into L2.  After the last tile, one without rows.
+      // and the request for them into L2.  Behind the last tile, one without rows for
+      // each group.
       const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
       Cursor at;
       at.ui = u0;
       at.read(a.units);
       bool more = true;
+      int behind = 0;
       for (int g = 0;; ++g) {
         const int t = at.tok0() + kTokWarp * lane;
         uint64_t r = 0;
-        if (more && lane < kExpandWarps && t < at.tok_end) {
+        if (more && lane < kTileWarps && t < at.tok_end) {
           const int page = a.kv_indices[at.page_base + (t >> page_shift)];
           if (page < 0 || page >= a.num_pages) {   // its rows count as zeros
             report_error(a.err, kErrBounds);
@@ -407,11 +413,11 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           }
         }
         if (g >= S::kRowsAhead) wait(S::kRowsFree0 + g % S::kRowsAhead, (g - S::kRowsAhead) / S::kRowsAhead);
-        if (lane < kExpandWarps) reinterpret_cast<uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kExpandWarps + lane] = r;
+        if (lane < kTileWarps) reinterpret_cast<uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kTileWarps + lane] = r;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::kRowsFull0 + g % S::kRowsAhead));
-        if (!more) break;
-        more = at.next(a.units, u1);
+        if (more) more = at.next(a.units, u1);
+        else if (++behind == S::kGroups) break;
       }
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
     } else if (warp <= kIssueWarp + 1) {
@@ -481,11 +487,13 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     // ================= expanding warps =================
     set_registers<S::kRegs, S::kRegsExpand>();
     if (u0 < u1) {
-      const int ew = warp - kSoftmaxWarps;
+      const int group = (warp - kSoftmaxWarps) / kTileWarps, ew = (warp - kSoftmaxWarps) % kTileWarps;
+      int tiles = 0;
+      for (int ui = u0; ui < u1; ++ui) tiles += (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
       const uint2* table = reinterpret_cast<const uint2*>(sm + S::kOffTable);
       auto rows_of = [&](int g) {
         wait(S::kRowsFull0 + g % S::kRowsAhead, g / S::kRowsAhead);
-        const Rows r(reinterpret_cast<const uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kExpandWarps + ew]);
+        const Rows r(reinterpret_cast<const uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kTileWarps + ew]);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::kRowsFree0 + g % S::kRowsAhead));
         return r;
@@ -580,18 +588,14 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (!whole) load_part(next);
       };
       {
-        const Rows rows = rows_of(0);
+        const Rows rows = rows_of(group);
         load_part(rows);
         load_rest(rows);
       }
-      int g = 0;
-      for (int ui = u0; ui < u1; ++ui) {
-        const int n = (a.units[ui].tok_end - a.units[ui].tok_begin + kT - 1) / kT;
-        for (int i = 0; i < n; ++i, ++g) {
-          // the buffer was read by P . V of g - kBufs
-          if (g >= kBufs) wait(S::kPvDone0 + 4 * (g % kBufs) + ew * kTokWarp / 32, g / kBufs - 1);
-          expand(g, rows_of(g + 1));
-        }
+      for (int g = group; g < tiles; g += S::kGroups) {
+        // the buffer was read by P . V of g - kBufs
+        if (g >= kBufs) wait(S::kPvDone0 + 4 * (g % kBufs) + ew * kTokWarp / 32, g / kBufs - 1);
+        expand(g, rows_of(g + S::kGroups));
       }
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
     }
