@@ -143,7 +143,7 @@ struct Shape {
     return kExpInP ? kOffP + tok * kPRow + ((3 ^ ((tok >> 1) & 3)) << 4) + buf : kOffExp + buf * kT + tok;
   }
   static constexpr int kOffScale = kOffExp + (kExpInP ? 0 : kBufs * kT);   // [2][rows] 1 / query scale, by unit parity
-  static constexpr int kOffRef = kOffScale + 2 * kRows * 4;   // [rows] reference, less kTop - kSlack
+  static constexpr int kOffRef = kOffScale + 2 * kRows * 4;   // [rows] kTop - kSlack, less the reference
   static constexpr int kOffTable = kOffRef + kRows * 4;    // [4] e4m3 codes of the magnitudes, for shifts 12 ..
   static constexpr int kOffRed = kOffTable + 4 * 8;        // [softmax warps][kJ] floats
   static constexpr int kOffRows = kOffRed + kSoftmaxWarps * kJ * 4;   // [kRowsAhead][warps of a tile] packed rows
@@ -671,20 +671,23 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           const float unit = exponent == kQ4NanExp ? __int_as_float(0x7fffffff) : pow2(e - 6) * (prm.sm_scale * kLog2e);
           const float fe = static_cast<float>(e);
           tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < kJ; j += 2) {
-            const float2 f = *reinterpret_cast<const float2*>(scale + j);
-            const float2 ref = *reinterpret_cast<const float2*>(refs + j);
-            const float2 s = add2(make_float2(__uint_as_float(hi[j]), __uint_as_float(hi[j + 1])),
-                                  make_float2(__uint_as_float(lo[j]), __uint_as_float(lo[j + 1])));
-            const float2 b = make_float2(fe - ref.x, fe - ref.y);
-            const float2 y = fma2(mul2(s, make_float2(unit, unit)), f, b);
-            z[j] = y.x;
-            z[j + 1] = y.y;
-          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(S::kSFree0 + (g & 1)));
+#pragma unroll
+          for (int j = 0; j < kJ; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(scale + j);
+            const float4 ref = *reinterpret_cast<const float4*>(refs + j);
+            auto two = [&](int i, float2 f2, float2 ref2) {
+              const float2 s = add2(make_float2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
+                                    make_float2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+              const float2 y = fma2(mul2(s, make_float2(unit, unit)), f2, add2(make_float2(fe, fe), ref2));
+              z[i] = y.x;
+              z[i + 1] = y.y;
+            };
+            two(j, make_float2(f.x, f.y), make_float2(ref.x, ref.y));
+            two(j + 2, make_float2(f.z, f.w), make_float2(ref.z, ref.w));
+          }
         }
         if (t0 + kT > u.tok_end - (prm.q_len > 1 ? prm.q_len - 1 : 0)) {
           // the query rows that see token t: of query tokens packed into rows, row h sees
@@ -720,7 +723,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
               ld[j] *= alpha;
               if (lane == j) mine = alpha;
             }
-            if (q == 0 && lane == j) refs[j] += up;
+            if (q == 0 && lane == j) refs[j] -= up;
           }
           if (moved) {   // their columns of O, a row at a time: few move at once
             wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + 3, (g - 1) / kBufs);
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       if (q == 0 && lane < kJ && row0 + kJ * cg + lane < H) {
         const int h = row0 + kJ * cg + lane;
         const float s = (red[lane] + red[kJ + lane]) + (red[2 * kJ + lane] + red[3 * kJ + lane]);
-        const float lse = (refs[lane] + log2f(s)) * kLn2;
+        const float lse = (log2f(s) - refs[lane]) * kLn2;
         if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
         else a.lse[static_cast<size_t>(u.req) * H + h] = lse;
       }
