@@ -591,10 +591,13 @@ mla_status_t mla_decode_run_q4(mla_plan_t plan, const void* q_nope, const void* 
   if ((reinterpret_cast<uintptr_t>(cache) | reinterpret_cast<uintptr_t>(q_nope) |
        reinterpret_cast<uintptr_t>(q_pe) | reinterpret_cast<uintptr_t>(out)) & 15)
     return fail(plan, MLA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  int device = -1;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return cuda_fail(plan, e, "cudaGetDevice");
+  if (device != plan->device) return fail(plan, MLA_ERR_INVALID_ARG, "the plan was made on another device than the current one");
   const bool out_f32 = out_dtype == MLA_DTYPE_FP32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const DecodeArgs a = decode_args(plan, q_nope, q_pe, cache, nullptr, 1.f, num_pages, out, lse);
-  cudaError_t e;
   if (plan->prof_start && (e = cudaEventRecord(plan->prof_start, s)) != cudaSuccess)
     return cuda_fail(plan, e, "cudaEventRecord");
   if ((e = launch_decode_q4(a, out_f32, s)) != cudaSuccess) return cuda_fail(plan, e, "decode kernel launch");

@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       const uint2* table = reinterpret_cast<const uint2*>(sm + S::kOffTable);
       auto rows_of = [&](int g) {
         wait(S::kRowsFull0 + g % S::kRowsAhead, g / S::kRowsAhead);
-        const Rows r(reinterpret_cast<const uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kTileWarps + ew]);
+        Rows r(reinterpret_cast<const uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kTileWarps + ew]);
+        if (!ok) r.n = 0;   // given up: nothing need be there
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::kRowsFree0 + g % S::kRowsAhead));
         return r;

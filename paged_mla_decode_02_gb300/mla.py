@@ -382,7 +382,11 @@ def mla_decode_run_q4(plan, q_nope, q_pe, cache, out, lse, stream=None, page_siz
     import torch
     lib = load_library()
     _on_cuda("q_nope q_pe cache out lse", q_nope, q_pe, cache, out, lse)
-    shape, q = cache.shape, q_nope.shape
+    device = torch.cuda.current_device()
+    for name, t in (("q_nope", q_nope), ("q_pe", q_pe), ("cache", cache), ("out", out), ("lse", lse)):
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on the current CUDA device")
+    shape = cache.shape
     if cache.dtype != torch.uint8 or len(shape) != 3 or shape[2] != Q4_ROW_BYTES:
         raise ValueError(f"cache must be uint8 [num_pages, page_size, {Q4_ROW_BYTES}], got {cache.dtype} "
                          f"{tuple(shape)}")
@@ -965,6 +969,18 @@ class MLASparseDecoder:
             out_dtype=None, stream=None):
         """One step: q_nope [B, H, 512] and q_pe [B, H, 64] (or [B, Q, H, .]),
         the cache and its page summaries [num_pages, 576]; returns out, lse."""
+        out, lse, stream = self._choose(q_nope, q_pe, summaries, out, lse, out_dtype, stream)
+        return self.decoder.run(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale, out_dtype, stream)
+
+    def run_q4(self, q_nope, q_pe, cache, summaries, out=None, lse=None, out_dtype=None, stream=None):
+        """run() over a 4-bit cache, for a decoder made with kernel="q4".  Its
+        pages' summaries are those of the rows before they were quantised, or of
+        the rows that mla_read_cache brings back."""
+        out, lse, stream = self._choose(q_nope, q_pe, summaries, out, lse, out_dtype, stream)
+        return self.decoder.run_q4(q_nope, q_pe, cache, out, lse, out_dtype, stream)
+
+    def _choose(self, q_nope, q_pe, summaries, out, lse, out_dtype, stream):
+        """Queues the choice of pages; returns what the decode over them takes."""
         if self._kv_indices is None:
             raise MLAError(ERR_NOT_PLANNED, "MLASparseDecoder.run before plan")
         import torch
@@ -992,7 +1008,7 @@ class MLASparseDecoder:
             st = lib.mla_select_pages(*self._select_args, stream)
         if st != OK:
             _check(st, None, "MLASparseDecoder.run")
-        return self.decoder.run(q_nope, q_pe, ckv_cache, kpe_cache, out, lse, kv_scale, out_dtype, stream)
+        return out, lse, stream
 
     def check_status(self) -> int:
         """Synchronise and raise on a device error of the decode, or of any call of

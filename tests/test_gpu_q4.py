@@ -808,3 +808,88 @@ def test_decode_nan_in_a_split_request(H):
 @pytest.mark.parametrize("H, lens", [(1, [20000, 0, 150, 9000]), (20, [30000]), (64, [9000] * 4), (100, [5000, 5000]), (128, [12000, 1])])
 def test_decode_many_shares(H, lens):
     run_check(Batch(rng_of(56, H), lens, H, 64), torch.bfloat16)
+
+
+@pytest.mark.parametrize("H, P, k, q_len", [(16, 32, 8, 1), (128, 64, 4, 1), (16, 16, 12, 4)])
+def test_sparse_decode_over_a_4bit_cache(H, P, k, q_len):
+    """Summaries of the rows read back, the choice of pages, and the decode over them."""
+    from oracle import paging_oracle as PO
+    rng = rng_of(57, H, P)
+    lens = [40 * P - 3, 9 * P, 3 * P + 1, P // 2, 25 * P - 7]
+    b = Batch(rng, lens, H, P, q_len=q_len, poison=False)
+    n = b.pages * P
+    ckv = torch.zeros(b.pages, P, 512, dtype=torch.bfloat16, device="cuda")
+    kpe = torch.zeros(b.pages, P, 64, dtype=torch.bfloat16, device="cuda")
+    mla.mla_read_cache(b.cache, None, i32([0, b.pages]), torch.arange(b.pages, dtype=torch.int32, device="cuda"), i32([0]),
+                       i32([0, n]), ckv.view(n, 512), kpe.view(n, 64), check_status=True)
+    summaries = torch.zeros(b.pages, 576, dtype=torch.bfloat16, device="cuda")
+    mla.mla_summarize_pages(torch.arange(P - 1, n, P, device="cuda"), ckv, kpe, summaries, check_status=True)
+    dec = mla.MLASparseDecoder(len(lens) * q_len, H, 64, k, 1, 2, kernel="q4")
+    dec.plan(b.indptr, i32(b.ids), lens, P, b.sm_scale, q_len=q_len if q_len > 1 else 0)
+    out, lse = dec.run_q4(b.q_nope, b.q_pe, b.cache, summaries, out_dtype=torch.float32)
+    dec.check_status()
+    # the selected lists, checked against the oracle's choice, then decoded
+    sel, ids = dec.sel_indptr.cpu().numpy(), dec.sel_indices.cpu().numpy()
+    s64 = f64(summaries)
+    for r, count in enumerate(lens):
+        pages = b.ids[b.indptr[r]:b.indptr[r + 1]]
+        q = f64(b.q)[r].reshape(-1, 576)
+        score = (q @ s64[pages].T).max(0)
+        got = ids[sel[r]:sel[r + 1]]
+        assert len(got) == min(k, len(pages)) and got[-1] == pages[-1] and got[0] == pages[0]
+        left = sorted(set(range(1, len(pages) - 2)) - {list(pages).index(p) for p in got}, key=lambda i: -score[i])
+        kept = [list(pages).index(p) for p in got]
+        inner = [i for i in kept if 1 <= i < len(pages) - 2]
+        if left and inner:
+            assert min(score[i] for i in inner) >= score[left[0]] - 2.0 ** -10 * abs(score[left[0]])
+    part = Batch.__new__(Batch)
+    part.__dict__.update(b.__dict__)
+    part.lens = [min(k, -(-x // P)) * P - (-x) % P for x in lens]
+    part.indptr, part.ids = sel, ids
+    check_decode(part, out, lse)
+    with pytest.raises(mla.MLAError):                      # the plan is one for 4-bit caches
+        dec.run(b.q_nope, b.q_pe, ckv, kpe, summaries)
+    dec.close()
+
+
+def test_two_decoders_and_row_calls_at_once():
+    """Decoders of their own on two streams, rows written and read on a third."""
+    rng = rng_of(58)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    batches = [Batch(rng, [3000, 200, 17], 16, 32), Batch(rng, [900, 1200], 128, 64)]
+    decs = [b.decoder() for b in batches]
+    x = torch.from_numpy(rows_of(rng, 500)).to(torch.bfloat16).cuda()
+    cache = torch.zeros(32, 16, 304, dtype=torch.uint8, device="cuda")
+    slots = torch.arange(500, device="cuda")
+    ckv, pe = torch.zeros(500, 512, device="cuda"), torch.zeros(500, 64, device="cuda")
+    idx, start, rows = torch.arange(32, dtype=torch.int32, device="cuda"), i32([0]), i32([0, 500])
+    indptr = i32([0, 32])
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            outs[i].append(decs[i].run_q4(batches[i].q_nope, batches[i].q_pe, batches[i].cache, out_dtype=torch.float32,
+                                          stream=streams[i]))
+        mla.mla_quantize_append(x[:, :512], x[:, 512:], slots, cache, stream=streams[2])
+        mla.mla_read_cache(cache, None, indptr, idx, start, rows, ckv, pe, stream=streams[2])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_decode(batches[i], *outs[i][0])
+        for o, l in outs[i][1:]:
+            assert torch.equal(o, outs[i][0][0]) and torch.equal(l, outs[i][0][1])
+        decs[i].check_status()
+        decs[i].close()
+    want = O.unpack(O.pack(f64(x)))
+    np.testing.assert_array_equal(np.concatenate([f64(ckv), f64(pe)], 1), want)
+
+
+def test_decode_of_rows_written_out_of_place():
+    """Exponents and shifts that no row of mla_quantize_append has: numbers, and no error."""
+    rng = rng_of(59)
+    for H in (16, 32, 128):
+        b = Batch(rng, [300, 40], H, 32)
+        b.cache = torch.from_numpy(rng.integers(0, 256, (b.pages, 32, 304)).astype(np.uint8)).cuda()
+        dec = b.decoder()
+        dec.run_q4(b.q_nope, b.q_pe, b.cache)
+        dec.check_status()
+        dec.close()
