@@ -101,7 +101,7 @@ struct Shape {
   static constexpr int kTokWarp = kT / kTileWarps;         // rows that a warp expands, of one page
   // registers a thread at launch, then by role
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kRegsSoftmax = kRows == 32 ? 88 : 80, kRegsExpand = kRows == 32 ? 72 : 80;
+  static constexpr int kRegsSoftmax = kRows == 32 ? 96 : 80, kRegsExpand = kRows == 32 ? 72 : 80;
   static constexpr int kRegsIssue = 24;
   static_assert(32 * (kSoftmaxWarps * kRegsSoftmax + kExpandWarps * kRegsExpand + 4 * kRegsIssue) <= kThreads * kRegs, "registers");
   // p reaches 2^kTop: the reference is set to leave kSlack of that, and moves when it is used up
@@ -315,8 +315,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 struct Cursor {
   int ui, tile, tiles;      // unit, tile of the unit
   int tok_begin, tok_end, page_base;
-  __device__ __forceinline__ void read(const WorkUnit* units) {
-    const WorkUnit u = units[ui];
+  __device__ __forceinline__ void set(const WorkUnit& u) {
     tok_begin = u.tok_begin;
     tok_end = u.tok_end;
     page_base = u.page_base;
@@ -328,15 +327,13 @@ struct Cursor {
   __device__ __forceinline__ bool next(const WorkUnit* units, int end) {
     if (++tile < tiles) return true;
     if (++ui >= end) return false;
-    read(units);
+    set(units[ui]);
     return true;
   }
 };
 
 template <int kRows, bool kOutF32>
 __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(const DecodeArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using S = Shape<kRows>;
   constexpr int kJ = S::kJ, kSoftmaxWarps = S::kSoftmaxWarps, kTileWarps = S::kTileWarps, kIssueWarp = S::kIssueWarp, kTokWarp = S::kTokWarp;
   constexpr int kBufs = S::kBufs;
@@ -347,18 +344,22 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
-  const PlanDev prm = *a.params;
+  // The plan's arrays were uploaded before the kernel ahead on the stream began, so
+  // they may be read while that one ends; everything else is read after the wait.
   const int H = a.num_heads;
   const int groups = (H + 63) / 64;                 // CTAs to a worker (1 below kRows = 64)
   const int worker = blockIdx.x / groups, row0 = 64 * (blockIdx.x % groups);
-  const int u0 = worker < prm.n_workers ? a.worker_ptr[worker] : 0;
-  const int u1 = worker < prm.n_workers ? a.worker_ptr[worker + 1] : 0;
+  int u0 = a.worker_ptr[worker], u1 = a.worker_ptr[worker + 1];   // of a.n_workers + 1 entries
+  const PlanDev prm = *a.params;
+  if (worker >= prm.n_workers) u0 = u1 = 0;
+  WorkUnit unit0{};
+  if (u0 < u1) unit0 = a.units[u0];
   const int page_shift = 31 - __clz(prm.page_size);
 
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < S::kNumBars; ++i)
-      mbar_init(bar(i), i < S::kSFull0 || (i >= S::kRowsFree0 && i < S::kQReady) ? kTileWarps
+  if (threadIdx.x < S::kNumBars) {
+    if (threadIdx.x == 0) *abort_flag = 0;
+    const int i = threadIdx.x;
+    mbar_init(bar(i), i < S::kSFull0 || (i >= S::kRowsFree0 && i < S::kQReady) ? kTileWarps
                         : (i >= S::kSFree0 && i < S::kPReady0) || i == S::kQReady ? kSoftmaxWarps
                         : i >= S::kPReady0 && i < S::kPvDone0                     ? kSoftmaxWarps / 4
                                                                                   : 1);
@@ -377,6 +378,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     reinterpret_cast<uint2*>(sm + S::kOffTable)[threadIdx.x] = make_uint2(t[0], t[1]);
   }
   if (threadIdx.x < kRows) reinterpret_cast<float*>(sm + S::kOffRef)[threadIdx.x] = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == kIssueWarp) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
       Cursor at;
       at.ui = u0;
-      at.read(a.units);
+      at.set(unit0);
       bool more = true;
       int behind = 0;
       for (int g = 0;; ++g) {
@@ -511,23 +514,25 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       auto load_ckv = [&](const Rows& r, int i) {   // rows 2 i and 2 i + 1
         return __ldg(reinterpret_cast<const uint4*>(r.src + (2 * i + odd) * kQ4Row) + 4 * panel + pair);
       };
-      auto load_rest = [&](const Rows& r) {
+      auto load_meta = [&](const Rows& r) {
 #pragma unroll
         for (int i = 0; i < kTokWarp / 8; ++i) {
           shifts[i] = 0;
           if (8 * i + (lane >> 2) < r.n) shifts[i] = __ldg(reinterpret_cast<const uint16_t*>(r.src + (8 * i + (lane >> 2)) * kQ4Row + kQ4Meta) + pair);
         }
-        raw_pe = make_uint4(0, 0, 0, 0);
         meta_pe = 127 << 8;
+        if ((lane >> kPeShift) < r.n) meta_pe = __ldg(reinterpret_cast<const uint16_t*>(r.src + (lane >> kPeShift) * kQ4Row + kQ4Meta + 8));
+      };
+      auto load_pe = [&](const Rows& r) {
+        raw_pe = make_uint4(0, 0, 0, 0);
         if ((lane >> kPeShift) < r.n) {
-          const uint8_t* row = r.src + (lane >> kPeShift) * kQ4Row;
+          const uint8_t* codes = r.src + (lane >> kPeShift) * kQ4Row + kDCkv / 2;
           if constexpr (kTokWarp == 16) {
-            raw_pe = __ldg(reinterpret_cast<const uint4*>(row + kDCkv / 2) + (lane & 1));
+            raw_pe = __ldg(reinterpret_cast<const uint4*>(codes) + (lane & 1));
           } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + kDCkv / 2) + (lane & 3));
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(codes) + (lane & 3));
             raw_pe.x = v.x, raw_pe.y = v.y;
           }
-          meta_pe = __ldg(reinterpret_cast<const uint16_t*>(row + kQ4Meta + 8));
         }
       };
       auto load_part = [&](const Rows& r) {   // not all of a warp's rows: the others hold zeros
@@ -542,9 +547,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         uint32_t shift[kTokWarp / 8];
 #pragma unroll
         for (int i = 0; i < kTokWarp / 8; ++i) shift[i] = shifts[i];
-        const uint4 codes_pe = raw_pe;
         const uint32_t meta = meta_pe;
-        load_rest(next);
+        load_meta(next);
         // shifts past 11 lead to subnormal numbers, by a table
         uint32_t large = (meta & (meta << 1)) & 0x88u;
 #pragma unroll
@@ -571,10 +575,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           const uint2 t = table_of((meta >> (kTokWarp == 16 ? 4 * (lane & 1) : 2 * (lane & 2))) & 15);
           if constexpr (kTokWarp == 16) {
             const int at = ((2 * (lane & 1)) ^ ((row >> 1) & 3)) << 4;
-            *reinterpret_cast<uint4*>(pe + at) = expand16(t, codes_pe.x, codes_pe.y);
-            *reinterpret_cast<uint4*>(pe + (at ^ 16)) = expand16(t, codes_pe.z, codes_pe.w);
+            *reinterpret_cast<uint4*>(pe + at) = expand16(t, raw_pe.x, raw_pe.y);
+            *reinterpret_cast<uint4*>(pe + (at ^ 16)) = expand16(t, raw_pe.z, raw_pe.w);
           } else {
-            *reinterpret_cast<uint4*>(pe + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) = expand16(t, codes_pe.x, codes_pe.y);
+            *reinterpret_cast<uint4*>(pe + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) = expand16(t, raw_pe.x, raw_pe.y);
           }
           if ((lane & ((1 << kPeShift) - 1)) == 0) sm[S::exp_at(g % kBufs, row)] = static_cast<unsigned char>(meta >> 8);
         };
@@ -586,12 +590,14 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (blockIdx.x == 0 && ew == 0 && g + 1 == g_q4_stall) return;
 #endif
         if (lane == 0) mbar_arrive(bar(S::kKFull0 + g % kBufs));
+        load_pe(next);
         if (!whole) load_part(next);
       };
       {
         const Rows rows = rows_of(group);
         load_part(rows);
-        load_rest(rows);
+        load_meta(rows);
+        load_pe(rows);
       }
       for (int g = group; g < tiles; g += S::kGroups) {
         // the buffer was read by P . V of g - kBufs
@@ -608,47 +614,58 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     const int tok = 32 * q + lane;
     float* refs = reinterpret_cast<float*>(sm + S::kOffRef) + kJ * cg;
     float* red = reinterpret_cast<float*>(sm + S::kOffRed) + 4 * cg * kJ;   // of the four warps of these query rows
-    // ---- the query of a unit, a few rows a warp ----
-    auto put_query = [&](int ui) {
-      const size_t first_row = static_cast<size_t>(a.units[ui].req) * H + row0;
-      float* out = reinterpret_cast<float*>(sm + S::kOffScale) + ((ui - u0) & 1) * kRows;
+    // ---- the query of a unit, a few rows a warp, two at a time ----
+    auto put_query = [&](int req, int parity) {
+      constexpr int kOwn = kRows / kSoftmaxWarps;
+      float* out = reinterpret_cast<float*>(sm + S::kOffScale) + parity * kRows;
 #pragma unroll 1
-      for (int k = 0; k < kRows / kSoftmaxWarps; ++k) {
-        const int r = warp * (kRows / kSoftmaxWarps) + k;
-        uint32_t w[9] = {};   // dims 16 lane .. + 15 of q_nope, 2 lane and + 1 of q_pe
-        if (row0 + r < H) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_nope) + (first_row + r) * kDCkv + 16 * lane);
-          const uint4 v0 = src[0], v1 = src[1];
-          w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w, w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
-          w[8] = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q_pe) + (first_row + r) * kDKpe)[lane];
+      for (int k = 0; k < kOwn; k += 2) {
+        uint32_t w[2][9];   // dims 16 lane .. + 15 of q_nope, 2 lane and + 1 of q_pe
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = row0 + warp * kOwn + k + i;
+#pragma unroll
+          for (int j = 0; j < 9; ++j) w[i][j] = 0;
+          if (r < H) {
+            const size_t row = static_cast<size_t>(req) * H + r;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_nope) + row * kDCkv + 16 * lane);
+            const uint4 v0 = src[0], v1 = src[1];
+            w[i][0] = v0.x, w[i][1] = v0.y, w[i][2] = v0.z, w[i][3] = v0.w;
+            w[i][4] = v1.x, w[i][5] = v1.y, w[i][6] = v1.z, w[i][7] = v1.w;
+            w[i][8] = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q_pe) + row * kDKpe)[lane];
+          }
         }
-        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 9; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-        const uint32_t top = __reduce_max_sync(~0u, max(m >> 16, m & 0xffffu));   // bits of the largest magnitude
-        const int e = top == 0 ? 0 : min(max(7 - (static_cast<int>(top >> 7) - 127), -100), 100);
-        const float up = pow2(e);
-        uint32_t hi[9], lo[9];
+        for (int i = 0; i < 2; ++i) {
+          const int r = warp * kOwn + k + i;
+          uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 9; ++i)
-          split_query(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up, hi[i], lo[i]);
+          for (int j = 0; j < 9; ++j) m = __vmaxu2(m, w[i][j] & 0x7fff7fffu);
+          const uint32_t top = __reduce_max_sync(~0u, max(m >> 16, m & 0xffffu));   // bits of the largest magnitude
+          const int e = top == 0 ? 0 : min(max(7 - (static_cast<int>(top >> 7) - 127), -100), 100);
+          const float up = pow2(e);
+          uint32_t hi[9], lo[9];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t* c = t ? lo : hi;
-          const int row = t * kRows + r;
-          *reinterpret_cast<uint4*>(sm + S::kOffQ + (lane >> 3) * S::kQPanel + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
-              make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
-          *reinterpret_cast<uint16_t*>(sm + S::kOffQPe + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7)) =
-              static_cast<uint16_t>(c[8]);
+          for (int j = 0; j < 9; ++j)
+            split_query(__uint_as_float(w[i][j] << 16) * up, __uint_as_float(w[i][j] & 0xffff0000u) * up, hi[j], lo[j]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t* c = t ? lo : hi;
+            const int row = t * kRows + r;
+            *reinterpret_cast<uint4*>(sm + S::kOffQ + (lane >> 3) * S::kQPanel + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+                make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+            *reinterpret_cast<uint16_t*>(sm + S::kOffQPe + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7)) =
+                static_cast<uint16_t>(c[8]);
+          }
+          // an infinite or NaN query has NaN scores
+          if (lane == 0) out[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff) : pow2(-e);
         }
-        // an infinite or NaN query has NaN scores
-        if (lane == 0) out[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff) : pow2(-e);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(S::kQReady));
     };
-    if (u0 < u1) put_query(u0);
+    if (u0 < u1) put_query(unit0.req, 0);
     int g = 0;
     for (int ui = u0; ui < u1; ++ui) {
       const WorkUnit u = a.units[ui];
@@ -795,11 +812,24 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (lane == 0) mbar_arrive(bar(S::kPReady0 + q));
       }
       // the next unit's query: every score of this one is made
-      if (ui + 1 < u1) put_query(ui + 1);
-      // ---- epilogue: the sums over the unit's tokens of all lanes and quadrants ----
+      if (ui + 1 < u1) put_query(a.units[ui + 1].req, (ui + 1 - u0) & 1);
+      // ---- epilogue: the sums over the unit's tokens of all lanes and quadrants; the second
+      // ones are exchanged where these query rows had their P, which no MMA reads any more ----
       const bool split = u.out_slot >= 0;
-      const float sx = warp_reduce<false>(lx);
-      if ((lane & (32 / kJ - 1)) == 0) red[q * kJ + lane * kJ / 32] = sx;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) ld[j] = lx[j] - ld[j];   // of what P stands for
+      const float sx = warp_reduce<false>(lx), sr = warp_reduce<false>(ld);
+      wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + 3, (g - 1) / kBufs);
+      tc_fence_after();
+      auto shared_sum = [&](int from, int j) -> float* {   // of quadrant `from`, row j
+        const int at = from * kJ + j;                       // 4 kJ floats, in the first terms of tokens 0 ..
+        const int t = at / (kJ / 4), chunk = kRows == 64 ? cg ^ ((t >> 1) & 3) : kRows == 32 ? cg ^ (t & 7) : (t >> 1) & 3;
+        return reinterpret_cast<float*>(sm + S::kOffP + t * S::kPRow + (chunk << 4) + (kRows == 16 ? 8 * cg : 0)) + at % (kJ / 4);
+      };
+      if ((lane & (32 / kJ - 1)) == 0) {
+        red[q * kJ + lane * kJ / 32] = sx;
+        *shared_sum(q, lane * kJ / 32) = sr;
+      }
       named_bar_sync(1 + cg, 128);
       if (q == 0 && lane < kJ && row0 + kJ * cg + lane < H) {
         const int h = row0 + kJ * cg + lane;
@@ -808,20 +838,12 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
         else a.lse[static_cast<size_t>(u.req) * H + h] = lse;
       }
-      named_bar_sync(1 + cg, 128);
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) lx[j] -= ld[j];   // of what P stands for
-      const float sr = warp_reduce<false>(lx);
-      if ((lane & (32 / kJ - 1)) == 0) red[q * kJ + lane * kJ / 32] = sr;
-      named_bar_sync(1 + cg, 128);
       float inv[kJ];
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
-        const float s = (red[j] + red[kJ + j]) + (red[2 * kJ + j] + red[3 * kJ + j]);
+        const float s = (*shared_sum(0, j) + *shared_sum(1, j)) + (*shared_sum(2, j) + *shared_sum(3, j));
         inv[j] = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
       }
-      wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + 3, (g - 1) / kBufs);
-      tc_fence_after();
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
         uint32_t o[kJ];
