@@ -721,12 +721,13 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #pragma unroll
         for (int j = 1; j < kJ; ++j) top = fmaxf(top, z[j]);
         // ---- the reference moves: the four warps of these query rows together ----
-        if (bar_any(1 + cg, 128, first || top > S::kTop)) {
+        uint32_t moved = 0;   // rows whose reference moves
+        float factor = 1.f;   // lane j: of row j
+        const bool moves = bar_any(1 + cg, 128, first || top > S::kTop);
+        if (moves) {
           const float most = warp_reduce<true>(z);
           if ((lane & (32 / kJ - 1)) == 0) red[q * kJ + lane * kJ / 32] = most;
           named_bar_sync(1 + cg, 128);
-          uint32_t moved = 0;
-          float mine = 1.f;   // lane j: the factor of row j
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             const float m = fmaxf(fmaxf(red[j], red[kJ + j]), fmaxf(red[2 * kJ + j], red[3 * kJ + j]));
@@ -739,30 +740,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
               const float alpha = fast_exp2(-up);
               lx[j] *= alpha;
               ld[j] *= alpha;
-              if (lane == j) mine = alpha;
+              if (lane == j) factor = alpha;
             }
             if (q == 0 && lane == j) refs[j] -= up;
           }
-          if (moved) {   // their columns of O, a row at a time: few move at once
-            wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + 3, (g - 1) / kBufs);
-            tc_fence_after();
-            do {
-              const int j = __ffs(moved) - 1;
-              moved &= moved - 1;
-              constexpr int kCols = S::kSide ? 12 : 4;
-              uint32_t o[kCols];
-#pragma unroll
-              for (int i = 0; i < kCols; ++i) tmem_ld(lane_addr + (i & 3) * S::kOBlock + (i >> 2) * kRows + kJ * cg + j, o[i]);
-              const float alpha = __shfl_sync(~0u, mine, j);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < kCols; ++i)
-                tmem_st(lane_addr + (i & 3) * S::kOBlock + (i >> 2) * kRows + kJ * cg + j, __float_as_uint(__uint_as_float(o[i]) * alpha));
-            } while (moved);
-            tmem_st_wait();
-            tc_fence_before();
-          }
-          named_bar_sync(1 + cg, 128);
         }
         // ---- p and its terms ----
         constexpr int kTerms = S::kSide ? 3 : 2;
@@ -796,6 +777,28 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
         }
         if (g > 0) wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + q, (g - 1) / kBufs);   // P . V of the tile before has read these rows of P
+        if (moves) {
+          if (moved) {   // their columns of O, a row at a time: few move at once
+            wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + 3, (g - 1) / kBufs);
+            tc_fence_after();
+            do {
+              const int j = __ffs(moved) - 1;
+              moved &= moved - 1;
+              constexpr int kCols = S::kSide ? 12 : 4;
+              uint32_t o[kCols];
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) tmem_ld(lane_addr + (i & 3) * S::kOBlock + (i >> 2) * kRows + kJ * cg + j, o[i]);
+              const float alpha = __shfl_sync(~0u, factor, j);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < kCols; ++i)
+                tmem_st(lane_addr + (i & 3) * S::kOBlock + (i >> 2) * kRows + kJ * cg + j, __float_as_uint(__uint_as_float(o[i]) * alpha));
+            } while (moved);
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          named_bar_sync(1 + cg, 128);   // P is signalled once O and the references are right for all
+        }
         unsigned char* prow = sm + S::kOffP + tok * S::kPRow;
 #pragma unroll
         for (int i = 0; i < kTerms; ++i) {
