@@ -44,8 +44,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) merge_shares_kernel(co
     const int h = item % per_entry / (kDCkv / 8) * rows + row, d = item % (kDCkv / 8) * 8 + 4 * half;
     float M = -INFINITY, W = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float m, float w, const float4& o) {   // a state of weight w
-      if (m == -INFINITY) return;
+    // A state of weight w.  Not one without tokens (w = 0): m would not be a number above
+    // -inf.  A NaN share leaves M as it was, maybe -inf, and makes W NaN.
+    auto add = [&](float m, float w, const float4& o) {
       const float top = fmaxf(M, m);
       const float x = __expf(M - top), y = __expf(m - top);   // a NaN stays one in W and the sums
       sum = make_float4(sum.x * x + o.x * y, sum.y * x + o.y * y, sum.z * x + o.z * y, sum.w * x + o.w * y);
@@ -66,7 +67,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) merge_shares_kernel(co
           }
         }
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) add(l[j], 1.f, o[j]);
+        for (int j = 0; j < kAhead; ++j)
+          if (l[j] != -INFINITY) add(l[j], 1.f, o[j]);
       }
     }
     if (groups > 1) {

@@ -805,6 +805,27 @@ def test_decode_nan_in_a_split_request(H):
     dec.close()
 
 
+@pytest.mark.parametrize("H, n", [(1, 900), (16, 900), (16, 2000), (40, 1500), (128, 1100)])
+def test_decode_nan_in_any_share(H, n):
+    """The same with few shares, each of which is read by threads of its own: the row
+    at the ends of every tile in turn."""
+    b = Batch(rng_of(57, H, n), [n], H, 64)
+    dec = b.decoder()
+    assert dec.info()["num_partial_slots"] > 1
+    for t in sorted({0, n - 1} | set(range(127, n, 128)) | set(range(128, n, 128))):
+        slot = int(b.ids[b.indptr[0] + t // 64]) * 64 + t % 64
+        flat = b.cache.view(-1, 304)
+        was = int(flat[slot, 297])
+        flat[slot, 297] = 255
+        out, lse = dec.run_q4(b.q_nope, b.q_pe, b.cache, out_dtype=torch.float32)
+        assert out.isnan().all() and lse.isnan().all(), t
+        flat[slot, 297] = was
+    out, lse = dec.run_q4(b.q_nope, b.q_pe, b.cache, out_dtype=torch.float32)
+    dec.check_status()
+    check_decode(b, out, lse)
+    dec.close()
+
+
 @pytest.mark.parametrize("H, lens", [(1, [20000, 0, 150, 9000]), (20, [30000]), (64, [9000] * 4), (100, [5000, 5000]), (128, [12000, 1])])
 def test_decode_many_shares(H, lens):
     run_check(Batch(rng_of(56, H), lens, H, 64), torch.bfloat16)
