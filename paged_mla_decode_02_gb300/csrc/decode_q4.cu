@@ -238,22 +238,9 @@ __device__ __forceinline__ void split_query(float x0, float x1, uint32_t& hi, ui
 __device__ __forceinline__ uint32_t expand4(uint2 table, uint32_t select, uint32_t signs) {
   return __byte_perm(table.x, table.y, select) | (signs & 0x80808080u);
 }
-// w >> 16 and w << 4 by multiplication: what is left of the expansion is bound by
-// the integer pipe, and these run on another.
-__device__ __forceinline__ uint32_t upper_half(uint32_t w) {
-  uint32_t d;
-  asm("mul.hi.u32 %0, %1, 65536;" : "=r"(d) : "r"(w));
-  return d;
-}
-__device__ __forceinline__ uint32_t times16(uint32_t w) {
-  uint32_t d;
-  asm("mul.lo.u32 %0, %1, 16;" : "=r"(d) : "r"(w));
-  return d;
-}
 __device__ __forceinline__ uint4 expand16(uint2 table, uint32_t w0, uint32_t w1) {
   const uint32_t a = w0 & 0x77777777u, b = w1 & 0x77777777u;
-  return make_uint4(expand4(table, a, w0), expand4(table, upper_half(a), times16(w0)), expand4(table, b, w1),
-                    expand4(table, upper_half(b), times16(w1)));
+  return make_uint4(expand4(table, a, w0), expand4(table, a >> 16, w0 << 4), expand4(table, b, w1), expand4(table, b >> 16, w1 << 4));
 }
 // e4m3 codes of magnitude * 2^(6 - shift): up to a shift of 11 all are normal
 // numbers, whose exponent field starts at bit 3.
