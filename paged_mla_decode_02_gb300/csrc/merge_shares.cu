@@ -26,10 +26,9 @@ constexpr int kMinRows = 16;   // of a block
 
 template <bool kOutF32>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) merge_shares_kernel(const MergeArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ float4 s_sum[kThreads];
   __shared__ float2 s_mw[kThreads];
+  // The plan's arrays were uploaded before the decode ahead began: read while it ends.
   const int H = a.num_heads, n_merge = a.params->n_merge;
   // rows of a block: a power of two that leaves a group for every kAhead shares
   const int shares = n_merge > 0 ? (a.params->n_slots + n_merge - 1) / n_merge : 0;
@@ -39,8 +38,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) merge_shares_kernel(co
   const int row_blocks = (H + rows - 1) / rows;
   const int per_entry = row_blocks * (kDCkv / 8);
   const int half = threadIdx.x & 1, row = (threadIdx.x >> 1) % rows, group = (threadIdx.x >> 1) / rows;
+  MergeEntry me{};
+  if (static_cast<int>(blockIdx.x) < n_merge * per_entry) me = a.merge[blockIdx.x / per_entry];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int item = blockIdx.x; item < n_merge * per_entry; item += gridDim.x) {
-    const MergeEntry me = a.merge[item / per_entry];
+    if (item != static_cast<int>(blockIdx.x)) me = a.merge[item / per_entry];
     const int h = item % per_entry / (kDCkv / 8) * rows + row, d = item % (kDCkv / 8) * 8 + 4 * half;
     float M = -INFINITY, W = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
