@@ -37,12 +37,24 @@
 // both: the row of a small E_t may weigh much and hold little, so that its p is
 // rounded coarsely, or away.
 //
-// Roles: 8 or 16 warps expand tiles, up to a tile ahead of the products, with the
-// raw rows of the next one on their way into registers; a warp for each 32 tokens
-// and 8 or 16 query rows makes P; one issues the MMAs, scores of tile g + 1 before P . V
-// of tile g.  Registers are dealt out by role.  Waits are bounded (2 s): a warp that gives up says so, and
+// Roles, with registers dealt out to each: 8 or 16 warps expand tiles into two or
+// three buffers, with the raw rows of the next tile on their way into registers; a
+// warp for each 32 tokens and 8 or 16 query rows makes P; one warp issues the MMAs of
+// the scores, one those of P . V; one looks up where the rows are, four tiles ahead,
+// and asks for them into L2.  Waits are bounded (2 s): a warp that gives up says so, and
 // goes on without waiting, so that the named barriers and commits of the others
 // still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is recorded.
+//
+// What bounds it (device time from a graph, cold L2): with 16 query rows the way of
+// a tile through its buffer.  4 requests of 131072 tokens take 61.5 us, 2.6 TB/s, 27
+// tiles a CTA at 1.5 to 1.9 us each; a buffer is held for the expansion (about 3700
+// cycles of a warp, among 28 warps that take 54 % of the issue slots), the scores
+// (1250), P (1700) and P . V (1700), and shared memory has room for three.  Loads or
+// stores left out gain 2 us, the arithmetic of P nothing.  With 64 rows a tile takes
+// 2.9 us (64 requests of 4096 tokens, 128 heads: 102.7 us; 72 GFLOP, 0.71 PFLOP/s):
+// both products read the tile and their other operand through shared memory, 2700
+// cycles of 128 bytes in 5700, next to the expansion's stores and its 4500
+// instructions.  All MMAs left out it is 82 us, half of the expansion left out 95.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -236,7 +248,9 @@ __device__ __forceinline__ void split_query(float x0, float x1, uint32_t& hi, ui
 // Four codes to four e4m3 numbers: the magnitudes' indices select bytes of the
 // table, the signs (in place already) go on top.
 __device__ __forceinline__ uint32_t expand4(uint2 table, uint32_t select, uint32_t signs) {
-  return __byte_perm(table.x, table.y, select) | (signs & 0x80808080u);
+  uint32_t d;   // of select's low 16 bits; __byte_perm would mask them once more
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(table.x), "r"(table.y), "r"(select));
+  return d | (signs & 0x80808080u);
 }
 __device__ __forceinline__ uint4 expand16(uint2 table, uint32_t w0, uint32_t w1) {
   const uint32_t a = w0 & 0x77777777u, b = w1 & 0x77777777u;

@@ -813,6 +813,7 @@ class MLADecoder:
         self.handle = mla_plan_create(max_batch, num_heads, kernel)
         self._kv_indices = None
         self.page_size = None
+        self._rows = 0                    # query rows of the planned batch
 
     def plan(self, kv_indptr, kv_indices, kv_len, page_size: int, sm_scale: float,
              head_dim_ckv: int = 512, head_dim_kpe: int = 64, stream=None, q_len: int = 0) -> None:
@@ -827,6 +828,7 @@ class MLADecoder:
                             head_dim_ckv, head_dim_kpe, page_size, sm_scale, stream)
         self.q_len = int(q_len)
         self.page_size = int(page_size)
+        self._rows = len(kv_len) * max(1, self.q_len) * self.num_heads
         self._kv_indices = kv_indices     # keep the borrowed page table alive
 
     def run(self, q_nope, q_pe, ckv_cache, kpe_cache, out=None, lse=None,
@@ -842,9 +844,13 @@ class MLADecoder:
         return out, lse
 
     def run_q4(self, q_nope, q_pe, cache, out=None, lse=None, out_dtype=None, stream=None):
-        """run() over a 4-bit cache, for a decoder made with kernel="q4"."""
+        """run() over a 4-bit cache, for a decoder made with kernel="q4".  Rows of
+        q_nope behind the planned batch are not read, theirs of out and lse left as
+        they were."""
         import torch
         lead = tuple(q_nope.shape[:-1])
+        if q_nope.numel() < 512 * self._rows:
+            raise ValueError(f"q_nope must hold the plan's {self._rows} query rows, got {lead}")
         if out is None:
             out = _empty(lead + (512,), out_dtype or torch.bfloat16, q_nope.device, stream)
         if lse is None:

@@ -601,6 +601,7 @@ def test_decode_refuses():
                        ((b.q_nope, b.q_pe, b.cache.view(torch.int8)), "cache must be"),
                        ((b.q_nope, b.q_pe, b.cache.view(-1, 16, 304)), "pages of 16"),
                        ((b.q_nope, b.q_pe[..., :32].contiguous(), b.cache), "q_pe"),
+                       ((b.q_nope[:, :15].contiguous(), b.q_pe[:, :15].contiguous(), b.cache), "plan's 16 query rows"),
                        ((b.q_nope.float(), b.q_pe, b.cache), "q_pe must have")):
         with pytest.raises(ValueError, match=match):
             dec.run_q4(*bad)
@@ -616,6 +617,24 @@ def test_decode_refuses():
 # ---------------------------------------------------------------------------
 # Streams, graphs, runs together
 # ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("H, q_len, lens", [(16, 1, [300, 0, 77]), (128, 1, [5000, 40]), (16, 4, [900, 130])])
+def test_rows_behind_the_batch_stay(H, q_len, lens):
+    """Buffers for more requests than the plan has: a padded batch."""
+    b = Batch(rng_of(58, H, q_len), lens, H, 32, q_len)
+    B, more = len(lens), 3
+    q_nope, q_pe = (torch.full((B + more, *t.shape[1:]), math.nan, dtype=t.dtype, device="cuda") for t in (b.q_nope, b.q_pe))
+    q_nope[:B], q_pe[:B] = b.q_nope, b.q_pe
+    out = torch.full(q_nope.shape, 7.0, dtype=torch.float32, device="cuda")
+    lse = torch.full(q_nope.shape[:-1], 7.0, dtype=torch.float32, device="cuda")
+    dec = mla.MLADecoder((B + more) * q_len, H, kernel="q4")
+    b.plan(dec)
+    dec.run_q4(q_nope, q_pe, b.cache, out=out, lse=lse)
+    dec.check_status()
+    check_decode(b, out[:B], lse[:B])
+    assert (out[B:] == 7).all() and (lse[B:] == 7).all()
+    dec.close()
+
 
 def test_calls_on_another_stream():
     rng = rng_of(51)
