@@ -420,8 +420,21 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (lane < kTileWarps) reinterpret_cast<uint64_t*>(sm + S::kOffRows)[g % S::kRowsAhead * kTileWarps + lane] = r;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::kRowsFull0 + g % S::kRowsAhead));
-        if (more) more = at.next(a.units, u1);
-        else if (++behind == S::kGroups) break;
+        if (more) {
+          const int ui = at.ui;
+          more = at.next(a.units, u1);
+          // Another unit's: its query will be wanted too.  Of 64 rows (72 KB; 0.5 to 1 % of
+          // batches of several units a worker), fewer come as fast by themselves, and their
+          // tiles are found too quickly for a warp with more to do (2 us of 48).
+          if (kRows == 64 && more && at.ui != ui) {
+            const size_t row = static_cast<size_t>(a.units[at.ui].req) * H + row0;
+            const int n = min(kRows, H - row0);
+            for (int i = lane; i < n; i += 32) bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q_nope) + (row + i) * kDCkv, 2 * kDCkv);
+            if (lane == 0) bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q_pe) + row * kDKpe, 2 * kDKpe * n);
+          }
+        } else if (++behind == S::kGroups) {
+          break;
+        }
       }
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
     } else if (warp <= kIssueWarp + 1) {
@@ -815,14 +828,14 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::kPReady0 + q));
       }
-      // the next unit's query: every score of this one is made
-      if (ui + 1 < u1) put_query(a.units[ui + 1].req, (ui + 1 - u0) & 1);
       // ---- epilogue: the sums over the unit's tokens of all lanes and quadrants; the second
       // ones are exchanged where these query rows had their P, which no MMA reads any more ----
       const bool split = u.out_slot >= 0;
 #pragma unroll
       for (int j = 0; j < kJ; ++j) ld[j] = lx[j] - ld[j];   // of what P stands for
       const float sx = warp_reduce<false>(lx), sr = warp_reduce<false>(ld);
+      // the next unit's query: every score of this one is made
+      if (ui + 1 < u1) put_query(a.units[ui + 1].req, (ui + 1 - u0) & 1);
       wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + 3, (g - 1) / kBufs);
       tc_fence_after();
       auto shared_sum = [&](int from, int j) -> float* {   // of quadrant `from`, row j
@@ -835,19 +848,23 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         *shared_sum(q, lane * kJ / 32) = sr;
       }
       named_bar_sync(1 + cg, 128);
-      if (q == 0 && lane < kJ && row0 + kJ * cg + lane < H) {
+      // lane j joins the sums of row j: little code, which a unit's first epilogue waits for
+      float inverse = 0.f;
+      if (lane < kJ) {
+        const float s = (*shared_sum(0, lane) + *shared_sum(1, lane)) + (*shared_sum(2, lane) + *shared_sum(3, lane));
+        inverse = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
         const int h = row0 + kJ * cg + lane;
-        const float s = (red[lane] + red[kJ + lane]) + (red[2 * kJ + lane] + red[3 * kJ + lane]);
-        const float lse = (log2f(s) - refs[lane]) * kLn2;
-        if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
-        else a.lse[static_cast<size_t>(u.req) * H + h] = lse;
+        if (q == 0 && h < H) {
+          const float sum = (red[lane] + red[kJ + lane]) + (red[2 * kJ + lane] + red[3 * kJ + lane]);
+          const float lse = (log2f(sum) - refs[lane]) * kLn2;
+          if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
+          else a.lse[static_cast<size_t>(u.req) * H + h] = lse;
+        }
       }
+      __syncwarp();
       float inv[kJ];
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const float s = (*shared_sum(0, j) + *shared_sum(1, j)) + (*shared_sum(2, j) + *shared_sum(3, j));
-        inv[j] = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
-      }
+      for (int j = 0; j < kJ; ++j) inv[j] = __shfl_sync(~0u, inverse, j);
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
         uint32_t o[kJ];
