@@ -61,4 +61,27 @@ __device__ __forceinline__ float q4_unit(const Q4Meta& m, int group) {
   return pow2(min(26 + e - 127 - m.shift(group), 127));
 }
 
+
+// A group's magnitudes as bf16 numbers, which are the upper halves of the fp32
+// ones: the values 2^-47 .. 6 * 2^63 are exact in both.  Split into the numbers'
+// upper and lower bytes, which the indices select as they do in the decode.
+struct Q4Table {
+  uint2 hi, lo;
+};
+__device__ __forceinline__ Q4Table q4_table(const Q4Meta& m, int group) {
+  // 2^(E - k) has the exponent field f; index 1 is half of it, 2 itself, 3 1.5 times ..
+  const uint32_t f = min(max(m.exp_byte() - m.shift(group), 1), 250), two = f * 0x00800080u;
+  uint32_t w[4] = {(f - 1) << 23, two + 0x00400000u, two + 0x00c00080u, two + 0x01400100u};
+  if (m.exp_byte() == kQ4NanExp) w[0] = w[1] = w[2] = w[3] = 0x7fff7fffu;
+  return {make_uint2(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531)),
+          make_uint2(__byte_perm(w[0], w[1], 0x6420), __byte_perm(w[2], w[3], 0x6420))};
+}
+// The bf16 numbers of a word's 8 dims, two to a word.
+__device__ __forceinline__ uint4 q4_bf16x8(const Q4Table& t, uint32_t w) {
+  const uint32_t a = w & 0x77777777u;
+  const uint32_t h0 = __byte_perm(t.hi.x, t.hi.y, a) | (w & 0x80808080u), l0 = __byte_perm(t.lo.x, t.lo.y, a);
+  const uint32_t h1 = __byte_perm(t.hi.x, t.hi.y, a >> 16) | ((w << 4) & 0x80808080u), l1 = __byte_perm(t.lo.x, t.lo.y, a >> 16);
+  return make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140), __byte_perm(l1, h1, 0x7362));
+}
+
 }  // namespace mla

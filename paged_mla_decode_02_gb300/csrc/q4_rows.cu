@@ -254,12 +254,24 @@ __global__ void __launch_bounds__(kThreads) read_kernel(ReadArgs a) {
     const Q4Meta m{*reinterpret_cast<const uint4*>(row + kQ4Meta)};
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      float x[8];
-      q4_expand(w[i], x);
-      const float unit = q4_unit(m, 2 * i + (j >> 2));
+      const int group = 2 * i + (j >> 2);
+      if constexpr (std::is_same<T, __half>::value) {   // whose range the values may leave
+        float x[8];
+        q4_expand(w[i], x);
+        const float unit = q4_unit(m, group);
 #pragma unroll
-      for (int d = 0; d < 8; ++d) x[d] *= unit;
-      put(i, x);
+        for (int d = 0; d < 8; ++d) x[d] *= unit;
+        put(i, x);
+      } else {
+        const uint4 v = q4_bf16x8(q4_table(m, group), w[i]);
+        uint4* dst = reinterpret_cast<uint4*>(i < kChunks - 1 ? ckv + 8 * kLanes * i : kpe);
+        if constexpr (sizeof(T) == 2) {
+          *dst = v;
+        } else {
+          dst[0] = make_uint4(v.x << 16, v.x & 0xffff0000u, v.y << 16, v.y & 0xffff0000u);
+          dst[1] = make_uint4(v.z << 16, v.z & 0xffff0000u, v.w << 16, v.w & 0xffff0000u);
+        }
+      }
     }
   } else if constexpr (kKind == Kind::kFp8) {
     uint2 w[kChunks];
