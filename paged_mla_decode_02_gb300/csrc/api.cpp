@@ -254,6 +254,11 @@ mla_status_t mla_plan_create(int max_batch, int num_heads, int kernel, mla_plan_
     return MLA_ERR_CUDA;
   }
   p->n_workers = workers_for(p->kernel, p->num_sms, num_heads);
+  if (p->kernel == MLA_KERNEL_Q4 && (e = prepare_decode_q4()) != cudaSuccess) {
+    delete p;
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
   if (p->kernel == MLA_KERNEL_TCGEN05 || p->kernel == MLA_KERNEL_PAIR) {
     int resident = 0;
     if ((e = p->kernel == MLA_KERNEL_PAIR ? decode_pair_max_workers(&resident) : decode_tc_max_workers(&resident)) !=
@@ -502,7 +507,7 @@ mla_status_t merge_shares(mla_plan_t plan, const DecodeArgs& a, bool out_f32, cu
   m.lse = a.lse;
   m.num_heads = plan->params.num_heads;
   m.merge_cap = plan->merge_cap;
-  const cudaError_t e = q4 ? launch_merge_shares(m, out_f32, s) : launch_merge(m, out_f32, s);
+  const cudaError_t e = q4 ? launch_merge_shares(m, out_f32, plan->num_sms, s) : launch_merge(m, out_f32, s);
   return e == cudaSuccess ? MLA_OK : cuda_fail(plan, e, "merge kernel launch");
 }
 
@@ -603,6 +608,11 @@ mla_status_t mla_decode_run_q4(mla_plan_t plan, const void* q_nope, const void* 
   if ((e = launch_decode_q4(a, out_f32, s)) != cudaSuccess) return cuda_fail(plan, e, "decode kernel launch");
   if (plan->prof_stop && (e = cudaEventRecord(plan->prof_stop, s)) != cudaSuccess)
     return cuda_fail(plan, e, "cudaEventRecord");
+  // A plan without split or empty requests has nothing to merge; a captured run may be
+  // replayed over one that has.
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusActive;
+  if (plan->params.n_merge == 0 && cudaStreamIsCapturing(s, &capture) == cudaSuccess && capture == cudaStreamCaptureStatusNone)
+    return MLA_OK;
   return merge_shares(plan, a, out_f32, s, true);
 }
 

@@ -923,9 +923,11 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 }
 
 template <int kRows, bool kOutF32>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(decode_q4_kernel<kRows, kOutF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<kRows>());
+}
+template <int kRows, bool kOutF32>
 cudaError_t launch(const DecodeArgs& a, int groups, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<kRows, kOutF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<kRows>());
-  if (e != cudaSuccess) return e;
   return launch_dependent(decode_q4_kernel<kRows, kOutF32>, a.n_workers / groups * groups, Shape<kRows>::kThreads, smem_bytes<kRows>(), 1, s, a);
 }
 
@@ -937,6 +939,13 @@ extern "C" int mla_test_set_q4_stall(int signal) {
   return static_cast<int>(cudaMemcpyToSymbol(g_q4_stall, &signal, sizeof(signal)));
 }
 #endif
+
+cudaError_t prepare_decode_q4() {
+  for (const cudaError_t e : {prepare<16, false>(), prepare<16, true>(), prepare<32, false>(), prepare<32, true>(), prepare<64, false>(),
+                              prepare<64, true>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
 
 int decode_q4_groups(int rows) { return (rows + 63) / 64; }
 

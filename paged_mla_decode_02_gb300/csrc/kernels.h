@@ -108,6 +108,7 @@ cudaError_t decode_pair_max_workers(int* workers);
 // Decode over a 4-bit cache (a.ckv: its rows; kpe and kv_scale unused): units
 // of 128-token tiles, partials as for the CTA-pair kernel.  decode_q4_groups
 // CTAs share a worker's units, 64 query rows each.
+cudaError_t prepare_decode_q4();   // once per device, before its launches
 int decode_q4_groups(int rows);
 cudaError_t launch_decode_q4(const DecodeArgs& a, bool out_f32, cudaStream_t s);
 
@@ -116,6 +117,6 @@ cudaError_t launch_decode_q4(const DecodeArgs& a, bool out_f32, cudaStream_t s);
 cudaError_t launch_merge(const MergeArgs& a, bool out_f32, cudaStream_t s);
 // The same after the 4-bit decode, whose plans cut a few requests of any number
 // of query rows into many shares.
-cudaError_t launch_merge_shares(const MergeArgs& a, bool out_f32, cudaStream_t s);
+cudaError_t launch_merge_shares(const MergeArgs& a, bool out_f32, int num_sms, cudaStream_t s);
 
 }  // namespace mla

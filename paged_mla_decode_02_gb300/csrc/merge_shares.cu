@@ -104,13 +104,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) merge_shares_kernel(co
 
 }  // namespace
 
-cudaError_t launch_merge_shares(const MergeArgs& a, bool out_f32, cudaStream_t s) {
+cudaError_t launch_merge_shares(const MergeArgs& a, bool out_f32, int num_sms, cudaStream_t s) {
   if (a.merge_cap <= 0) return cudaSuccess;
-  int sms = 0;
-  const cudaError_t e = current_sms(&sms);
-  if (e != cudaSuccess) return e;
   const long long items = static_cast<long long>(a.merge_cap) * (kDCkv / 8) * ((a.num_heads + kMinRows - 1) / kMinRows);
-  const int grid = static_cast<int>(items < kBlocksPerSm * sms ? items : kBlocksPerSm * sms);
+  const int grid = static_cast<int>(items < kBlocksPerSm * num_sms ? items : kBlocksPerSm * num_sms);
   return launch_dependent(out_f32 ? merge_shares_kernel<true> : merge_shares_kernel<false>, grid, kThreads, 0, 1, s, a);
 }
 

@@ -381,11 +381,12 @@ def mla_decode_run_q4(plan, q_nope, q_pe, cache, out, lse, stream=None, page_siz
     304] (see mla_decode.h); the plan's kernel is "q4"."""
     import torch
     lib = load_library()
-    _on_cuda("q_nope q_pe cache out lse", q_nope, q_pe, cache, out, lse)
+    names, tensors = "q_nope q_pe cache out lse", (q_nope, q_pe, cache, out, lse)
     device = torch.cuda.current_device()
-    for name, t in (("q_nope", q_nope), ("q_pe", q_pe), ("cache", cache), ("out", out), ("lse", lse)):
+    _on_cuda(names, *tensors)
+    for t in tensors:
         if t.get_device() != device:
-            raise ValueError(f"{name} must be on the current CUDA device")
+            raise ValueError(f"{names.split()[[x is t for x in tensors].index(True)]} must be on the current CUDA device")
     shape = cache.shape
     if cache.dtype != torch.uint8 or len(shape) != 3 or shape[2] != Q4_ROW_BYTES:
         raise ValueError(f"cache must be uint8 [num_pages, page_size, {Q4_ROW_BYTES}], got {cache.dtype} "
@@ -395,7 +396,7 @@ def mla_decode_run_q4(plan, q_nope, q_pe, cache, out, lse, stream=None, page_siz
     _check_queries(q_nope, q_pe, out, lse)
     st = lib.mla_decode_run_q4(plan, q_nope.data_ptr(), q_pe.data_ptr(), _dtype_code(q_nope, "q_nope"),
                                cache.data_ptr(), shape[0], out.data_ptr(), _dtype_code(out, "out"), lse.data_ptr(),
-                               _stream_handle(stream))
+                               _stream_handle(stream, device))
     if st != OK:
         _check(st, plan, "mla_decode_run_q4")
 
