@@ -92,7 +92,7 @@ typedef enum {
 /* Plan statistics, filled by mla_plan_info. */
 typedef struct {
   int32_t num_sms;            /* SMs of the plan's device */
-  int32_t num_workers;        /* persistent workers (CTA pairs for tcgen05, CTAs for mma.sync) */
+  int32_t num_workers;        /* persistent workers (CTA pairs for tcgen05, CTAs for mma.sync and the 4-bit kernel) */
   int32_t num_units;          /* work units (contiguous tile ranges of one request) */
   int32_t num_partial_slots;  /* split partial results written to the workspace */
   int32_t num_merge;          /* split and empty requests (merged / zero-filled) */
@@ -101,7 +101,7 @@ typedef struct {
   int32_t num_heads;
   int32_t page_size;
   int32_t kernel;             /* mla_kernel_t the partition is made for (DEFAULT: PAIR) */
-  int32_t tile_tokens;        /* token granularity of the split (128 tcgen05, 64 mma.sync) */
+  int32_t tile_tokens;        /* token granularity of the split (256 pair, 128 tcgen05 and 4-bit, 64 mma.sync) */
   int64_t workspace_bytes;    /* device bytes owned by the plan */
 } mla_plan_info_t;
 
@@ -157,8 +157,8 @@ mla_status_t mla_decode_plan(mla_plan_t plan, const int32_t* kv_indptr_host,
  *   mla_decode_run then takes
  *     q_nope [batch, q_len, num_heads, 512],  q_pe [batch, q_len, num_heads, 64],
  *     out    [batch, q_len, num_heads, 512],  lse  [batch, q_len, num_heads].
- *   With the CTA-pair kernel (MLA_KERNEL_DEFAULT or MLA_KERNEL_PAIR) and
- *   q_len * num_heads <= 128, the q_len query tokens of a request share
+ *   With the CTA-pair kernel (MLA_KERNEL_DEFAULT or MLA_KERNEL_PAIR) or the
+ *   4-bit kernel (MLA_KERNEL_Q4) and q_len * num_heads <= 128, the q_len query tokens of a request share
  *   the rows of one request (row j * num_heads + h of the [batch, q_len *
  *   num_heads] view of the query and output arrays, each row masked to its
  *   own prefix), so a step reads each request's cache once;

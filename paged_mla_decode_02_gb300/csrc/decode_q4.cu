@@ -45,16 +45,19 @@
 // goes on without waiting, so that the named barriers and commits of the others
 // still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is recorded.
 //
-// What bounds it (device time from a graph, cold L2): with 16 query rows the way of
-// a tile through its buffer.  4 requests of 131072 tokens take 61.5 us, 2.6 TB/s, 27
-// tiles a CTA at 1.5 to 1.9 us each; a buffer is held for the expansion (about 3700
-// cycles of a warp, among 28 warps that take 54 % of the issue slots), the scores
-// (1250), P (1700) and P . V (1700), and shared memory has room for three.  Loads or
-// stores left out gain 2 us, the arithmetic of P nothing.  With 64 rows a tile takes
-// 2.9 us (64 requests of 4096 tokens, 128 heads: 102.7 us; 72 GFLOP, 0.71 PFLOP/s):
-// both products read the tile and their other operand through shared memory, 2700
-// cycles of 128 bytes in 5700, next to the expansion's stores and its 4500
-// instructions.  All MMAs left out it is 82 us, half of the expansion left out 95.
+// What bounds it (device time from a graph, cold L2): the way of a tile through its
+// buffer, among 28 warps that take 52 % of the issue slots.
+// - 16 query rows: 4 requests of 131072 tokens take 61 us, 2.6 TB/s, 27 tiles a CTA at
+//   1.5 to 1.9 us each.  A buffer is held for the expansion (about 3700 cycles of a
+//   warp), the scores (1250), P (1700) and P . V (1700); shared memory has room for
+//   three.  Loads or stores left out gain 2 us, the arithmetic of P nothing.
+// - 64 rows: 64 requests of 4096 tokens and 128 heads take 101 us, 0.72 PFLOP/s, 2.9 us
+//   a tile.  Expansion 2250, scores 2000, P 3300 and P . V 3300 cycles, over two
+//   buffers.  Both products read the tile and their other operand through shared
+//   memory, 2700 cycles of 128 bytes a tile.  Of 105 us, all MMAs left out made 82, half
+//   of the expansion left out 95.
+// A unit costs 3.4 us (16 rows) to 5.7 us (64) beyond its tiles: its last P . V, the
+// sums, the output; the first one of a launch more, for its code is fetched then.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -483,8 +486,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       };
       // The scores of a tile need its rows, P . V of the tile before its P: whichever
       // comes first goes first, so each has a warp of its own (with one warp for both,
-      // in a fixed order, the rows of a tile waited for those of the one before:
-      // 2.4 us a tile of 16 query rows, against 1.5).
+      // in a fixed order, the scores of a tile wait for P of the one before).
       const int role = warp - kIssueWarp;
       int g = 0;
       for (int ui = u0; ui < u1; ++ui) {

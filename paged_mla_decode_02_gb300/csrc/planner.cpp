@@ -274,11 +274,11 @@ void partition_batch_pair(const int32_t* kv_indptr, const int32_t* kv_len, int b
 }
 
 namespace {
-double q4_tile_us(int rows) { return rows <= 16 ? 1.7 : rows <= 32 ? 2.0 : 2.8; }
+double q4_tile_us(int rows) { return rows <= 16 ? 1.9 : rows <= 32 ? 2.2 : 3.3; }
 }  // namespace
 
 PlanCosts q4_costs(int rows) {
-  const int unit = static_cast<int>(4 * 5.0 / q4_tile_us(rows));
+  const int unit = static_cast<int>(4 * 6.0 / q4_tile_us(rows));
   return PlanCosts{4, unit, 2, 1};
 }
 

@@ -710,6 +710,53 @@ def test_decode_replayed_after_new_plans(H, q_len):
     dec.close()
 
 
+@pytest.mark.parametrize("H", [16, 128])
+def test_capture_of_a_plan_without_merges(H):
+    """Captured over a plan that splits no request, replayed over one that splits some
+    and has an empty one; eager runs of both in between."""
+    rng = rng_of(59, H)
+    lens = [6000, 40, 0, 33]
+    b = Batch(rng, lens, H, 32)
+    dec = mla.MLADecoder(len(lens), H, kernel="q4")
+    idx = i32(np.concatenate([b.ids, np.zeros(16, np.int32)]))
+    small = Batch.__new__(Batch)
+    small.__dict__.update(b.__dict__)
+    small.lens = [30, 32, 17, 33]
+    small.indptr = np.arange(5, dtype=np.int32)
+    small.ids = np.concatenate([b.ids[:3], b.ids[b.indptr[3]:b.indptr[3] + 2]])
+    small.indptr[4] = 5
+    out = torch.empty(b.q_nope.shape, dtype=torch.float32, device="cuda")
+    lse = torch.empty(b.q_nope.shape[:-1], device="cuda")
+
+    def plan(part):
+        idx[:len(part.ids)] = i32(part.ids)
+        dec.plan(part.indptr, idx, part.lens, 32, b.sm_scale)
+
+    def check(part, run, what):
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        run()
+        dec.check_status()
+        check_decode(part, out, lse, what)
+
+    eager = lambda: dec.run_q4(b.q_nope, b.q_pe, b.cache, out=out, lse=lse)
+    plan(small)
+    assert dec.info()["num_merge"] == 0
+    check(small, eager, "eager, nothing to merge")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        eager()
+    check(small, g.replay, "replayed, nothing to merge")
+    plan(b)
+    assert dec.info()["num_merge"] >= 2 and dec.info()["num_partial_slots"] > 1
+    check(b, g.replay, "replayed over splits")
+    check(b, eager, "eager over splits")
+    plan(small)
+    check(small, g.replay, "replayed again")
+    check(small, eager, "eager again")
+    dec.close()
+
+
 def test_a_serving_step_together():
     """Tables, rope append into a bf16 cache of the step's tokens, those rows quantised
     into the pages, the decode over them, and the context read back: captured, and
