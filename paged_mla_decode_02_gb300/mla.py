@@ -382,11 +382,11 @@ def mla_decode_run_q4(plan, q_nope, q_pe, cache, out, lse, stream=None, page_siz
     import torch
     lib = load_library()
     names, tensors = "q_nope q_pe cache out lse", (q_nope, q_pe, cache, out, lse)
-    device = torch.cuda.current_device()
     _on_cuda(names, *tensors)
-    for t in tensors:
+    device = torch.cuda.current_device()
+    for i, t in enumerate(tensors):
         if t.get_device() != device:
-            raise ValueError(f"{names.split()[[x is t for x in tensors].index(True)]} must be on the current CUDA device")
+            raise ValueError(f"{names.split()[i]} must be on the current CUDA device")
     shape = cache.shape
     if cache.dtype != torch.uint8 or len(shape) != 3 or shape[2] != Q4_ROW_BYTES:
         raise ValueError(f"cache must be uint8 [num_pages, page_size, {Q4_ROW_BYTES}], got {cache.dtype} "
