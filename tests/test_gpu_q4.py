@@ -351,7 +351,7 @@ def tolerances(b, values, spread):
         slots = [int(b.ids[b.indptr[i] + t // b.P]) * b.P + t % b.P for t in range(int(length))]
         n[i] = length
         if slots:
-            A[i] = (q[i] @ np.abs(values[slots]).T).max(-1) * b.sm_scale
+            A[i] = (q[i] @ np.abs(values[slots]).T).max(-1) * abs(b.sm_scale)
             s = f64(b.q)[i] @ values[slots].T * b.sm_scale
             w = np.exp(s - s.max(-1, keepdims=True))
             w /= w.sum(-1, keepdims=True)
@@ -754,6 +754,39 @@ def test_capture_of_a_plan_without_merges(H):
     plan(small)
     check(small, g.replay, "replayed again")
     check(small, eager, "eager again")
+    dec.close()
+
+
+@pytest.mark.parametrize("H, most", [(16, 40), (24, 200), (128, 150)])
+def test_decode_of_many_short_requests(H, most):
+    """More requests than workers, many of them empty or of one token."""
+    rng = rng_of(60, H)
+    lens = rng.integers(0, most, 700)
+    lens[rng.permutation(700)[:150]] = 0
+    lens[rng.permutation(700)[:150]] = 1
+    run_check(Batch(rng, lens.tolist(), H, 16), torch.bfloat16)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("sm_scale", [0.0, -0.05, 2.0])
+def test_decode_of_other_scales(H, sm_scale):
+    b = Batch(rng_of(61, H), [700, 1, 33, 5000], H, 64, q_scale=0.2)
+    b.sm_scale = sm_scale
+    run_check(b)
+
+
+def test_profile_events_around_the_decode():
+    b = Batch(rng_of(62), [3000, 20], 16, 64)
+    dec = b.decoder()
+    start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    stop.record()
+    mla.mla_plan_set_profile_events(dec.handle, start, stop)
+    out, lse = dec.run_q4(b.q_nope, b.q_pe, b.cache, out_dtype=torch.float32)
+    mla.mla_plan_set_profile_events(dec.handle, None, None)
+    dec.check_status()
+    assert 0 < start.elapsed_time(stop) < 100
+    check_decode(b, out, lse)
     dec.close()
 
 
