@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     if (warp == kIssueWarp + 2 && u0 < u1) {
       // ================= the warp that finds the rows =================
       // Lane e: where expanding warp e has its rows of each tile, S::kRowsAhead tiles ahead,
-      // and the request for them into L2.  Behind the last tile, one without rows for
-      // each group.
+      // and the request for them into L2 (without it 4 requests of 131072 tokens take 64
+      // us for 60).  Behind the last tile, one without rows for each group.
       const uint8_t* cache = static_cast<const uint8_t*>(a.ckv);
       Cursor at;
       at.ui = u0;

@@ -736,20 +736,28 @@ def mla_select_pages(scores, kv_indptr, kv_indices, top_k: int, keep_first: int,
     _check(st, None, "mla_select_pages")
 
 
+_row_codes: dict = {}
+
+
 def _row_code(name: str, t) -> int:
     """The dtype code of plain rows given to or taken from a cache."""
-    import torch
-    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}.get(t.dtype)
+    if not _row_codes:
+        import torch
+        _row_codes.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32})
+    code = _row_codes.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     return code
 
 
-def _check_q4_cache(device: int, cache) -> None:
+def _check_q4_cache(device: int, cache):
+    """The layout of a 4-bit cache; returns its shape."""
     import torch
     _on_device(device, torch.uint8, "cache", cache)
-    if cache.dim() != 3 or cache.shape[2] != Q4_ROW_BYTES:
-        raise ValueError(f"cache must be [num_pages, page_size, {Q4_ROW_BYTES}], got {tuple(cache.shape)}")
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] != Q4_ROW_BYTES:
+        raise ValueError(f"cache must be [num_pages, page_size, {Q4_ROW_BYTES}], got {tuple(shape)}")
+    return shape
 
 
 def mla_quantize_append(ckv, kpe, slots, cache, check_status: bool = False, stream=None) -> None:
@@ -758,14 +766,14 @@ def mla_quantize_append(ckv, kpe, slots, cache, check_status: bool = False, stre
     fp32; rows may be strided), slots int64 [T], negative for padding."""
     import torch
     device = torch.cuda.current_device()
-    _check_q4_cache(device, cache)
+    shape = _check_q4_cache(device, cache)
     code = _row_code("ckv", ckv)
     _on_device(device, ckv.dtype, "ckv kpe", ckv, kpe, contiguous=False)
     _on_device(device, torch.int64, "slots", slots)
     T = slots.numel()
     ckv_stride, kpe_stride = _row_stride("ckv", ckv, T, 512), _row_stride("kpe", kpe, T, 64)
     st = load_library().mla_quantize_append(ckv.data_ptr(), ckv_stride, kpe.data_ptr(), kpe_stride, code,
-                                            slots.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1], T,
+                                            slots.data_ptr(), cache.data_ptr(), shape[0], shape[1], T,
                                             int(bool(check_status)), _stream_handle(stream, device))
     _check(st, None, "mla_quantize_append")
 
