@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         *shared_sum(q, lane * kJ / 32) = sr;
       }
       named_bar_sync(1 + cg, 128);
-      // lane j joins the sums of row j: little code, which a unit's first epilogue waits for
+      // lane j joins the sums of row j (little code: the first unit of a launch waits for it)
       float inverse = 0.f;
       if (lane < kJ) {
         const float s = (*shared_sum(0, lane) + *shared_sum(1, lane)) + (*shared_sum(2, lane) + *shared_sum(3, lane));
