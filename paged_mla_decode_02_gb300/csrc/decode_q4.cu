@@ -51,9 +51,9 @@
 //   1.5 to 1.9 us each.  A buffer is held for the expansion (about 3700 cycles of a
 //   warp), the scores (1250), P (1700) and P . V (1700); shared memory has room for
 //   three.  Loads or stores left out gain 2 us, the arithmetic of P nothing.
-// - 64 rows: 64 requests of 4096 tokens and 128 heads take 101 us, 0.72 PFLOP/s, 2.9 us
-//   a tile.  Expansion 2250, scores 2000, P 3300 and P . V 3300 cycles, over two
-//   buffers.  Both products read the tile and their other operand through shared
+// - 64 rows: 64 requests of 4096 tokens and 128 heads take 96 us, 0.76 PFLOP/s, 2.7 us
+//   a tile.  Expansion 2250, scores 2000 (500 after it), P 3300 and P . V 3300 cycles,
+//   over two buffers.  Both products read the tile and their other operand through shared
 //   memory, 2700 cycles of 128 bytes a tile.  Of 105 us, all MMAs left out made 82, half
 //   of the expansion left out 95.
 // A unit costs 3.4 us (16 rows) to 5.7 us (64) beyond its tiles: its last P . V, the
@@ -114,6 +114,12 @@ struct Shape {
   static constexpr int kGroups = kRows == 16 ? 2 : 1;
   static constexpr int kTileWarps = kExpandWarps / kGroups;
   static constexpr int kTokWarp = kT / kTileWarps;         // rows that a warp expands, of one page
+  // The scores' MMAs follow the expansion in kStages steps of 4 / kStages panels.  With 64
+  // rows they take 2000 cycles, of which three quarters lie beside the expansion then (96.4
+  // us for 100.8, 64 requests of 4096 tokens and 128 heads).  Fewer rows have fewer to hide,
+  // and the loads, 64 bytes of a row at a time instead of 256, cost more (63.9 us for 60.2,
+  // 4 requests of 131072 tokens, 16 heads; 32 rows the same either way).
+  static constexpr int kStages = kRows == 64 ? 4 : 1;
   // registers a thread at launch, then by role
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;
   static constexpr int kRegsSoftmax = kRows == 32 ? 96 : 80, kRegsExpand = kRows == 32 ? 72 : 80;
@@ -131,8 +137,8 @@ struct Shape {
   static constexpr int kPeBufs = kRows == 32 ? 2 : 1;      // of the rope part
   static constexpr int kRowsAhead = 4;                     // tiles whose rows are known ahead
   // barriers
-  static constexpr int kKFull0 = 0;                        // [kBufs] tile expanded (a signal of each of its warps)
-  static constexpr int kSFull0 = kKFull0 + kBufs;          // [2] scores made
+  static constexpr int kKFull0 = 0;                        // [kBufs][kStages] panels of the tile expanded (a signal of each of its warps)
+  static constexpr int kSFull0 = kKFull0 + kBufs * kStages;   // [2] scores made
   static constexpr int kSFree0 = kSFull0 + 2;              // [2] scores read (a signal of every softmax warp)
   static constexpr int kPReady0 = kSFree0 + 2;             // [4] P of 32 tokens written (a signal for every kJ query rows)
   // [kBufs][4] P . V over 32 tokens made: their rows of K and P may be written again (by
@@ -450,11 +456,13 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       constexpr uint32_t id_s = idesc_f8(S::kNS, 0, false), id_hi = idesc_f8(S::kPN, 1, true), id_lo = idesc_f8(S::kPN, 0, true);
       auto scores = [&](int g) {
         if (g > 1) wait(S::kSFree0 + (g & 1), (g - 2) >> 1);
-        wait(S::kKFull0 + g % kBufs, g / kBufs);
-        tc_fence_after();
         const uint32_t d = tmem + S::kColS + (g & 1) * S::kNS;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
+          if (p % (4 / S::kStages) == 0) {
+            wait(S::kKFull0 + g % kBufs * S::kStages + p / (4 / S::kStages), g / kBufs);
+            tc_fence_after();
+          }
           const uint64_t ka = k_desc + static_cast<uint64_t>(((g % kBufs * 4 + p) * S::kPanel) >> 4);
           const uint64_t qb = q_desc + static_cast<uint64_t>((p * S::kQPanel) >> 4);
 #pragma unroll
@@ -518,17 +526,18 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (lane == 0) mbar_arrive(bar(S::kRowsFree0 + g % S::kRowsAhead));
         return r;
       };
-      // A lane takes whole groups (16 bytes of codes): of ckv, group 4 (lane / 8) + lane % 4
-      // of row 2 i + lane / 4 % 2 for each i, so that eight lanes write to eight groups of
-      // banks; of kpe, group lane % 2 of row lane / 2.  Shifts of ckv: four of row 8 i +
-      // lane / 4 a lane.
-      const int panel = lane >> 3, odd = (lane >> 2) & 1, pair = lane & 3;
+      // A lane takes whole groups (16 bytes of codes).  Of ckv, at a time, a warp takes kRun
+      // rows of kSpan panels: eight lanes the four groups of two rows, which they write to
+      // eight groups of banks.  Of kpe, group lane % 2 of row lane / 2.  Shifts of ckv: four of
+      // row 8 i + lane / 4 a lane.
+      constexpr int kSpan = 4 / S::kStages, kRun = 8 / kSpan, kRuns = kTokWarp / kRun;
+      const int pair = lane & 3, panel = (lane >> 3) % kSpan, sub = ((lane >> 2) & 1) + 2 * ((lane >> 3) / kSpan);
       // Of kpe with eight rows a warp: half a group a lane, a quarter of row lane / 4.
       uint4 raw[kTokWarp / 2], raw_pe;
       uint32_t shifts[kTokWarp / 8], meta_pe;
       constexpr int kPeShift = kTokWarp == 16 ? 1 : 2;   // lanes of a row's kpe
-      auto load_ckv = [&](const Rows& r, int i) {   // rows 2 i and 2 i + 1
-        return __ldg(reinterpret_cast<const uint4*>(r.src + (2 * i + odd) * kQ4Row) + 4 * panel + pair);
+      auto load_ckv = [&](const Rows& r, int i) {   // run i % kRuns of stage i / kRuns
+        return __ldg(reinterpret_cast<const uint4*>(r.src + (kRun * (i % kRuns) + sub) * kQ4Row) + 4 * (kSpan * (i / kRuns) + panel) + pair);
       };
       auto load_meta = [&](const Rows& r) {
 #pragma unroll
@@ -555,7 +564,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #pragma unroll
         for (int i = 0; i < kTokWarp / 2; ++i) {
           raw[i] = make_uint4(0, 0, 0, 0);
-          if (2 * i + odd < r.n) raw[i] = load_ckv(r, i);
+          if (kRun * (i % kRuns) + sub < r.n) raw[i] = load_ckv(r, i);
         }
       };
       // Tile g from registers, which take the rows `next` meanwhile.
@@ -571,19 +580,29 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         for (int i = 0; i < kTokWarp / 8; ++i) large |= shift[i] & (shift[i] << 1) & 0x8888u;
         const bool whole = next.n == kTokWarp;
         auto fill = [&](auto table_of) {
-          // chunk 2 pair of row 2 i + odd is at 2 pair ^ odd ^ (2 i & 7)
-          unsigned char* dst = sm + S::kOffK + g % kBufs * 4 * S::kPanel + panel * S::kPanel + (kTokWarp * ew + odd) * 128;
-          uint32_t mine[kTokWarp / 2];   // shifts of groups 4 panel ..
+          unsigned char* dst = sm + S::kOffK + g % kBufs * 4 * S::kPanel + panel * S::kPanel + (kTokWarp * ew + sub) * 128;
 #pragma unroll
-          for (int i = 0; i < kTokWarp / 2; ++i) mine[i] = __shfl_sync(~0u, shift[i / 4], 8 * (i % 4) + 4 * odd + panel);
+          for (int stage = 0; stage < S::kStages; ++stage) {
+            uint32_t mine[kRuns];   // shifts of the groups of this lane's panel
 #pragma unroll
-          for (int i = 0; i < kTokWarp / 2; ++i) {
-            const uint2 t = table_of((mine[i] >> (4 * pair)) & 15);
-            unsigned char* at = dst + (((2 * pair) ^ odd ^ (2 * i & 6)) << 4);
-            unsigned char* at2 = dst + (((2 * pair + 1) ^ odd ^ (2 * i & 6)) << 4);
-            *reinterpret_cast<uint4*>(at + 256 * i) = expand16(t, raw[i].x, raw[i].y);
-            *reinterpret_cast<uint4*>(at2 + 256 * i) = expand16(t, raw[i].z, raw[i].w);
-            if (whole) raw[i] = load_ckv(next, i);
+            for (int j = 0; j < kRuns; ++j)
+              mine[j] = __shfl_sync(~0u, shift[kRun * j / 8], 4 * (kRun * j % 8 + sub) + kSpan * stage + panel);
+#pragma unroll
+            for (int j = 0; j < kRuns; ++j) {
+              const int i = stage * kRuns + j;
+              const uint2 t = table_of((mine[j] >> (4 * pair)) & 15);
+              // chunk 2 pair of a row is at 2 pair ^ row % 8
+              unsigned char* at = dst + kSpan * stage * S::kPanel + kRun * j * 128;
+              const int chunk = (2 * pair) ^ sub ^ (kRun * j % 8);
+              *reinterpret_cast<uint4*>(at + (chunk << 4)) = expand16(t, raw[i].x, raw[i].y);
+              *reinterpret_cast<uint4*>(at + ((chunk ^ 1) << 4)) = expand16(t, raw[i].z, raw[i].w);
+              if (whole) raw[i] = load_ckv(next, i);
+            }
+            if (stage + 1 < S::kStages) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(S::kKFull0 + g % kBufs * S::kStages + stage));
+            }
           }
           if (S::kPeBufs == 1 && g > 0) wait(S::kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read it
           const int row = kTokWarp * ew + (lane >> kPeShift);
@@ -605,7 +624,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #ifdef MLA_STALL_TEST
         if (blockIdx.x == 0 && ew == 0 && g + 1 == g_q4_stall) return;
 #endif
-        if (lane == 0) mbar_arrive(bar(S::kKFull0 + g % kBufs));
+        if (lane == 0) mbar_arrive(bar(S::kKFull0 + g % kBufs * S::kStages + S::kStages - 1));
         load_pe(next);
         if (!whole) load_part(next);
       };
