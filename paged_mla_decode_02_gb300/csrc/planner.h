@@ -87,9 +87,9 @@ void partition_batch_pair(const int32_t* kv_indptr, const int32_t* kv_len, int b
 // more (its query, the first rows, the sums and the output), so a short request
 // is worth cutting down to single tiles (4 requests of up to 2000 tokens, 16
 // heads: 28 us in pieces of four tiles or more, 19 with single ones), and 64
-// requests of 32 tiles and 128 rows are left whole on 128 of 152 CTAs (100.8 us;
-// cut evenly 113).  With a unit at 4 us 128 ragged requests take 194.6 us, 189
-// with 6.
+// requests of 32 tiles and 128 rows are left whole on 128 of 152 CTAs (100.8 us
+// then; cut evenly 113).  With a unit at 4 us 128 ragged requests took 194.6 us,
+// 189 with 6.
 PlanCosts q4_costs(int rows);
 double q4_step_estimate_us(const Partition& p, int rows);
 void partition_batch_q4(const int32_t* kv_indptr, const int32_t* kv_len, int batch, int n_workers,
