@@ -579,18 +579,29 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #pragma unroll
         for (int i = 0; i < kTokWarp / 8; ++i) large |= shift[i] & (shift[i] << 1) & 0x8888u;
         const bool whole = next.n == kTokWarp;
-        auto fill = [&](auto table_of) {
+        // the tables of this lane's groups, made before the buffer is free
+        uint2 tables[kTokWarp / 2], table_pe;
+        auto make = [&](auto table_of) {
+#pragma unroll
+          for (int i = 0; i < kTokWarp / 2; ++i) {
+            const int row = kRun * (i % kRuns);
+            const uint32_t mine = __shfl_sync(~0u, shift[row / 8], 4 * (row % 8 + sub) + kSpan * (i / kRuns) + panel);
+            tables[i] = table_of((mine >> (4 * pair)) & 15);
+          }
+          table_pe = table_of((meta >> (kTokWarp == 16 ? 4 * (lane & 1) : 2 * (lane & 2))) & 15);
+        };
+        if (__any_sync(~0u, large)) make([&](uint32_t k) { return k >= 12 ? table[k - 12] : normal_table(k); });
+        else make([](uint32_t k) { return normal_table(k); });
+        // the buffer was read by P . V of g - kBufs
+        if (g >= kBufs) wait(S::kPvDone0 + 4 * (g % kBufs) + ew * kTokWarp / 32, g / kBufs - 1);
+        {
           unsigned char* dst = sm + S::kOffK + g % kBufs * 4 * S::kPanel + panel * S::kPanel + (kTokWarp * ew + sub) * 128;
 #pragma unroll
           for (int stage = 0; stage < S::kStages; ++stage) {
-            uint32_t mine[kRuns];   // shifts of the groups of this lane's panel
-#pragma unroll
-            for (int j = 0; j < kRuns; ++j)
-              mine[j] = __shfl_sync(~0u, shift[kRun * j / 8], 4 * (kRun * j % 8 + sub) + kSpan * stage + panel);
 #pragma unroll
             for (int j = 0; j < kRuns; ++j) {
               const int i = stage * kRuns + j;
-              const uint2 t = table_of((mine[j] >> (4 * pair)) & 15);
+              const uint2 t = tables[i];
               // chunk 2 pair of a row is at 2 pair ^ row % 8
               unsigned char* at = dst + kSpan * stage * S::kPanel + kRun * j * 128;
               const int chunk = (2 * pair) ^ sub ^ (kRun * j % 8);
@@ -607,7 +618,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           if (S::kPeBufs == 1 && g > 0) wait(S::kSFull0 + ((g - 1) & 1), (g - 1) >> 1);   // the scores before have read it
           const int row = kTokWarp * ew + (lane >> kPeShift);
           unsigned char* pe = sm + S::kOffKPe + (S::kPeBufs == 2 ? (g & 1) * kT * 64 : 0) + row * 64;
-          const uint2 t = table_of((meta >> (kTokWarp == 16 ? 4 * (lane & 1) : 2 * (lane & 2))) & 15);
+          const uint2 t = table_pe;
           if constexpr (kTokWarp == 16) {
             const int at = ((2 * (lane & 1)) ^ ((row >> 1) & 3)) << 4;
             *reinterpret_cast<uint4*>(pe + at) = expand16(t, raw_pe.x, raw_pe.y);
@@ -616,9 +627,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             *reinterpret_cast<uint4*>(pe + (((lane & 3) ^ ((row >> 1) & 3)) << 4)) = expand16(t, raw_pe.x, raw_pe.y);
           }
           if ((lane & ((1 << kPeShift) - 1)) == 0) sm[S::exp_at(g % kBufs, row)] = static_cast<unsigned char>(meta >> 8);
-        };
-        if (__any_sync(~0u, large)) fill([&](uint32_t k) { return k >= 12 ? table[k - 12] : normal_table(k); });
-        else fill([](uint32_t k) { return normal_table(k); });
+        }
         fence_proxy_async_smem();
         __syncwarp();
 #ifdef MLA_STALL_TEST
@@ -635,8 +644,6 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         load_pe(rows);
       }
       for (int g = group; g < tiles; g += S::kGroups) {
-        // the buffer was read by P . V of g - kBufs
-        if (g >= kBufs) wait(S::kPvDone0 + 4 * (g % kBufs) + ew * kTokWarp / 32, g / kBufs - 1);
         expand(g, rows_of(g + S::kGroups));
       }
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
