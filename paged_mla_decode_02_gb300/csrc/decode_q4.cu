@@ -474,8 +474,10 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         mma_commit_elect(bar(S::kSFull0 + (g & 1)));
       };
       auto values = [&](int g, bool first) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {   // 32 tokens
+        // 32 tokens at a time, rolled up: with less code for 28 warps to fetch 4 requests of
+        // 131072 tokens and 16 heads take 59.8 us for 61.2 (the scores rolled up too: no more)
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
           wait(S::kPReady0 + j, g);
           tc_fence_after();
           const uint64_t pb = p_desc + static_cast<uint64_t>((j * 32 * S::kPRow) >> 4);
