@@ -47,12 +47,12 @@
 //
 // What bounds it (device time from a graph, cold L2): the way of a tile through its
 // buffer, among 28 warps that take 52 % of the issue slots.
-// - 16 query rows: 4 requests of 131072 tokens take 61 us, 2.6 TB/s, 27 tiles a CTA at
+// - 16 query rows: 4 requests of 131072 tokens take 60 us, 2.7 TB/s, 27 tiles a CTA at
 //   1.5 to 1.9 us each.  A buffer is held for the expansion (about 3700 cycles of a
 //   warp), the scores (1250), P (1700) and P . V (1700); shared memory has room for
 //   three.  Loads or stores left out gain 2 us, the arithmetic of P nothing.
-// - 64 rows: 64 requests of 4096 tokens and 128 heads take 96 us, 0.76 PFLOP/s, 2.7 us
-//   a tile.  Expansion 2250, scores 2000 (500 after it), P 3300 and P . V 3300 cycles,
+// - 64 rows: 64 requests of 4096 tokens and 128 heads take 93 us, 0.79 PFLOP/s, 2.6 us
+//   a tile.  Expansion 2250, scores 2000 (500 after it), P 3300 and P . V 2500 cycles,
 //   over two buffers.  Both products read the tile and their other operand through shared
 //   memory, 2700 cycles of 128 bytes a tile.  Of 105 us, all MMAs left out made 82, half
 //   of the expansion left out 95.
@@ -116,7 +116,8 @@ struct Shape {
   static constexpr int kTokWarp = kT / kTileWarps;         // rows that a warp expands, of one page
   // The scores' MMAs follow the expansion in kStages steps of 4 / kStages panels.  With 64
   // rows they take 2000 cycles, of which three quarters lie beside the expansion then (96.4
-  // us for 100.8, 64 requests of 4096 tokens and 128 heads).  Fewer rows have fewer to hide,
+  // us for 100.8 at first, 64 requests of 4096 tokens and 128 heads; two steps 94.7 for
+  // 92.7 now).  Fewer rows have fewer to hide,
   // and the loads, 64 bytes of a row at a time instead of 256, cost more (63.9 us for 60.2,
   // 4 requests of 131072 tokens, 16 heads; 32 rows the same either way).
   static constexpr int kStages = kRows == 64 ? 4 : 1;
