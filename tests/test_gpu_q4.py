@@ -208,6 +208,25 @@ def test_read_of_special_rows():
         assert torch.equal(pe.cpu().nan_to_num(9), want[:, 512:].nan_to_num(9))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_read_of_every_unit(dtype):
+    """Every exponent with every shift, all eight magnitudes of both signs."""
+    rng = rng_of(23)
+    b = np.zeros((96 * 15, O.ROW), np.uint8)
+    b[:, :288] = rng.integers(0, 256, (len(b), 288))
+    first = np.tile(np.arange(15), 96)
+    k = (first[:, None] + np.arange(18)) % 15
+    b[:, 288:297] = k[:, ::2] | k[:, 1::2] << 4
+    b[:, 297] = np.repeat(np.arange(127 - 32, 127 + 64), 15)
+    cache = torch.from_numpy(b.reshape(-1, 32, O.ROW)).cuda()
+    ckv = torch.zeros(len(b), 512, dtype=TYPES[dtype], device="cuda")
+    pe = torch.zeros(len(b), 64, dtype=TYPES[dtype], device="cuda")
+    mla.mla_read_cache(cache, None, i32([0, len(b) // 32]), i32(np.arange(len(b) // 32)), i32([0]), i32([0, len(b)]), ckv, pe,
+                       check_status=True)
+    got, want = torch.cat([ckv, pe], 1).cpu(), rounded(O.unpack(b), dtype)
+    assert torch.equal(got, want) and torch.equal(got.signbit(), want.signbit())
+
+
 def test_read_of_many_requests():
     """4096 requests, most of them without rows."""
     rng = rng_of(22)
@@ -436,6 +455,25 @@ def test_decode_rows_of_different_exponents(H):
         x[rng.permutation(n)[:n // 8]] = 0
         return x
     b = Batch(rng, [300, 128, 1, 40], H, 64, rows=rows, q_scale=2.0 ** -9)
+    run_check(b)
+
+
+@pytest.mark.parametrize("H", [1, 16, 32, 64, 128])
+@pytest.mark.parametrize("lens", [[700, 33], [2500]])
+def test_decode_groups_far_apart(H, lens):
+    """Every shift up to the largest, in some rows all of them: numbers that are
+    subnormal in e4m3 beside such that are not."""
+    rng = rng_of(63, H, lens[0])
+
+    def rows(n):
+        shift = rng.integers(0, 17, (n, 18))
+        shift[rng.permutation(n)[:n // 3]] %= 4
+        return rng.standard_normal((n, 576)) * np.repeat(2.0 ** -shift.astype(float), 32, 1)
+
+    b = Batch(rng, lens, H, 32, rows=rows)
+    held = b.bytes[b.bytes[:, 297] != 255]
+    shifts = np.stack([held[:, 288:297] & 15, held[:, 288:297] >> 4], -1).reshape(len(held), 18)
+    assert set(np.unique(shifts)) >= set(range(15))
     run_check(b)
 
 
