@@ -17,10 +17,13 @@
 //
 // The other operand of each product is split into terms of 8 bits:
 // - the query row, under a power of two that brings its largest magnitude into
-//   [2^7, 2^8), into hi = e4m3(x) and lo = e4m3(x - hi), which together are the
-//   bf16 query exactly (but for elements below 2^-2 after the scaling, off by
-//   2^-11 at most).  Both are rows of the same B: S^T has a column for each, and
-//   their sum is the score.
+//   [2^7, 2^8), into hi = e4m3(x) and lo = e4m3(2^5 (x - hi)).  Both are rows of the
+//   same B: S^T has a column for each, and hi's + 2^-5 lo's is the score.  The rest is
+//   2^3 at most, so that lo fits under the largest e4m3 number, 448; held as it is it
+//   would be off by 2^-10 for elements below 2^-2, a hundredth of the largest and less,
+//   which a row with one large dim has many of (scores off by 6e-3 where it is 300
+//   times the others).  So hi + 2^-5 lo is the bf16 query exactly down to 2^-7, and
+//   within 2^-15 below.
 // - P.  With the row's unit 2^(E_t - 6) moved into it, p = 2^(s_t + E_t - ref)
 //   can span many powers of two that add up over a long context, so the terms'
 //   range matters as much as their bits.  Up to 32 query rows, three e5m2 terms
@@ -248,11 +251,12 @@ __device__ __forceinline__ __half2 from_fp8x2(uint32_t codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), kType);
   return *reinterpret_cast<const __half2*>(&h);
 }
-// Two floats -> hi + lo in e4m3 (x - hi is exact).
+// Two floats -> hi and lo in e4m3, x = hi + lo / kLoScale (x - hi is exact).
+constexpr float kLoScale = 32.f;
 __device__ __forceinline__ void split_query(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
   const float2 h = __half22float2(from_fp8x2<__NV_E4M3>(hi));
-  lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 - h.x, x1 - h.y), __NV_SATFINITE, __NV_E4M3);
+  lo = __nv_cvt_float2_to_fp8x2(make_float2((x0 - h.x) * kLoScale, (x1 - h.y) * kLoScale), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Four codes to four e4m3 numbers: the magnitudes' indices select bytes of the
@@ -742,8 +746,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             const float4 f = *reinterpret_cast<const float4*>(scale + j);
             const float4 ref = *reinterpret_cast<const float4*>(refs + j);
             auto two = [&](int i, float2 f2, float2 ref2) {
-              const float2 s = add2(make_float2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
-                                    make_float2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+              const float2 s = fma2(make_float2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])), make_float2(1 / kLoScale, 1 / kLoScale),
+                                    make_float2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])));
               const float2 y = fma2(mul2(s, make_float2(unit, unit)), f2, add2(make_float2(fe, fe), ref2));
               z[i] = y.x;
               z[i + 1] = y.y;
