@@ -29,8 +29,16 @@
 //   range matters as much as their bits.  Up to 32 query rows, three e5m2 terms
 //   side by side in B (the columns of O^T are added in the epilogue): nine bits,
 //   from 2^15 down to 2^-17.  64 rows (O^T's three terms would not fit into
-//   tensor memory): hi = e5m2(p), lo = e4m3(p - hi), two MMAs into the same
-//   columns: eight bits for the larger p, from 2^12 down to 2^-17.
+//   tensor memory): two terms, two MMAs into the same columns.  hi = e5m2(p), and
+//   lo, of p - hi, in one of two forms that a unit's scores choose: e4m3, eight bits
+//   of p from 2^12 down to 2^-3 and ever fewer below, or e5m2, seven bits from 2^15
+//   down to 2^-11.  The first suits weights of which some are of like size.  Where a
+//   row has but a few large ones (a token that all attend to, whose own value may
+//   say nothing), the sum of many small ones may be the result: 64 rows with such a
+//   one among them take the second for the rest of the unit.  Off by 2^-8 or 2^-7 of
+//   a weight at most, 0.12 or 0.25 % of a result whose values add up like a random
+//   walk; with the first form alone 0.6 % where a token stands 6 natural units above
+//   the rest, 5 % at 9.
 //
 // The softmax's state is kept per query row: a reference that moves (and O with
 // it) when a score passes it by more than kSlack, and two sums in fp32 per
@@ -64,6 +72,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <climits>
+#include <type_traits>
 
 #include "device_utils.cuh"
 #include "issue.cuh"
@@ -133,6 +144,13 @@ struct Shape {
   static constexpr float kTop = kSide ? 15.f : 12.f, kSlack = kSide ? 8.f : 7.f;
   // p from here on has all its bits (the last term's least unit is 2^-16, 2^-9)
   static constexpr float kFull = kSide ? 0x1p-8f : 0x1p-2f;
+  // the same with lo in e5m2, of least unit 2^-16: the largest at 2^7 leaves seven bits of
+  // weights 2^-18 of it.  (A slack too small is paid for in moves, which cost a good part of a
+  // tile's time.)
+  static constexpr float kTopWide = 15.f, kSlackWide = 8.f, kFullWide = 0x1p-9f;
+  // a row found to need it in the middle of a unit has two tiles to go until all rows take
+  // it, and its largest p up here
+  static constexpr float kSlackFew = 1.f;
   // tensor memory columns
   static constexpr int kOBlock = kRows == 16 ? 64 : kPN;   // of 128 dims
   static constexpr int kColS = 4 * kOBlock;
@@ -172,7 +190,12 @@ struct Shape {
   static constexpr int kOffTable = kOffRef + kRows * 4;    // [4] e4m3 codes of the magnitudes, for shifts 12 ..
   static constexpr int kOffRed = kOffTable + 4 * 8;        // [softmax warps][kJ] floats
   static constexpr int kOffRows = kOffRed + kSoftmaxWarps * kJ * 4;   // [kRowsAhead][warps of a tile] packed rows
-  static constexpr int kOffBar = kOffRows + kRowsAhead * kTileWarps * 8;
+  static constexpr int kOffWide = kOffRows + kRowsAhead * kTileWarps * 8;   // [4] of 32 tokens: lo in e5m2
+  static constexpr int kOffFew = kOffWide + (kSide ? 0 : 16);   // [2][softmax warps] few_large, of a unit's first tile and of later ones
+  static constexpr int kOffForm = kOffFew + (kSide ? 0 : 2 * 4 * kSoftmaxWarps);   // [kRows / kJ] lo in e5m2 where a reference moves
+  static constexpr int kOffWant = kOffForm + (kSide ? 0 : 4 * (kRows / kJ));   // [2] by unit parity, the tile from which lo is e5m2
+  static constexpr int kOffBar = kOffWant + (kSide ? 0 : 8);
+  static_assert(kOffFew % 16 == 0, "read as uint4");
   static_assert(kOffP % 1024 == 0 && kOffK % 1024 == 0 && kOffKPe % 1024 == 0, "swizzle atoms");
 };
 
@@ -326,6 +349,23 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
+// A bit for each of N rows that has next to none of its weights p = 2^z in this
+// warp's `valid` tokens (the first ones) at 1/2 or above: one, or two of 32.
+template <int N>
+__device__ __forceinline__ uint32_t few_large(const float (&z)[N], int valid) {
+  const uint32_t small = valid == 32 ? 30 : valid > 0 ? 31 : 32;   // -inf behind the last token
+  uint32_t rows = 0;
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    // the signs of four rows' z + 1, a byte each, summed over the lanes
+    auto bits = [&](int i) { return __float_as_uint(z[j + i] + 1.f); };
+    const uint32_t signs = __byte_perm(__byte_perm(bits(0), bits(1), 0x0073), __byte_perm(bits(2), bits(3), 0x0073), 0x5410);
+    const uint32_t enough = (__reduce_add_sync(~0u, (signs >> 7) & 0x01010101u) + (128 - small) * 0x01010101u) >> 7;
+    rows |= ((enough & 1) | (enough >> 7 & 2) | (enough >> 14 & 4) | (enough >> 21 & 8)) << j;
+  }
+  return rows;
+}
+
 // Where the walk over a worker's tiles stands.
 struct Cursor {
   int ui, tile, tiles;      // unit, tile of the unit
@@ -393,6 +433,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     reinterpret_cast<uint2*>(sm + S::kOffTable)[threadIdx.x] = make_uint2(t[0], t[1]);
   }
   if (threadIdx.x < kRows) reinterpret_cast<float*>(sm + S::kOffRef)[threadIdx.x] = 0.f;
+  if (!S::kSide && threadIdx.x < 2) reinterpret_cast<int*>(sm + S::kOffWant)[threadIdx.x] = INT_MAX;
+  if (!S::kSide && threadIdx.x < 4) reinterpret_cast<uint32_t*>(sm + S::kOffWide)[threadIdx.x] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == kIssueWarp) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -458,7 +500,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       const uint64_t q_desc = smem_desc(base + S::kOffQ, 16, 1024, kSw128);
       const uint64_t qpe_desc = smem_desc(base + S::kOffQPe, 16, 512, kSw64);
       const uint64_t p_desc = smem_desc(base + S::kOffP, 16, 8 * S::kPRow, S::kPSwizzle);
-      constexpr uint32_t id_s = idesc_f8(S::kNS, 0, false), id_hi = idesc_f8(S::kPN, 1, true), id_lo = idesc_f8(S::kPN, 0, true);
+      constexpr uint32_t id_s = idesc_f8(S::kNS, 0, false), id_hi = idesc_f8(S::kPN, 1, true);
       auto scores = [&](int g) {
         if (g > 1) wait(S::kSFree0 + (g & 1), (g - 2) >> 1);
         const uint32_t d = tmem + S::kColS + (g & 1) * S::kNS;
@@ -485,6 +527,9 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         for (int j = 0; j < 4; ++j) {
           wait(S::kPReady0 + j, g);
           tc_fence_after();
+          uint32_t id_lo = idesc_f8(S::kPN, 0, true);
+          if constexpr (!S::kSide)   // e4m3 or e5m2; through a shuffle, for the MMAs' operands are to be known uniform
+            id_lo |= (__shfl_sync(~0u, reinterpret_cast<volatile const uint32_t*>(sm + S::kOffWide)[j], 0) & 1) << 10;
           const uint64_t pb = p_desc + static_cast<uint64_t>((j * 32 * S::kPRow) >> 4);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
@@ -722,6 +767,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       float lx[kJ], ld[kJ];
 #pragma unroll
       for (int j = 0; j < kJ; ++j) lx[j] = ld[j] = 0.f;
+      bool wide = false;   // 64 rows: lo is e5m2 from here to the unit's end
+      int* want = reinterpret_cast<int*>(sm + S::kOffWant) + ((ui - u0) & 1);
       for (int t0 = u.tok_begin; t0 < u.tok_end; t0 += kT, ++g) {
         const bool first = t0 == u.tok_begin;
         // ---- scores of this thread's token and query rows, less the reference, in log2 ----
@@ -772,59 +819,118 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         // ---- the reference moves: the four warps of these query rows together ----
         uint32_t moved = 0;   // rows whose reference moves
         float factor = 1.f;   // lane j: of row j
-        const bool moves = bar_any(1 + cg, 128, first || top > S::kTop);
+        const float limit = first ? -INFINITY : wide ? S::kTopWide : S::kTop;
+        const bool moves = bar_any(1 + cg, 128, first || top > limit);
+        // Another row's wish of two tiles ago: written before P of that tile was signalled, which
+        // P . V waited for, and for that the warps here, before P of the last one.  A later
+        // wish is for a later tile, seen here or not, so that all warps go over at once.
+        if (!S::kSide && !first) wide |= g >= *reinterpret_cast<volatile int*>(want);
         if (moves) {
           const float most = warp_reduce<true>(z);
           if ((lane & (32 / kJ - 1)) == 0) red[q * kJ + lane * kJ / 32] = most;
+          uint32_t* form = reinterpret_cast<uint32_t*>(sm + S::kOffForm) + cg;
+          if (!S::kSide && q == 0 && lane == 0) *form = wide;
           named_bar_sync(1 + cg, 128);
+          // The first warp's word on it, so that after a wait that ran out, too, the four meet at
+          // the barriers below equally often.
+          if (!S::kSide) wide = *form != 0;
+          // lane j (and those kJ apart): row j.  The largest p becomes 2^(kTop - kSlack); a row that
+          // sees no token in its unit's first tile sees none later, and keeps the reference 0
+          // with p = 0
+          const int r = lane % kJ;
+          const float m = fmaxf(fmaxf(red[r], red[kJ + r]), fmaxf(red[2 * kJ + r], red[3 * kJ + r]));
+          const float usual = wide ? S::kTopWide - S::kSlackWide : S::kTop - S::kSlack;
+          float up = m > limit ? m - usual : 0.f;
+          constexpr uint32_t kAll = (1u << kJ) - 1;
+          const uint32_t rows = __ballot_sync(~0u, m > limit) & kAll;   // whose reference moves
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            const float m = fmaxf(fmaxf(red[j], red[kJ + j]), fmaxf(red[2 * kJ + j], red[3 * kJ + j]));
-            // the largest p becomes 2^(kTop - kSlack); a row that sees no token in its unit's
-            // first tile sees none later, and keeps the reference 0 with p = 0
-            const float up = m > (first ? -INFINITY : S::kTop) ? m - (S::kTop - S::kSlack) : 0.f;
-            z[j] -= up;
-            if (!first && up != 0.f) {
-              moved |= 1u << j;
-              const float alpha = fast_exp2(-up);
-              lx[j] *= alpha;
-              ld[j] *= alpha;
-              if (lane == j) factor = alpha;
+          for (int j = 0; j < kJ; ++j)
+            if (rows >> j & 1) z[j] -= __shfl_sync(~0u, up, j);
+          if (!S::kSide && !wide) {
+            // rows with few large weights in all four warps' tokens; in a unit's first tile, where
+            // all rows' warps are here, of any of them (each reads the others' words then, which
+            // a later tile's must not replace)
+            uint32_t* few = reinterpret_cast<uint32_t*>(sm + S::kOffFew) + (first ? 0 : kSoftmaxWarps);
+            const uint32_t mine = few_large(z, min(max(u.tok_end - t0 - 32 * q, 0), 32));
+            const uint32_t blind = __ballot_sync(~0u, m == -INFINITY);   // not one that sees no token
+            if (lane == 0) few[warp] = mine & ~blind;
+            if (first) named_bar_sync(5, 32 * kSoftmaxWarps);
+            else named_bar_sync(1 + cg, 128);
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < kSoftmaxWarps / 4; ++i) {
+              const uint4 f = reinterpret_cast<const uint4*>(few)[i];
+              any |= (first || i == cg) && (f.x & f.y & f.z & f.w) != 0;
             }
-            if (q == 0 && lane == j) refs[j] -= up;
+            float further = 0.f;   // how much higher the largest p becomes
+            if (first) {
+              wide = any;
+              if (any) further = (S::kTopWide - S::kSlackWide) - (S::kTop - S::kSlack);
+              if (warp == 0 && lane == 0) reinterpret_cast<int*>(sm + S::kOffWant)[(ui - u0 + 1) & 1] = INT_MAX;   // the next unit's
+            } else if (any) {
+              if (lane == 0) atomicMin(want, g + 2);
+              further = S::kSlack - S::kSlackFew;
+            }
+            if (further != 0.f) {
+              if (m > limit) up -= further;
+#pragma unroll
+              for (int j = 0; j < kJ; ++j)
+                if (rows >> j & 1) z[j] += further;
+            }
           }
+          if (!first) {
+            moved = rows;
+            factor = fast_exp2(-up);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+              if (rows >> j & 1) {
+                const float alpha = __shfl_sync(~0u, factor, j);
+                lx[j] *= alpha;
+                ld[j] *= alpha;
+              }
+          }
+          if (q == 0 && lane < kJ) refs[lane] -= up;
         }
         // ---- p and its terms ----
         constexpr int kTerms = S::kSide ? 3 : 2;
         uint32_t c[kTerms][kJ / 4];
         const float2 weight = make_float2(pow2(-e), pow2(-e));
+        auto make_terms = [&](auto lo_in_e5m2) {
+          constexpr bool kWide = decltype(lo_in_e5m2)::value;
+          const __half2 full = __float2half2_rn(kWide ? 1 / S::kFullWide : 1 / S::kFull);
 #pragma unroll
-        for (int j = 0; j < kJ; j += 2) {
-          const float2 p = make_float2(fast_exp2(z[j]), fast_exp2(z[j + 1]));
-          const float2 x = fma2(p, weight, make_float2(lx[j], lx[j + 1]));
-          lx[j] = x.x;
-          lx[j + 1] = x.y;
-          const __half2 h = __floats2half2_rn(p.x, p.y);
-          uint32_t code[kTerms];
-          code[0] = to_fp8x2<__NV_E5M2>(h);
-          __half2 rest = __hsub2(h, from_fp8x2<__NV_E5M2>(code[0]));   // exact
-          if constexpr (S::kSide) {
-            code[1] = to_fp8x2<__NV_E5M2>(rest);
-            rest = __hsub2(rest, from_fp8x2<__NV_E5M2>(code[1]));
-            code[2] = to_fp8x2<__NV_E5M2>(rest);
-            rest = __hsub2(rest, from_fp8x2<__NV_E5M2>(code[2]));
-          } else {
-            code[1] = to_fp8x2<__NV_E4M3>(rest);
-            rest = __hsub2(rest, from_fp8x2<__NV_E4M3>(code[1]));
+          for (int j = 0; j < kJ; j += 2) {
+            const float2 p = make_float2(fast_exp2(z[j]), fast_exp2(z[j + 1]));
+            const float2 x = fma2(p, weight, make_float2(lx[j], lx[j + 1]));
+            lx[j] = x.x;
+            lx[j + 1] = x.y;
+            const __half2 h = __floats2half2_rn(p.x, p.y);
+            uint32_t code[kTerms];
+            code[0] = to_fp8x2<__NV_E5M2>(h);
+            __half2 rest = __hsub2(h, from_fp8x2<__NV_E5M2>(code[0]));   // exact
+            if constexpr (S::kSide) {
+              code[1] = to_fp8x2<__NV_E5M2>(rest);
+              rest = __hsub2(rest, from_fp8x2<__NV_E5M2>(code[1]));
+              code[2] = to_fp8x2<__NV_E5M2>(rest);
+              rest = __hsub2(rest, from_fp8x2<__NV_E5M2>(code[2]));
+            } else if constexpr (kWide) {
+              code[1] = to_fp8x2<__NV_E5M2>(rest);
+              rest = __hsub2(rest, from_fp8x2<__NV_E5M2>(code[1]));
+            } else {
+              code[1] = to_fp8x2<__NV_E4M3>(rest);
+              rest = __hsub2(rest, from_fp8x2<__NV_E4M3>(code[1]));
+            }
+            // what the terms leave of p, counted in full from kFull on and less below
+            rest = __hmul2(rest, __hmul2_sat(h, full));
+            const float2 y = fma2(__half22float2(rest), weight, make_float2(ld[j], ld[j + 1]));
+            ld[j] = y.x;
+            ld[j + 1] = y.y;
+#pragma unroll
+            for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
           }
-          // what the terms leave of p, counted in full from kFull on and less below
-          rest = __hmul2(rest, __hmul2_sat(h, __float2half2_rn(1 / S::kFull)));
-          const float2 y = fma2(__half22float2(rest), weight, make_float2(ld[j], ld[j + 1]));
-          ld[j] = y.x;
-          ld[j + 1] = y.y;
-#pragma unroll
-          for (int i = 0; i < kTerms; ++i) c[i][j / 4] = j % 4 ? c[i][j / 4] | code[i] << 16 : code[i];
-        }
+        };
+        if (wide) make_terms(std::true_type{});
+        else make_terms(std::false_type{});
         if (g > 0) wait(S::kPvDone0 + 4 * ((g - 1) % kBufs) + q, (g - 1) / kBufs);   // P . V of the tile before has read these rows of P
         if (moves) {
           if (moved) {   // their columns of O, a row at a time: few move at once
@@ -858,6 +964,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           else
             *reinterpret_cast<uint2*>(prow + ((i ^ ((tok >> 1) & 3)) << 4) + 8 * cg) = make_uint2(c[i][0], c[i][1]);
         }
+        if constexpr (!S::kSide)
+          if (cg == 0 && lane == 0) reinterpret_cast<volatile uint32_t*>(sm + S::kOffWide)[q] = wide;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
