@@ -736,7 +736,9 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
 #pragma unroll
           for (int j = 0; j < 9; ++j) m = __vmaxu2(m, w[i][j] & 0x7fff7fffu);
           const uint32_t top = __reduce_max_sync(~0u, max(m >> 16, m & 0xffffu));   // bits of the largest magnitude
-          const int e = top == 0 ? 0 : min(max(7 - (static_cast<int>(top >> 7) - 127), -100), 100);
+          // in -120 .. 126, where fp32 has 2^e and 2^-e, both normal: a row whose largest is below
+          // 2^-119 is left under [2^7, 2^8)
+          const int e = top == 0 ? 0 : min(7 - (static_cast<int>(top >> 7) - 127), 126);
           const float up = pow2(e);
           uint32_t hi[9], lo[9];
 #pragma unroll
@@ -795,7 +797,8 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             auto two = [&](int i, float2 f2, float2 ref2) {
               const float2 s = fma2(make_float2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])), make_float2(1 / kLoScale, 1 / kLoScale),
                                     make_float2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])));
-              const float2 y = fma2(mul2(s, make_float2(unit, unit)), f2, add2(make_float2(fe, fe), ref2));
+              // (the units first: their product is exact, and in range where the score is)
+              const float2 y = fma2(s, mul2(make_float2(unit, unit), f2), add2(make_float2(fe, fe), ref2));
               z[i] = y.x;
               z[i + 1] = y.y;
             };

@@ -50,3 +50,22 @@ def test_small_dims_beside_a_large_one(H, ratio, dim):
     tol = b.sm_scale * (off * k).sum(-1) + 2.0 ** -15 * (b.sm_scale * (q * k).sum(-1) + 1)
     worst = np.max(np.abs(got - want) / tol)
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("H", [16, 32, 128])
+@pytest.mark.parametrize("q_power, key_power, scale_power", [(115, -30, -90), (120, -20, -105), (-118, 20, 93), (-60, 30, 25),
+                                                             (0, -28, 23)])
+def test_very_large_and_very_small_queries(H, q_power, key_power, scale_power):
+    """Queries to the ends of bf16's range, under scales that make their scores ordinary
+    ones: bounds as above, with a largest magnitude of up to 2^5 below [2^7, 2^8)."""
+    rng = rng_of(82, H, q_power + 200)
+    b = Batch(rng, [1] * 6 + [40], H, 16, rows=lambda n: rng.standard_normal((n, 576)) * 2.0 ** key_power)
+    b.sm_scale = 2.0 ** scale_power
+    b.set_query(torch.from_numpy(rng.standard_normal((7, 1, H, 576)) * 2.0 ** q_power).to(torch.bfloat16))
+    got, want, keys = scores_of_single_tokens(b)
+    q, k = np.abs(f64(b.q))[:6], np.abs(keys)[:6, None, None, :]
+    off = np.minimum(q, q.max(-1, keepdims=True) * 2.0 ** -18)          # 2^-15 where the largest is 2^3
+    tol = b.sm_scale * (off * k).sum(-1) + 2.0 ** -15 * (b.sm_scale * (q * k).sum(-1) + 1)
+    worst = np.max(np.abs(got - want)[:6] / tol)
+    assert worst <= 1, worst
+    assert np.abs(got - want)[6].max() <= 2.0 ** -15 * 64                # sum |q k| of a few times ten
