@@ -14,6 +14,7 @@ the decode_wrapper.plan call reviewed in "[WIP] support flashinfer_mla"
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -853,13 +854,18 @@ class MLADecoder:
         return out, lse
 
     def run_q4(self, q_nope, q_pe, cache, out=None, lse=None, out_dtype=None, stream=None):
-        """run() over a 4-bit cache, for a decoder made with kernel="q4".  Rows of
-        q_nope behind the planned batch are not read, theirs of out and lse left as
-        they were."""
+        """run() over a 4-bit cache, for a decoder made with kernel="q4": q_nope
+        [B, H, 512], with q_len [B, Q, H, 512] (or a view of that as [B, Q * H, 512]
+        or [B * Q, H, 512]).  Rows of q_nope behind the planned batch are not read,
+        theirs of out and lse left as they were."""
         import torch
         lead = tuple(q_nope.shape[:-1])
-        if q_nope.numel() < 512 * self._rows:
-            raise ValueError(f"q_nope must hold the plan's {self._rows} query rows, got {lead}")
+        if self.page_size is not None:        # (else there is no plan, which the call below says)
+            q_len = max(1, self.q_len)
+            rows = (self.num_heads,), (q_len * self.num_heads,), (q_len, self.num_heads)
+            if not (lead[1:] in rows and math.prod(lead) >= self._rows):
+                raise ValueError(f"q_nope must hold the plan's {self._rows} query rows as [batch, "
+                                 f"{f'{q_len}, ' if q_len > 1 else ''}{self.num_heads}, 512], got {tuple(q_nope.shape)}")
         if out is None:
             out = _empty(lead + (512,), out_dtype or torch.bfloat16, q_nope.device, stream)
         if lse is None:
