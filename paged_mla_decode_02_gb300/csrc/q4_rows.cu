@@ -210,6 +210,19 @@ __device__ __forceinline__ void store_chunk(T* dst, const float (&x)[8]) {
   }
 }
 
+// code * scale for a conversion that rounds it to 16 bits as if it were exact.  A code
+// has 4 bits and the scale 24, fp32 holds 24 of the product's 28: a product rounded to
+// fp32 first may land in the middle between two numbers of the type and then on the
+// wrong one.  So it is truncated, and its last bit set if that lost anything (8 or 11
+// of the 24 bits are the type's, so the last one only breaks ties).
+__device__ __forceinline__ float truncated_product(float code, float scale) {
+  const float lo = __fmul_rd(fabsf(code), scale), hi = __fmul_ru(fabsf(code), scale);
+  return __uint_as_float(__float_as_uint(lo) | (lo != hi ? 1u : 0u) | (__float_as_uint(code) & 0x80000000u));
+}
+// A scale of 20 bits (a power of two first of all) whose products fp32 has without that,
+// none of them subnormal: 26.9 us for 29.9, 92000 rows to fp16.
+__device__ __forceinline__ bool short_scale(float scale) { return (__float_as_uint(scale) & 15u) == 0 && scale >= 0x1p-100f; }
+
 // The request of row r: how many of row_indptr[1 ..] are at or below it, found
 // by a row's eight lanes together, eight probes a step.
 __device__ __forceinline__ int request_of(const int32_t* row_indptr, int batch, int64_t r) {
@@ -287,19 +300,23 @@ __global__ void __launch_bounds__(kThreads) read_kernel(ReadArgs a) {
                                            : static_cast<const uint8_t*>(a.kpe_cache) + slot * kDKpe;
       w[i] = *reinterpret_cast<const uint2*>(src + 8 * j);
     }
+    auto expand = [&](auto product) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      float x[8];
+      for (int i = 0; i < kChunks; ++i) {
+        float x[8];
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const uint32_t half = (d < 2 ? w[i].x : w[i].y) >> (16 * (d & 1));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(half), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        x[2 * d] = f.x * a.kv_scale;
-        x[2 * d + 1] = f.y * a.kv_scale;
+        for (int d = 0; d < 4; ++d) {
+          const uint32_t half = (d < 2 ? w[i].x : w[i].y) >> (16 * (d & 1));
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(half), __NV_E4M3);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          x[2 * d] = product(f.x);
+          x[2 * d + 1] = product(f.y);
+        }
+        put(i, x);
       }
-      put(i, x);
-    }
+    };
+    if (sizeof(T) == 4 || short_scale(a.kv_scale)) expand([&](float f) { return f * a.kv_scale; });
+    else expand([&](float f) { return truncated_product(f, a.kv_scale); });
   } else {
     Chunk<__nv_bfloat16> c[kChunks];
 #pragma unroll
