@@ -38,8 +38,8 @@
  * check_status share one word, whichever of them recorded the error and on
  * whichever stream: a step may check once, through its last call, and callers
  * that are to tell their errors apart check after each of their calls.  A call
- * of no tokens or rows checks without a kernel of its own.  It cannot be
- * captured.
+ * of no tokens or rows checks without a kernel of its own (but for
+ * mla_read_cache, whose rows row_indptr counts).  It cannot be captured.
  */
 #ifndef MLA_PAGING_H
 #define MLA_PAGING_H

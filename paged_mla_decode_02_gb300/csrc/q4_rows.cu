@@ -402,8 +402,7 @@ extern "C" mla_status_t mla_read_cache(const void* cache, const void* kpe_cache,
   if (q4 ? kpe_cache != nullptr : (!kpe_cache || !aligned16(kpe_cache))) return MLA_ERR_INVALID_ARG;
   if (fp8 && (!std::isfinite(kv_scale) || kv_scale <= 0.f)) return MLA_ERR_INVALID_ARG;
   if (batch > 4096 || max_rows > INT32_MAX) return MLA_ERR_CAPACITY;
-  const bool any = batch > 0 && max_rows > 0;
-  if (any) {
+  if (batch > 0 && max_rows > 0) {
     if (!kv_indptr || !starts || !row_indptr || !ckv_out || !kpe_out || (n_indices > 0 && !kv_indices))
       return MLA_ERR_INVALID_ARG;
     if (!aligned16(ckv_out) || !aligned16(kpe_out) || ((ckv_stride | kpe_stride) & (16 / elt - 1)) || ckv_stride < kDCkv ||
@@ -429,8 +428,9 @@ extern "C" mla_status_t mla_read_cache(const void* cache, const void* kpe_cache,
   a.max_rows = max_rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (any && (e = paging_error_word(&a.err)) == cudaSuccess) {
-    const int grid = static_cast<int>((max_rows + kRowsPerBlock - 1) / kRowsPerBlock);
+  // outputs of no rows: a block that looks at what row_indptr places
+  if (batch > 0 && row_indptr && (e = paging_error_word(&a.err)) == cudaSuccess) {
+    const int grid = max_rows > 0 ? static_cast<int>((max_rows + kRowsPerBlock - 1) / kRowsPerBlock) : 1;
     auto kernel = q4    ? read_kernel_for<Kind::kQ4>(out_dtype)
                   : fp8 ? read_kernel_for<Kind::kFp8>(out_dtype)
                         : read_kernel_for<Kind::kBf16>(out_dtype);

@@ -84,3 +84,14 @@ def test_e4m3_nan_stays():
         mla.mla_read_cache(cache[:, :512].contiguous().view(1, 16, 512), cache[:, 512:].contiguous().view(1, 16, 64),
                            i32([0, 1]), i32([0]), i32([0]), i32([0, 16]), out, pe, kv_scale=0.3, check_status=True)
         assert out.isnan().all() and pe.isnan().all()
+
+
+@pytest.mark.gpu
+def test_rows_past_outputs_of_no_rows_are_reported():
+    cache = torch.zeros(2, 16, 304, dtype=torch.uint8, device="cuda")
+    ckv, pe = torch.zeros(0, 512, device="cuda"), torch.zeros(0, 64, device="cuda")
+    with pytest.raises(mla.MLAError) as e:
+        mla.mla_read_cache(cache, None, i32([0, 1]), i32([0]), i32([0]), i32([0, 3]), ckv, pe, check_status=True)
+    assert e.value.status == mla.ERR_DEVICE_BOUNDS
+    mla.mla_read_cache(cache, None, i32([0, 1]), i32([0]), i32([0]), i32([0, 0]), ckv, pe, check_status=True)
+    mla.mla_read_cache(cache, None, i32([0]), i32([]), i32([]), i32([0]), ckv, pe, check_status=True)
