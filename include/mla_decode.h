@@ -234,7 +234,11 @@ mla_status_t mla_decode_run(mla_plan_t plan, const void* q_nope, const void* q_p
  *   cache     [num_pages, page_size, MLA_Q4_ROW_BYTES] uint8, 16-byte aligned
  * Rows behind a request's last token may hold anything.  Everything that
  * mla_decode_run says of page sizes, launches, graphs, errors and bad page ids
- * holds here too; a row that held a NaN makes its request's results NaN.  With
+ * holds here too, but for two replays that it does not allow: over a plan of a
+ * larger batch the requests behind the captured ones are neither read nor
+ * written, and one over a plan of other query rows to a request (heads times the
+ * query tokens that share a pass) does nothing and is reported
+ * (MLA_ERR_DEVICE_BOUNDS).  A row that held a NaN makes its request's results NaN.  With
  * q_len * num_heads <= 128 the q_len query tokens of mla_decode_plan_multi
  * share one pass over their request's rows.
  */

@@ -493,6 +493,7 @@ DecodeArgs decode_args(mla_plan_t plan, const void* q_nope, const void* q_pe, co
   a.kv_scale = kv_scale;                  // the dequantisation scale of fp8 codes only
   a.units_cap = plan->units_cap;
   a.n_workers = plan->n_workers;
+  a.batch = plan->params.batch;
   return a;
 }
 
@@ -507,6 +508,7 @@ mla_status_t merge_shares(mla_plan_t plan, const DecodeArgs& a, bool out_f32, cu
   m.lse = a.lse;
   m.num_heads = plan->params.num_heads;
   m.merge_cap = plan->merge_cap;
+  m.batch = a.batch;
   const cudaError_t e = q4 ? launch_merge_shares(m, out_f32, plan->num_sms, s) : launch_merge(m, out_f32, s);
   return e == cudaSuccess ? MLA_OK : cuda_fail(plan, e, "merge kernel launch");
 }

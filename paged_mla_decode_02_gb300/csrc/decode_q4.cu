@@ -406,13 +406,16 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
   const int worker = blockIdx.x / groups, row0 = 64 * (blockIdx.x % groups);
   int u0 = a.worker_ptr[worker], u1 = a.worker_ptr[worker + 1];   // of a.n_workers + 1 entries
   const PlanDev prm = *a.params;
-  if (worker >= prm.n_workers) u0 = u1 = 0;
+  // A replay may meet another plan than its call did: one of other rows to a request is
+  // refused, and of a larger batch the requests behind the call's are neither read nor written.
+  if (worker >= prm.n_workers || prm.num_heads != H) u0 = u1 = 0;
   WorkUnit unit0{};
   if (u0 < u1) unit0 = a.units[u0];
   const int page_shift = 31 - __clz(prm.page_size);
 
   if (threadIdx.x < S::kNumBars) {
     if (threadIdx.x == 0) *abort_flag = 0;
+    if (threadIdx.x == 0 && blockIdx.x == 0 && prm.num_heads != H) report_error(a.err, kErrBounds);
     const int i = threadIdx.x;
     mbar_init(bar(i), i < S::kSFull0 || (i >= S::kRowsFree0 && i < S::kQReady) ? kTileWarps
                         : (i >= S::kSFree0 && i < S::kPReady0) || i == S::kQReady ? kSoftmaxWarps
@@ -483,10 +486,11 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           // batches of several units a worker), fewer come as fast by themselves, and their
           // tiles are found too quickly for a warp with more to do (2 us of 48).
           if (kRows == 64 && more && at.ui != ui) {
-            const size_t row = static_cast<size_t>(a.units[at.ui].req) * H + row0;
-            const int n = min(kRows, H - row0);
+            const int req = a.units[at.ui].req;
+            const size_t row = static_cast<size_t>(req) * H + row0;
+            const int n = req < a.batch ? min(kRows, H - row0) : 0;
             for (int i = lane; i < n; i += 32) bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q_nope) + (row + i) * kDCkv, 2 * kDCkv);
-            if (lane == 0) bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q_pe) + row * kDKpe, 2 * kDKpe * n);
+            if (lane == 0 && n > 0) bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q_pe) + row * kDKpe, 2 * kDKpe * n);
           }
         } else if (++behind == S::kGroups) {
           break;
@@ -711,6 +715,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
     // ---- the query of a unit, a few rows a warp, two at a time ----
     auto put_query = [&](int req, int parity) {
       constexpr int kOwn = kRows / kSoftmaxWarps;
+      const int rows = req < a.batch ? H : 0;
       float* out = reinterpret_cast<float*>(sm + S::kOffScale) + parity * kRows;
 #pragma unroll 1
       for (int k = 0; k < kOwn; k += 2) {
@@ -720,7 +725,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           const int r = row0 + warp * kOwn + k + i;
 #pragma unroll
           for (int j = 0; j < 9; ++j) w[i][j] = 0;
-          if (r < H) {
+          if (r < rows) {
             const size_t row = static_cast<size_t>(req) * H + r;
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_nope) + row * kDCkv + 16 * lane);
             const uint4 v0 = src[0], v1 = src[1];
@@ -977,6 +982,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
       // ---- epilogue: the sums over the unit's tokens of all lanes and quadrants; the second
       // ones are exchanged where these query rows had their P, which no MMA reads any more ----
       const bool split = u.out_slot >= 0;
+      const int rows = u.req < a.batch ? H : 0;   // that are written
 #pragma unroll
       for (int j = 0; j < kJ; ++j) ld[j] = lx[j] - ld[j];   // of what P stands for
       const float sx = warp_reduce<false>(lx), sr = warp_reduce<false>(ld);
@@ -1000,7 +1006,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         const float s = (*shared_sum(0, lane) + *shared_sum(1, lane)) + (*shared_sum(2, lane) + *shared_sum(3, lane));
         inverse = s == 0.f ? 0.f : 0x1p-6f / s;   // a row that saw no token: out 0
         const int h = row0 + kJ * cg + lane;
-        if (q == 0 && h < H) {
+        if (q == 0 && h < rows) {
           const float sum = (red[lane] + red[kJ + lane]) + (red[2 * kJ + lane] + red[3 * kJ + lane]);
           const float lse = (log2f(sum) - refs[lane]) * kLn2;
           if (split) a.lse_part[lse_part_offset(u.out_slot, 0, h, H)] = lse;
@@ -1034,11 +1040,11 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
         if (split) {
 #pragma unroll
           for (int j = 0; j < kJ; ++j)
-            if (h0 + j < H) a.o_part[part_offset(u.out_slot, h0 + j, d, H)] = x[j] * inv[j];
+            if (h0 + j < rows) a.o_part[part_offset(u.out_slot, h0 + j, d, H)] = x[j] * inv[j];
         } else if (kOutF32) {
 #pragma unroll
           for (int j = 0; j < kJ; ++j)
-            if (h0 + j < H) static_cast<float*>(a.out)[(row + j) * kDCkv + d] = x[j] * inv[j];
+            if (h0 + j < rows) static_cast<float*>(a.out)[(row + j) * kDCkv + d] = x[j] * inv[j];
         } else {
           // two lanes trade halves of two query rows: each stores two dims of one
 #pragma unroll
@@ -1048,7 +1054,7 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
             const float got = __shfl_xor_sync(~0u, odd ? x0 : x1, 1);
             const uint32_t w = odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got);
             const int h = j + (odd ? 1 : 0);
-            if (h0 + h < H)
+            if (h0 + h < rows)
               *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row + h) * kDCkv + (d & ~1)) = w;
           }
         }

@@ -30,6 +30,7 @@ struct DecodeArgs {
   float kv_scale;
   int units_cap;
   int n_workers;
+  int batch;                   // requests of the arrays, as planned when the call was made
 };
 
 // Element (slot, head h, dim d) of the fp32 partial outputs.  Dims are
@@ -58,6 +59,7 @@ struct MergeArgs {
   float* lse;
   int num_heads;
   int merge_cap;
+  int batch;
 };
 
 // Legacy warp-level tensor path (mma.sync m16n8k16): one CTA per (unit, 16-head group).

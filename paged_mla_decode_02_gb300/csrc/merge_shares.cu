@@ -33,7 +33,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) merge_shares_kernel(co
   __shared__ float4 s_sum[kThreads];
   __shared__ float2 s_mw[kThreads];
   // The plan's arrays were uploaded before the decode ahead began: read while it ends.
-  const int H = a.num_heads, n_merge = a.params->n_merge;
+  // (of a plan of other rows, as a replay may meet, the decode leaves nothing to merge)
+  const int H = a.num_heads, n_merge = a.params->num_heads == H ? a.params->n_merge : 0;
   // rows of a block: a power of two that leaves a group for every kAhead shares
   const int shares = n_merge > 0 ? (a.params->n_slots + n_merge - 1) / n_merge : 0;
   int rows = kThreads / 2;
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) merge_shares_kernel(co
         }
       __syncthreads();
     }
-    if (group == 0 && h < H) {
+    if (group == 0 && h < H && me.req < a.batch) {
       const float inv = W == 0.f ? 0.f : 1.f / W;
       const size_t at = (static_cast<size_t>(me.req) * H + h) * kDCkv + d;
       if (kOutF32)
