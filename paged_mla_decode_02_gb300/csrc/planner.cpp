@@ -274,11 +274,12 @@ void partition_batch_pair(const int32_t* kv_indptr, const int32_t* kv_len, int b
 }
 
 namespace {
-double q4_tile_us(int rows) { return rows <= 16 ? 1.9 : rows <= 32 ? 2.2 : 3.3; }
+double q4_tile_us(int rows) { return rows <= 16 ? 1.55 : rows <= 32 ? 1.9 : 2.5; }
+double q4_unit_us(int rows) { return rows <= 16 ? 3.2 : rows <= 32 ? 5.2 : 7.2; }
 }  // namespace
 
 PlanCosts q4_costs(int rows) {
-  const int unit = static_cast<int>(4 * 6.0 / q4_tile_us(rows));
+  const int unit = static_cast<int>(4 * q4_unit_us(rows) / q4_tile_us(rows) + 0.5);
   return PlanCosts{4, unit, 2, 1};
 }
 

@@ -82,14 +82,12 @@ void partition_batch_pair(const int32_t* kv_indptr, const int32_t* kv_len, int b
 
 // The 4-bit kernel's partition (128-token tiles, `rows` query rows per request),
 // chosen in the same way between splits where they even the workers out and
-// splits where a request must be cut.  A tile takes 1.9 us with up to 16 query
-// rows, 2.2 with 32 and 3.3 with more (of which a CTA takes 64), a unit 6 us
-// more (its query, the first rows, the sums and the output), so a short request
-// is worth cutting down to single tiles (4 requests of up to 2000 tokens, 16
-// heads: 28 us in pieces of four tiles or more, 19 with single ones), and 64
-// requests of 32 tiles and 128 rows are left whole on 128 of 152 CTAs (100.8 us
-// then; cut evenly 113).  With a unit at 4 us 128 ragged requests took 194.6 us,
-// 189 with 6.
+// splits where a request must be cut.  Batches of 1 to 64 tiles and of 1 to 4
+// units a worker give 1.55 us a tile and 3.2 a unit more (its query, the first
+// rows, the sums and the output) with up to 16 query rows, 1.9 and 5.2 with 32, 2.5
+// and 7.2 with more (of which a CTA takes 64).  A short request is worth cutting
+// down to single tiles, and 64 requests of 32 tiles and 128 rows are left whole on
+// 128 of 152 CTAs.
 PlanCosts q4_costs(int rows);
 double q4_step_estimate_us(const Partition& p, int rows);
 void partition_batch_q4(const int32_t* kv_indptr, const int32_t* kv_len, int batch, int n_workers,
