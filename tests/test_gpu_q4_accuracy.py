@@ -134,3 +134,48 @@ def test_weights_of_like_size(H, lens, spread):
     b.set_query(torch.from_numpy(q).to(torch.bfloat16))
     rel, lse = errors(b)
     assert rel <= (2.0 ** -9 if H > 32 else 2.0 ** -11) and lse <= 2.0 ** -12, (rel, lse)
+
+
+def many(b, B, rng):
+    """The batch's one request B times over, with other queries: as many as there are CTAs,
+    so that none is split and each unit has all its tiles."""
+    pages = len(b.ids)
+    b.lens = b.lens * B
+    b.indptr = (np.arange(B + 1) * pages).astype(np.int32)
+    b.ids = np.tile(b.ids, B)
+    q = f64(b.q).repeat(B, 0)
+    q[..., :512] = q[..., :512][rng.permutation(B)] * rng.choice([-1.0, 1.0], (B, 1, 1, 512))
+    b.set_query(torch.from_numpy(q).to(torch.bfloat16))
+    return b
+
+
+@pytest.mark.parametrize("H", [33, 64, 128])
+@pytest.mark.parametrize("gap", [5.0, 8.0, 10.0, 12.0])
+@pytest.mark.parametrize("at", [0, 127, 128, 500, 1299])
+def test_a_large_weight_in_units_of_many_tiles(H, gap, at):
+    """The token in each part of a unit.  Where it is not in the first tile, two tiles go
+    by until the other form is taken, with the largest weight at 2^11 and errors of a
+    root mean square of 2^-10 / sqrt(3) (a weight 2^-x of the largest: 2^(x - 21.8) of it)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n, B = 1300, sms if H <= 64 else sms // 2
+    rng = rng_of(78, H, int(gap), at)
+    b = many(sink_batch(rng, [n], H, 64, at, gap), B, rng)
+    dec = b.decoder()
+    assert dec.info()["num_partial_slots"] == 0
+    dec.close()
+    rel, lse = errors(b)
+    late = 2.0 ** (gap / math.log(2) - 21.8) * math.sqrt(256 / n) if at >= 128 else 0.0
+    assert rel <= 2.0 ** -8 + late and lse <= 2.0 ** -11, (rel, lse)
+
+
+@pytest.mark.parametrize("H", [64, 128])
+def test_units_that_take_either_form_in_turn(H):
+    """Several units to a CTA, with and without such a token: each starts anew."""
+    rng = rng_of(79, H)
+    B = 400 if H <= 64 else 200
+    b = many(sink_batch(rng, [400], H, 64, 70, 9.0), B, rng)
+    q = f64(b.q)
+    q[rng.permutation(B)[:B // 2], ..., 512] = 0
+    b.set_query(torch.from_numpy(q).to(torch.bfloat16))
+    rel, lse = errors(b)
+    assert rel <= 2.0 ** -8 and lse <= 2.0 ** -11, (rel, lse)
