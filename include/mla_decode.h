@@ -241,6 +241,20 @@ mla_status_t mla_decode_run(mla_plan_t plan, const void* q_nope, const void* q_p
  * (MLA_ERR_DEVICE_BOUNDS).  A row that held a NaN makes its request's results NaN.  With
  * q_len * num_heads <= 128 the q_len query tokens of mla_decode_plan_multi
  * share one pass over their request's rows.
+ * Numbers: the query is held in two e4m3 terms, exactly down to 2^-14 of its row's
+ * largest magnitude and within 2^-22 of that below; scores, softmax sums, lse and
+ * the values' sum are fp32.  A weight enters the values' sum in fewer bits, which
+ * an fp32 out shows, and only out:
+ *   up to 32 query rows (heads, or heads times query tokens, that share a pass)
+ *               to 2^-11 of itself or 2^-24 of the largest, whichever is more
+ *   more rows   to 2^-8 of itself or 2^-15 of the largest; where a row has only a
+ *               few large weights (as tokens that all attend to make them) to 2^-7
+ *               of itself or 2^-24 of the largest
+ * with 2^E of the tokens' rows (see the layout above) counted into both weights.
+ * Relative errors of an fp32 out in L2, 1300 tokens of random signs: 2e-4 and 1e-3
+ * where weights are alike; beside a token of value 0 that is 6, 10 and 12 natural
+ * units above the others 2e-4, 6e-4 and 3.5e-3 with up to 32 rows, 2e-3, 2e-3 and
+ * 4e-3 with more (1.2e-2 at 12 if it is not among the first tokens).
  */
 mla_status_t mla_decode_run_q4(mla_plan_t plan, const void* q_nope, const void* q_pe, int q_dtype,
                                const void* cache, int num_pages, void* out, int out_dtype,

@@ -36,9 +36,9 @@
 //   row has but a few large ones (a token that all attend to, whose own value may
 //   say nothing), the sum of many small ones may be the result: 64 rows with such a
 //   one among them take the second for the rest of the unit.  Off by 2^-8 or 2^-7 of
-//   a weight at most, 0.12 or 0.25 % of a result whose values add up like a random
-//   walk; with the first form alone 0.6 % where a token stands 6 natural units above
-//   the rest, 5 % at 9.
+//   a weight at most, 0.1 or 0.2 % of a result whose values add up like a random walk;
+//   with the first form alone 0.4 % where a token stands 6 natural units above the
+//   rest, 4 % at 9.
 //
 // The softmax's state is kept per query row: a reference that moves (and O with
 // it) when a score passes it by more than kSlack, and two sums in fp32 per
@@ -57,18 +57,19 @@
 // still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is recorded.
 //
 // What bounds it (device time from a graph, cold L2): the way of a tile through its
-// buffer, among 28 warps that take 52 % of the issue slots.
+// buffer, among 28 warps that take 54 to 56 % of the issue slots.
 // - 16 query rows: 4 requests of 131072 tokens take 60 us, 2.7 TB/s, 27 tiles a CTA at
-//   1.5 to 1.9 us each.  A buffer is held for the expansion (about 3700 cycles of a
+//   1.5 us each and a unit's start and end.  A buffer is held for the expansion (about 3700 cycles of a
 //   warp), the scores (1250), P (1700) and P . V (1700); shared memory has room for
 //   three.  Loads or stores left out gain 2 us, the arithmetic of P nothing.
-// - 64 rows: 64 requests of 4096 tokens and 128 heads take 93 us, 0.79 PFLOP/s, 2.6 us
-//   a tile.  Expansion 2250, scores 2000 (500 after it), P 3300 and P . V 2500 cycles,
-//   over two buffers.  Both products read the tile and their other operand through shared
+// - 64 rows: 64 requests of 4096 tokens and 128 heads take 94 us, 0.77 PFLOP/s, 2.5 us
+//   a tile.  Expansion 2250, scores 2000 (500 after it), P 3300 and P . V 2500 cycles
+//   (before lo had two forms), over two buffers.  Both products read the tile and their other operand through shared
 //   memory, 2700 cycles of 128 bytes a tile.  Of 105 us, all MMAs left out made 82, half
 //   of the expansion left out 95.
-// A unit costs 3.4 us (16 rows) to 5.7 us (64) beyond its tiles: its last P . V, the
-// sums, the output; the first one of a launch more, for its code is fetched then.
+// A unit costs 3.2 us (16 rows) to 7.2 us (64) beyond its tiles: its query and first rows,
+// its last P . V, the sums, the output; the first one of a launch more, for its code is
+// fetched then.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -130,9 +131,8 @@ struct Shape {
   static constexpr int kTokWarp = kT / kTileWarps;         // rows that a warp expands, of one page
   // The scores' MMAs follow the expansion in kStages steps of 4 / kStages panels.  With 64
   // rows they take 2000 cycles, of which three quarters lie beside the expansion then (96.4
-  // us for 100.8 at first, 64 requests of 4096 tokens and 128 heads; two steps 94.7 for
-  // 92.7 now).  Fewer rows have fewer to hide,
-  // and the loads, 64 bytes of a row at a time instead of 256, cost more (63.9 us for 60.2,
+  // us for 100.8, 64 requests of 4096 tokens and 128 heads; later two steps 94.7 where four
+  // made 92.7).  Fewer rows have fewer to hide, and the loads, 64 bytes of a row at a time instead of 256, cost more (63.9 us for 60.2,
   // 4 requests of 131072 tokens, 16 heads; 32 rows the same either way).
   static constexpr int kStages = kRows == 64 ? 4 : 1;
   // registers a thread at launch, then by role
