@@ -247,9 +247,10 @@ mla_status_t mla_decode_run(mla_plan_t plan, const void* q_nope, const void* q_p
  * an fp32 out shows, and only out:
  *   up to 32 query rows (heads, or heads times query tokens, that share a pass)
  *               to 2^-11 of itself or 2^-24 of the largest, whichever is more
- *   more rows   to 2^-8 of itself or 2^-15 of the largest; where a row has only a
- *               few large weights (as tokens that all attend to make them) to 2^-7
- *               of itself or 2^-24 of the largest
+ *   more rows   to 2^-8 of itself or 2^-15 of the largest; where some row has only
+ *               a few large weights, as tokens that all attend to make them (up to 16
+ *               of 128 within 2^6 of the largest), to 2^-7 of itself or 2^-24 of the
+ *               largest
  * with 2^E of the tokens' rows (see the layout above) counted into both weights.
  * Relative errors of an fp32 out in L2, 1300 tokens of random signs: 2e-4 and 1e-3
  * where weights are alike; beside a token of value 0 that is 6, 10 and 12 natural

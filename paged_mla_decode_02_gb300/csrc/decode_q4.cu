@@ -33,9 +33,9 @@
 //   lo, of p - hi, in one of two forms that a unit's scores choose: e4m3, eight bits
 //   of p from 2^12 down to 2^-3 and ever fewer below, or e5m2, seven bits from 2^15
 //   down to 2^-11.  The first suits weights of which some are of like size.  Where a
-//   row has but a few large ones (a token that all attend to, whose own value may
-//   say nothing), the sum of many small ones may be the result: 64 rows with such a
-//   one among them take the second for the rest of the unit.  Off by 2^-8 or 2^-7 of
+//   row has but a few large ones (tokens that all attend to, whose own values may say
+//   nothing), the sum of many small ones may be the result: 64 rows with such a one
+//   among them take the second for the rest of the unit.  Off by 2^-8 or 2^-7 of
 //   a weight at most, 0.1 or 0.2 % of a result whose values add up like a random walk;
 //   with the first form alone 0.4 % where a token stands 6 natural units above the
 //   rest, 4 % at 9.
@@ -59,14 +59,14 @@
 // What bounds it (device time from a graph, cold L2): the way of a tile through its
 // buffer, among 28 warps that take 54 to 56 % of the issue slots.
 // - 16 query rows: 4 requests of 131072 tokens take 60 us, 2.7 TB/s, 27 tiles a CTA at
-//   1.5 us each and a unit's start and end.  A buffer is held for the expansion (about 3700 cycles of a
-//   warp), the scores (1250), P (1700) and P . V (1700); shared memory has room for
-//   three.  Loads or stores left out gain 2 us, the arithmetic of P nothing.
-// - 64 rows: 64 requests of 4096 tokens and 128 heads take 94 us, 0.77 PFLOP/s, 2.5 us
+//   1.5 us each and a unit's start and end.  A buffer is held for the expansion (about
+//   3700 cycles of a warp), the scores (1250), P (1700) and P . V (1700); shared memory
+//   has room for three.  Loads or stores left out gain 2 us, the arithmetic of P nothing.
+// - 64 rows: 64 requests of 4096 tokens and 128 heads take 93 us, 0.79 PFLOP/s, 2.5 us
 //   a tile.  Expansion 2250, scores 2000 (500 after it), P 3300 and P . V 2500 cycles
-//   (before lo had two forms), over two buffers.  Both products read the tile and their other operand through shared
-//   memory, 2700 cycles of 128 bytes a tile.  Of 105 us, all MMAs left out made 82, half
-//   of the expansion left out 95.
+//   (before lo had two forms), over two buffers.  Both products read the tile and their
+//   other operand through shared memory, 2700 cycles of 128 bytes a tile.  Of 105 us, all
+//   MMAs left out made 82, half of the expansion left out 95.
 // A unit costs 3.2 us (16 rows) to 7.2 us (64) beyond its tiles: its query and first rows,
 // its last P . V, the sums, the output; the first one of a launch more, for its code is
 // fetched then.
@@ -132,8 +132,8 @@ struct Shape {
   // The scores' MMAs follow the expansion in kStages steps of 4 / kStages panels.  With 64
   // rows they take 2000 cycles, of which three quarters lie beside the expansion then (96.4
   // us for 100.8, 64 requests of 4096 tokens and 128 heads; later two steps 94.7 where four
-  // made 92.7).  Fewer rows have fewer to hide, and the loads, 64 bytes of a row at a time instead of 256, cost more (63.9 us for 60.2,
-  // 4 requests of 131072 tokens, 16 heads; 32 rows the same either way).
+  // made 92.7).  Fewer rows have fewer to hide, and the loads, 64 bytes of a row at a time
+  // instead of 256, cost more (63.9 us for 60.2, 4 requests of 131072 tokens, 16 heads; 32 rows the same either way).
   static constexpr int kStages = kRows == 64 ? 4 : 1;
   // registers a thread at launch, then by role
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;
@@ -148,6 +148,10 @@ struct Shape {
   // weights 2^-18 of it.  (A slack too small is paid for in moves, which cost a good part of a
   // tile's time.)
   static constexpr float kTopWide = 15.f, kSlackWide = 8.f, kFullWide = 0x1p-9f;
+  // That suits a row with no more large weights (2^-6 of the largest) in a tile than these:
+  // the others may be the result then.  Errors of e4m3's last unit, 2^-10 / sqrt(3) of up to
+  // 128 weights, are 0.3 % of 17 weights of 1/2, so with more of them it does as well.
+  static constexpr int kFewLarge = 16;
   // a row found to need it in the middle of a unit has two tiles to go until all rows take
   // it, and its largest p up here
   static constexpr float kSlackFew = 1.f;
@@ -191,11 +195,11 @@ struct Shape {
   static constexpr int kOffRed = kOffTable + 4 * 8;        // [softmax warps][kJ] floats
   static constexpr int kOffRows = kOffRed + kSoftmaxWarps * kJ * 4;   // [kRowsAhead][warps of a tile] packed rows
   static constexpr int kOffWide = kOffRows + kRowsAhead * kTileWarps * 8;   // [4] of 32 tokens: lo in e5m2
-  static constexpr int kOffFew = kOffWide + (kSide ? 0 : 16);   // [2][softmax warps] few_large, of a unit's first tile and of later ones
-  static constexpr int kOffForm = kOffFew + (kSide ? 0 : 2 * 4 * kSoftmaxWarps);   // [kRows / kJ] lo in e5m2 where a reference moves
+  static constexpr int kOffSmall = kOffWide + (kSide ? 0 : 16);   // [softmax warps] count_small
+  static constexpr int kOffForm = kOffSmall + (kSide ? 0 : 16 * kSoftmaxWarps);   // [kRows / kJ] lo in e5m2 where a reference moves
   static constexpr int kOffWant = kOffForm + (kSide ? 0 : 4 * (kRows / kJ));   // [2] by unit parity, the tile from which lo is e5m2
   static constexpr int kOffBar = kOffWant + (kSide ? 0 : 8);
-  static_assert(kOffFew % 16 == 0, "read as uint4");
+  static_assert(kOffSmall % 16 == 0, "read as uint4");
   static_assert(kOffP % 1024 == 0 && kOffK % 1024 == 0 && kOffKPe % 1024 == 0, "swizzle atoms");
 };
 
@@ -349,21 +353,27 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// A bit for each of N rows that has next to none of its weights p = 2^z in this
-// warp's `valid` tokens (the first ones) at 1/2 or above: one, or two of 32.
-template <int N>
-__device__ __forceinline__ uint32_t few_large(const float (&z)[N], int valid) {
-  const uint32_t small = valid == 32 ? 30 : valid > 0 ? 31 : 32;   // -inf behind the last token
-  uint32_t rows = 0;
+// How many of a warp's tokens have a weight p = 2^z below 1/2 (those that a row does
+// not see among them): of 16 rows, a byte each, row j in byte j % 4 of word j / 4.
+__device__ __forceinline__ uint4 count_small(const float (&z)[16]) {
+  uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < N; j += 4) {
-    // the signs of four rows' z + 1, a byte each, summed over the lanes
-    auto bits = [&](int i) { return __float_as_uint(z[j + i] + 1.f); };
+  for (int j = 0; j < 4; ++j) {
+    // the signs of four rows' z + 1, summed over the lanes
+    auto bits = [&](int i) { return __float_as_uint(z[4 * j + i] + 1.f); };
     const uint32_t signs = __byte_perm(__byte_perm(bits(0), bits(1), 0x0073), __byte_perm(bits(2), bits(3), 0x0073), 0x5410);
-    const uint32_t enough = (__reduce_add_sync(~0u, (signs >> 7) & 0x01010101u) + (128 - small) * 0x01010101u) >> 7;
-    rows |= ((enough & 1) | (enough >> 7 & 2) | (enough >> 14 & 4) | (enough >> 21 & 8)) << j;
+    w[j] = __reduce_add_sync(~0u, (signs >> 7) & 0x01010101u);
   }
-  return rows;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// A bit for each row with no more than `most` (up to 127) of its 128 tokens' weights at
+// 1/2 or above, from the sums of its four warps' counts.
+__device__ __forceinline__ uint32_t few_large(const uint4& small, uint32_t most) {
+  auto four = [&](uint32_t w) {
+    const uint32_t enough = ((w + most * 0x01010101u) >> 7) & 0x01010101u;   // 128 - most at least
+    return (enough | enough >> 7 | enough >> 14 | enough >> 21) & 15u;
+  };
+  return four(small.x) | four(small.y) << 4 | four(small.z) << 8 | four(small.w) << 12;
 }
 
 // Where the walk over a worker's tiles stands.
@@ -855,21 +865,18 @@ __global__ void __launch_bounds__(Shape<kRows>::kThreads, 1) decode_q4_kernel(co
           for (int j = 0; j < kJ; ++j)
             if (rows >> j & 1) z[j] -= __shfl_sync(~0u, up, j);
           if (!S::kSide && !wide) {
-            // rows with few large weights in all four warps' tokens; in a unit's first tile, where
-            // all rows' warps are here, of any of them (each reads the others' words then, which
-            // a later tile's must not replace)
-            uint32_t* few = reinterpret_cast<uint32_t*>(sm + S::kOffFew) + (first ? 0 : kSoftmaxWarps);
-            const uint32_t mine = few_large(z, min(max(u.tok_end - t0 - 32 * q, 0), 32));
-            const uint32_t blind = __ballot_sync(~0u, m == -INFINITY);   // not one that sees no token
-            if (lane == 0) few[warp] = mine & ~blind;
-            if (first) named_bar_sync(5, 32 * kSoftmaxWarps);
-            else named_bar_sync(1 + cg, 128);
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < kSoftmaxWarps / 4; ++i) {
-              const uint4 f = reinterpret_cast<const uint4*>(few)[i];
-              any |= (first || i == cg) && (f.x & f.y & f.z & f.w) != 0;
+            uint4* small = reinterpret_cast<uint4*>(sm + S::kOffSmall) + 4 * cg;
+            if constexpr (kJ == 16) {
+              const uint4 mine = count_small(z);
+              if (lane == 0) small[q] = mine;
             }
+            named_bar_sync(1 + cg, 128);
+            const uint4 s0 = small[0], s1 = small[1], s2 = small[2], s3 = small[3];   // bytes: up to 128 in all
+            const uint32_t few = few_large(make_uint4(s0.x + s1.x + s2.x + s3.x, s0.y + s1.y + s2.y + s3.y, s0.z + s1.z + s2.z + s3.z,
+                                                      s0.w + s1.w + s2.w + s3.w), S::kFewLarge);
+            // (not a row that sees no token); in a unit's first tile all rows' warps are here
+            bool any = (few & ~__ballot_sync(~0u, m == -INFINITY) & kAll) != 0;
+            if (first) any = bar_any(5, 32 * kSoftmaxWarps, any);
             float further = 0.f;   // how much higher the largest p becomes
             if (first) {
               wide = any;

@@ -10,10 +10,10 @@
 //
 // Measured from a graph, cold L2: 131000 fp32 rows written in 55.5 us, 6.2 TB/s,
 // 91 % of the copy rate; 100000 4-bit rows read to bf16 in 27.0 us, 5.4 TB/s, to fp16 in
-// 28.2 and to fp32 in 63.8, 4.1 TB/s;
-// as many rows of a bf16 cache to bf16 in 36.8 us, 6.3 TB/s; 92000 e4m3 rows to fp16 in
-// 26.9 us, 5.9 TB/s.  8190 rows written take 9.0 us and 64 take 6.7, 1600 read 8.6: the launch and a chain of dependent reads (slots, or offsets,
-// page list and page, then the row).
+// 28.2 and to fp32 in 63.8, 4.1 TB/s; as many rows of a bf16 cache to bf16 in 36.8 us,
+// 6.3 TB/s; 92000 e4m3 rows to fp16 in 26.9 us, 5.9 TB/s.  8190 rows written take 9.0 us
+// and 64 take 6.7, 1600 read 8.6: the launch and a chain of dependent reads (slots, or
+// offsets, page list and page, then the row).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>

@@ -136,6 +136,43 @@ def test_weights_of_like_size(H, lens, spread):
     assert rel <= (2.0 ** -9 if H > 32 else 2.0 ** -11) and lse <= 2.0 ** -12, (rel, lse)
 
 
+def sinks_batch(rng, n, H, where, gap, more=()):
+    """A request whose tokens `where` are `gap` natural units above the others, with ckv 0."""
+    b = sink_batch(rng, [n, *more], H, 64, 0, gap)
+    values = grid_rows(rng, b.pages * 64)
+    for r, length in enumerate(b.lens):
+        for t in where:
+            if t < length:
+                slot = int(b.ids[b.indptr[r] + t // 64]) * 64 + t % 64
+                values[slot, :512] = 0
+                values[slot, 512] = 4.0
+    b.set_rows(values)
+    return b
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("where", [range(2), range(4), range(16), range(0, 128, 10), (0, 31, 32, 63, 64, 95, 96, 127)])
+def test_several_large_weights(H, where):
+    """A few such tokens, adjacent or spread over a tile."""
+    rel, lse = errors(sinks_batch(rng_of(80, H, len(where)), 1500, H, where, 9.0, (128, 140, 40)))
+    assert rel <= bound(H, 13) and lse <= 2.0 ** -11, (rel, lse)
+
+
+@pytest.mark.parametrize("H", [64, 128])
+@pytest.mark.parametrize("at", [0, 500])
+def test_either_form_repeats_bit_for_bit(H, at):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rng = rng_of(81, H, at)
+    b = many(sink_batch(rng, [1300], H, 64, at, 9.0), sms if H <= 64 else sms // 2, rng)
+    dec = b.decoder()
+    first = dec.run_q4(b.q_nope, b.q_pe, b.cache, out_dtype=torch.float32)
+    for _ in range(20):
+        again = dec.run_q4(b.q_nope, b.q_pe, b.cache, out_dtype=torch.float32)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    dec.check_status()
+    dec.close()
+
+
 def many(b, B, rng):
     """The batch's one request B times over, with other queries: as many as there are CTAs,
     so that none is split and each unit has all its tiles."""
