@@ -57,7 +57,7 @@
 // still come; the results are void and MLA_ERR_DEVICE_TIMEOUT is recorded.
 //
 // What bounds it (device time from a graph, cold L2): the way of a tile through its
-// buffer, among 28 warps that take 54 to 56 % of the issue slots.
+// buffer, among 28 warps that take 54 to 57 % of the issue slots.
 // - 16 query rows: 4 requests of 131072 tokens take 60 us, 2.7 TB/s, 27 tiles a CTA at
 //   1.5 us each and a unit's start and end.  A buffer is held for the expansion (about
 //   3700 cycles of a warp), the scores (1250), P (1700) and P . V (1700); shared memory
@@ -133,7 +133,8 @@ struct Shape {
   // rows they take 2000 cycles, of which three quarters lie beside the expansion then (96.4
   // us for 100.8, 64 requests of 4096 tokens and 128 heads; later two steps 94.7 where four
   // made 92.7).  Fewer rows have fewer to hide, and the loads, 64 bytes of a row at a time
-  // instead of 256, cost more (63.9 us for 60.2, 4 requests of 131072 tokens, 16 heads; 32 rows the same either way).
+  // instead of 256, cost more (63.9 us for 60.2, 4 requests of 131072 tokens, 16 heads; 32
+  // rows the same either way).
   static constexpr int kStages = kRows == 64 ? 4 : 1;
   // registers a thread at launch, then by role
   static constexpr int kRegs = 65536 / kThreads / 8 * 8;
