@@ -256,6 +256,8 @@ mla_status_t mla_decode_run(mla_plan_t plan, const void* q_nope, const void* q_p
  * where weights are alike; beside a token of value 0 that is 6, 10 and 12 natural
  * units above the others 2e-4, 6e-4 and 3.5e-3 with up to 32 rows, 2e-3, 2e-3 and
  * 4e-3 with more (1.2e-2 at 12 if it is not among the first tokens).
+ * Time: a quarter of a bf16 cache's bytes, so faster where those are the bound (up
+ * to 32 query rows); with 128 a little slower than mla_decode_run over bf16.
  */
 mla_status_t mla_decode_run_q4(mla_plan_t plan, const void* q_nope, const void* q_pe, int q_dtype,
                                const void* cache, int num_pages, void* out, int out_dtype,
